@@ -247,6 +247,119 @@ sk_status sk_addmm(sk_dtype dtype, const void* bias, const void* A, const void* 
 sk_status sk_gemm_bf16_backward(const void* dC, const void* A, const void* B, void* dA, void* dB, void* dbias,
                                 int64_t M, int64_t N, int64_t K, int grid_cap, void* stream);
 
+/* ---- E4M3 with an fp32 scale for each block of 128, and the norms around it.
+ *
+ * The calls of this section that use no scratch of the library (the quantiser, the product,
+ * the norms' forward) may be captured into a HIP graph; the two backward calls use it and
+ * refuse a capturing stream (SK_ERR_UNSUPPORTED) like the Stream-K calls. */
+
+/* Element types of the quantiser's input and of the norms. */
+typedef enum sk_elem { SK_ELEM_BF16 = 0, SK_ELEM_F32 = 1 } sk_elem;
+/* What shares a scale: 128 consecutive elements of a row, or 128 rows of them. */
+typedef enum sk_block { SK_BLOCK_ROW = 0, SK_BLOCK_TILE = 1 } sk_block;
+
+/* E4M3 codes and scales of x [R][C] and / or of its transpose, in one pass over x:
+ *     s = max(fl(max|x| / 448), 2^-126) over each block,   code = E4M3 nearest to x / s
+ * (the exact quotient, ties to even; a block that holds an infinity or a NaN has a NaN scale
+ * and NaN codes).  Blocks start at multiples of 128 and end at the matrix's edge.
+ *   q        uint8 [R][Cp], Cp = C rounded up to 16 (codes past C are 0)
+ *   scale    float [ceil(C/128)][R] (SK_BLOCK_ROW) or [ceil(R/128)][ceil(C/128)] (SK_BLOCK_TILE)
+ *   qt       uint8 [C][Rp]: the codes of x^T, likewise, with blocks along R
+ *   scale_t  float [ceil(R/128)][C] or [ceil(C/128)][ceil(R/128)]
+ * q with scale, or qt with scale_t, may be NULL.  x is aligned to its elements, q and qt to 16
+ * bytes, scales to 4.  SK_ERR_ARG: a bad pointer set, R or C < 1, R or C >= 2^31 - 2^20, 2^31 or
+ * more blocks of 128 x 128, an output that overlaps x or another output. */
+sk_status sk_quantize_fp8_block(const void* x, sk_elem elem, sk_block block, void* q, float* scale, void* qt,
+                                float* scale_t, int64_t R, int64_t C, void* stream);
+
+/* C[m][n] = bf16( sum_b A_scale[b][m] B_scale(b, n) sum_{k in b} A[m][k] B[n][k] + bias[n] ),
+ * blocks of 128 along K, operands and scales as the quantiser writes them: A uint8 [M][K] with
+ * A_scale [ceil(K/128)][M]; B uint8 [N][K] with B_scale [ceil(K/128)][N] (b_block SK_BLOCK_ROW) or
+ * [ceil(N/128)][ceil(K/128)] (SK_BLOCK_TILE).  K is a multiple of 16 (the codes' row length).  bias
+ * bf16 [N] or NULL.  Each block's inner product is one matrix instruction's, the scaled blocks are
+ * added in fp32 in the order of K (or, for few rows and small tiles, in several fixed
+ * interleaved runs that are then added in order), and one rounding to bf16 ends it.  The
+ * product of the two scales is formed in fp32.  grid_cap > 0 holds the tiled kernels to that many
+ * workgroups.  SK_ERR_ALIGN: K not a multiple of 16, A, B or C not 16-byte aligned, scales not
+ * 4, bias not 2.  Sizes and overlap as for sk_gemm_fp8. */
+sk_status sk_gemm_fp8_block(const void* A, const void* B, const float* A_scale, const float* B_scale, sk_block b_block,
+                            const void* bias, void* C, int64_t M, int64_t N, int64_t K, int grid_cap, void* stream);
+
+/* Gradients of that product, C = A . B^T + bias with A [M][K] in blocks of a row and B [N][K] in
+ * tiles, given dC bf16 [M][N] and the transposed operands as the quantiser writes them:
+ *   At [K][Mp] with At_scale [ceil(M/128)][K] (SK_BLOCK_ROW), Bt [K][Np] with Bt_scale
+ *   [ceil(K/128)][ceil(N/128)] (SK_BLOCK_TILE), Mp, Np = M, N rounded up to 16:
+ *     dA[m][k] = bf16( sum_n q(dC)[m][n] B[n][k] ),   dB[n][k] = bf16( sum_m q(dC^T)[n][m] A[m][k] ),
+ *     dbias[n] = bf16( sum_m dC[m][n] )
+ * where q() quantises dC in blocks of 128 along the dimension summed over (one pass writes both
+ * forms, and the column sums, to the library's scratch).  Any output may be NULL (at least one is
+ * required); At is needed for dB, Bt for dA.  M, N and K need no alignment.  Repeats bit for bit. */
+sk_status sk_gemm_fp8_block_backward(const void* dC, const void* At, const float* At_scale, const void* Bt,
+                                     const float* Bt_scale, void* dA, void* dB, void* dbias, int64_t M, int64_t N,
+                                     int64_t K, int grid_cap, void* stream);
+
+/* Root-mean-square norms after and before a block, of T tokens of D elements:
+ *   with h:            out = residual_scale * residual + gate * (h rstd weight)
+ *   with next_weight:  y = v rstd_next next_weight, v = out as stored (or residual, without h)
+ *   rstd = (mean of squares + eps)^-1/2
+ * gate [gates][D] (gates divides T; token t takes row t / (T / gates)) or NULL, residual_scale [D] or
+ * NULL.  y is stored as it is (y), or as E4M3 codes q uint8 [T][Dp], Dp = D rounded up to 16, with
+ * scale float [ceil(D/128)][T].  Statistics are fp32, and so is what is quantised.  Row pointers
+ * need only their elements' alignment, q 16 bytes.  SK_ERR_ARG: a required pointer is NULL,
+ * both or neither of y and q with next_weight, T, D < 1, D > 32768, T >= 2^31 - 2^20, gates not a divisor of T, an
+ * output that overlaps an input or another output (out may be residual or h itself). */
+typedef struct sk_norm_args {
+  int32_t elem;               /* sk_elem of every tensor but the statistics and codes */
+  float eps;
+  const void* h;              /* NULL: only the norm before a block, of residual */
+  const void* residual;
+  const void* weight;         /* with h */
+  const void* gate;
+  const void* residual_scale;
+  const void* next_weight;    /* NULL: only the norm after a block */
+  void* out;                  /* with h */
+  float* rstd;                /* [T], with h */
+  void* y;
+  void* q;
+  float* scale;
+  float* rstd_next;           /* [T], with next_weight */
+  int64_t T, D, gates;
+  void* stream;
+} sk_norm_args;
+
+sk_status sk_norm_forward(const sk_norm_args* args);
+
+/* Their gradients, all sums in fp32 in a fixed order (repeats bit for bit).  dout is the gradient at
+ * out (without h: an additional gradient at x, or NULL), dy that at y; v as above is passed as
+ * `out`.  Outputs: dx (the gradient at h, or at x without h) [T][D]; with h also dresidual [T][D],
+ * dweight [D], dgate [gates][D] with a gate, dresidual_scale [D] with a residual scale (which
+ * needs residual); dnext_weight [D] with dy. */
+typedef struct sk_norm_grad_args {
+  int32_t elem;
+  int32_t reserved;
+  const void* dout;
+  const void* dy;             /* NULL: no norm before the next block; else out, next_weight, rstd_next too */
+  const void* out;
+  const void* next_weight;
+  const float* rstd_next;
+  const void* h;              /* NULL: only the norm before a block */
+  const void* residual;
+  const void* weight;
+  const void* gate;
+  const void* residual_scale;
+  const float* rstd;
+  void* dx;
+  void* dresidual;
+  void* dweight;
+  void* dgate;
+  void* dresidual_scale;
+  void* dnext_weight;
+  int64_t T, D, gates;
+  void* stream;
+} sk_norm_grad_args;
+
+sk_status sk_norm_backward(const sk_norm_grad_args* args);
+
 /* Full-control entry point: the same kernels with a chosen policy and tile, plus test hooks.
  * Zero-initialise and fill the fields you need.  The policies are the Stream-K
  * partition of the MAC-iteration space ("Stream-k mxfp4 kernel", description)

@@ -9,7 +9,9 @@ and streams only.
 
 Entry points mirror ``include/sk_gemm.h``:
 ``gemm_mxfp4``, ``gemm_mxfp8``, ``gemm_bf16``, ``gemm_fp8``, ``addmm`` and ``gemm_ex`` (policy,
-tile and test hooks), plus ``plan``, ``plan_wg_range``, ``check``,
+tile and test hooks); ``quantize_fp8_block``, ``gemm_fp8_block`` and ``gemm_fp8_block_backward``
+(E4M3 with an fp32 scale for each block of 128); ``rms_norm`` and ``gated_norm`` with
+``rms_norm_backward`` and ``gated_norm_backward`` (the norms before and after a block); plus ``plan``, ``plan_wg_range``, ``check``,
 ``release_workspace``, ``poison_workspace``, ``variants`` and the CU-masked
 streams ``cu_masked_stream`` / ``destroy_stream`` / ``stream_cu_count``.
 """
@@ -25,6 +27,8 @@ __all__ = [
     "library_path", "load", "gemm_mxfp4", "gemm_mxfp4_noalloc", "gemm_mxfp8", "gemm_bf16", "gemm_bf16_backward", "gemm_mx", "gemm_fp8", "addmm", "gemm_ex", "plan", "plan_wg_range",
     "plan_wg_work", "check", "release_workspace", "poison_workspace", "variants", "Plan",
     "cu_masked_stream", "destroy_stream", "stream_cu_count", "phase_summary",
+    "quantize_fp8_block", "gemm_fp8_block", "gemm_fp8_block_backward",
+    "rms_norm", "gated_norm", "rms_norm_backward", "gated_norm_backward",
 ]
 
 MXFP4, BF16, FP8, MXFP8 = 0, 1, 2, 3
@@ -90,6 +94,19 @@ class _WorkItem(ctypes.Structure):
                 ("mode", ctypes.c_int32), ("first", ctypes.c_int32)]
 
 
+class _NormArgs(ctypes.Structure):
+    _fields_ = [("elem", ctypes.c_int32), ("eps", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in (
+        "h", "residual", "weight", "gate", "residual_scale", "next_weight", "out", "rstd", "y", "q", "scale",
+        "rstd_next")] + [(n, ctypes.c_int64) for n in ("T", "D", "gates")] + [("stream", ctypes.c_void_p)]
+
+
+class _NormGradArgs(ctypes.Structure):
+    _fields_ = [("elem", ctypes.c_int32), ("reserved", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "dout", "dy", "out", "next_weight", "rstd_next", "h", "residual", "weight", "gate", "residual_scale", "rstd",
+        "dx", "dresidual", "dweight", "dgate", "dresidual_scale", "dnext_weight")] + [
+            (n, ctypes.c_int64) for n in ("T", "D", "gates")] + [("stream", ctypes.c_void_p)]
+
+
 @dataclass(frozen=True)
 class Plan:
     tile_m: int
@@ -137,6 +154,11 @@ def load():
     lib.sk_gemm_bf16_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
     lib.sk_gemm_mx.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
     lib.sk_addmm.argtypes = [i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
+    lib.sk_quantize_fp8_block.argtypes = [vp, i32, i32, vp, vp, vp, vp, i64, i64, vp]
+    lib.sk_gemm_fp8_block.argtypes = [vp, vp, vp, vp, i32, vp, vp, i64, i64, i64, i32, vp]
+    lib.sk_gemm_fp8_block_backward.argtypes = [vp] * 8 + [i64, i64, i64, i32, vp]
+    lib.sk_norm_forward.argtypes = [ctypes.POINTER(_NormArgs)]
+    lib.sk_norm_backward.argtypes = [ctypes.POINTER(_NormGradArgs)]
     lib.sk_gemm_ex.argtypes = [ctypes.POINTER(_Args)]
     lib.sk_plan.argtypes = [ctypes.POINTER(_PlanQuery), ctypes.POINTER(_PlanInfo)]
     lib.sk_plan_wg_range.argtypes = [ctypes.POINTER(_PlanInfo), ctypes.c_int32,
@@ -157,6 +179,7 @@ def load():
     lib.sk_status_string.argtypes = [ctypes.c_int]
     lib.sk_status_string.restype = ctypes.c_char_p
     for name in ("sk_gemm_mxfp4", "sk_gemm_mxfp4_noalloc", "sk_gemm_mxfp8", "sk_gemm_bf16", "sk_gemm_bf16_backward", "sk_gemm_mx", "sk_gemm_fp8", "sk_addmm", "sk_gemm_ex", "sk_plan",
+                 "sk_quantize_fp8_block", "sk_gemm_fp8_block", "sk_gemm_fp8_block_backward", "sk_norm_forward", "sk_norm_backward",
                  "sk_plan_wg_range", "sk_plan_wg_work", "sk_check", "sk_debug_poison_workspace", "sk_variant_info",
                  "sk_variant_k_split", "sk_stream_create_cu_masked", "sk_stream_destroy", "sk_stream_cu_count"):
         getattr(lib, name).restype = ctypes.c_int
@@ -411,6 +434,267 @@ def gemm_ex(dtype, A, B, A_scale=None, B_scale=None, bias=None, C=None, *, grid_
         a.trace = trace.data_ptr()
     _ok(load().sk_gemm_ex(ctypes.byref(a)), "sk_gemm_ex")
     return C
+
+
+# ---------------------------------------------------------------- E4M3 with a scale for each block of 128
+
+_BLOCKS = {"row": 0, "tile": 1}
+
+
+def _elem(t, name):
+    """SK_ELEM_* of a tensor."""
+    torch = _torch()
+    try:
+        e = {torch.bfloat16: 0, torch.float32: 1}.get(t.dtype)
+    except AttributeError:
+        raise TypeError(f"{name} must be a tensor") from None
+    if e is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected bfloat16 or float32")
+    return e
+
+
+def _up16(n):
+    return (n + 15) & ~15
+
+
+def _blocks(n):
+    return (n + 127) >> 7
+
+
+def quantize_fp8_block(x, block="row", *, transpose=False, stream=None):
+    """E4M3 codes of x [R, C] (bf16 or fp32) with an fp32 scale for each block, codes times scale
+    approximating x: s = max(max|x| / 448, 2^-126), code = the E4M3 value nearest to x / s, ties to even.
+
+    block "row": 128 consecutive elements of a row share a scale; returns (q, scale) with q
+    float8_e4m3fn [R, C rounded up to 16] (zeros past C) and scale [ceil(C/128), R].  block "tile":
+    128 x 128 elements do; scale [ceil(R/128), ceil(C/128)].  transpose=True gives the same of x^T (blocks
+    along R) instead, transpose="both" gives (q, scale, qt, scale_t) from one pass over x."""
+    torch = _torch()
+    e = _elem(x, "x")
+    if block not in _BLOCKS:
+        raise ValueError(f"block must be 'row' or 'tile', not {block!r}")
+    if transpose not in (False, True, "both"):
+        raise ValueError(f"transpose must be False, True or 'both', not {transpose!r}")
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected two dimensions")
+    R, C = x.shape
+    dev = x.device
+    _need(x, "x", (x.dtype,), (R, C), dev)
+    tile = block == "tile"
+    q = s = qt = st = None
+    if transpose is not True:
+        q = torch.empty((R, _up16(C)), dtype=torch.float8_e4m3fn, device=dev)
+        s = torch.empty((_blocks(R) if tile else _blocks(C), _blocks(C) if tile else R), dtype=torch.float32, device=dev)
+    if transpose:
+        qt = torch.empty((C, _up16(R)), dtype=torch.float8_e4m3fn, device=dev)
+        st = torch.empty((_blocks(C) if tile else _blocks(R), _blocks(R) if tile else C), dtype=torch.float32, device=dev)
+    _ok(load().sk_quantize_fp8_block(_ptr(x), e, _BLOCKS[block], _ptr(q), _ptr(s), _ptr(qt), _ptr(st), R, C,
+                                     _stream(x, stream)), "sk_quantize_fp8_block")
+    if transpose == "both":
+        return q, s, qt, st
+    return (qt, st) if transpose else (q, s)
+
+
+def gemm_fp8_block(A, B, A_scale, B_scale, bias=None, C=None, grid_cap=0, stream=None):
+    """C = A . B^T (+ bias) of E4M3 operands with an fp32 scale for each block of 128 along K; returns C
+    (bf16 [M, N]).  Operands as quantize_fp8_block gives them: A [M, K] with A_scale [ceil(K/128), M],
+    B [N, K] with B_scale [ceil(K/128), N] (block "row") or [ceil(N/128), ceil(K/128)] (block "tile")."""
+    torch = _torch()
+    M, K = A.shape
+    N = B.shape[0]
+    dev = A.device
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    _need(A, "A", codes, (M, K), dev)
+    _need(B, "B", codes, (N, K), dev)
+    kb = _blocks(K)
+    _need(A_scale, "A_scale", (torch.float32,), (kb, M), dev)
+    tile = B_scale.shape == (_blocks(N), kb)
+    _need(B_scale, "B_scale", (torch.float32,), (_blocks(N), kb) if tile else (kb, N), dev)
+    if bias is not None:
+        _need(bias, "bias", (torch.bfloat16, torch.int16, torch.uint16), (N,), dev)
+    C = _out(C, M, N, dev)
+    _ok(load().sk_gemm_fp8_block(A.data_ptr(), B.data_ptr(), A_scale.data_ptr(), B_scale.data_ptr(), 1 if tile else 0,
+                                 _ptr(bias), C.data_ptr(), M, N, K, int(grid_cap), _stream(A, stream)),
+        "sk_gemm_fp8_block")
+    return C
+
+
+def gemm_fp8_block_backward(dC, At=None, At_scale=None, Bt=None, Bt_scale=None, *, need_dA=True, need_dB=True,
+                            need_dbias=True, grid_cap=0, stream=None):
+    """Gradients of C = A . B^T + bias for block-scaled E4M3: returns (dA, dB, dbias), bf16, None where not
+    asked for.
+
+    dC is bf16 [M, N] (quantised inside, along N for dA and along M for dB).  At [K, M rounded up to 16] with
+    At_scale [ceil(M/128), K] is A's transposed form from quantize_fp8_block(a, "row", transpose=...),
+    needed for dB; Bt [K, N rounded up to 16] with Bt_scale [ceil(K/128), ceil(N/128)] is B's from
+    quantize_fp8_block(b, "tile", transpose=...), needed for dA."""
+    torch = _torch()
+    if dC.dim() != 2:
+        raise ValueError(f"dC has shape {tuple(dC.shape)}, expected two dimensions")
+    M, N = dC.shape
+    dev = dC.device
+    _need(dC, "dC", (torch.bfloat16,), (M, N), dev)
+    ref = Bt if need_dA else At
+    if ref is None:
+        if need_dA or need_dB:
+            raise ValueError("Bt is needed for dA, At for dB")
+        K = 1
+    else:
+        K = ref.shape[0]
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    dA = dB = db = None
+    if need_dA:
+        _need(Bt, "Bt", codes, (K, _up16(N)), dev)
+        _need(Bt_scale, "Bt_scale", (torch.float32,), (_blocks(K), _blocks(N)), dev)
+        dA = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if need_dB:
+        _need(At, "At", codes, (K, _up16(M)), dev)
+        _need(At_scale, "At_scale", (torch.float32,), (_blocks(M), K), dev)
+        dB = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+    if need_dbias:
+        db = torch.empty((N,), dtype=torch.bfloat16, device=dev)
+    _ok(load().sk_gemm_fp8_block_backward(_ptr(dC), _ptr(At) if need_dB else None, _ptr(At_scale) if need_dB else None,
+                                          _ptr(Bt) if need_dA else None, _ptr(Bt_scale) if need_dA else None, _ptr(dA),
+                                          _ptr(dB), _ptr(db), M, N, K, int(grid_cap), _stream(dC, stream)),
+        "sk_gemm_fp8_block_backward")
+    return dA, dB, db
+
+
+# ---------------------------------------------------------------- norms around a block
+
+def _norm_shape(x, name):
+    e = _elem(x, name)
+    if x.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected two dimensions")
+    return e, x.shape[0], x.shape[1], x.device, (x.dtype,)
+
+
+def _gates(gate, T, D, types, dev):
+    """Rows of a gate: [G, D] (or [D], one row), G a divisor of T."""
+    if gate.dim() == 1:
+        _need(gate, "gate", types, (D,), dev)
+        return 1
+    G = gate.shape[0]
+    _need(gate, "gate", types, (G, D), dev)
+    if G < 1 or T % G:
+        raise ValueError(f"gate has {G} rows, which do not divide {T} tokens")
+    return G
+
+
+def _norm_outputs(a, like, next_weight, quantize, T, D, types, dev):
+    """Allocates the outputs of the norm before a block; returns them in order."""
+    torch = _torch()
+    _need(next_weight, "weight" if a.h is None else "next_weight", types, (D,), dev)
+    a.next_weight = next_weight.data_ptr()
+    rstd = torch.empty((T,), dtype=torch.float32, device=dev)
+    a.rstd_next = rstd.data_ptr()
+    if not quantize:
+        y = torch.empty_like(like)
+        a.y = y.data_ptr()
+        return y, rstd
+    q = torch.empty((T, _up16(D)), dtype=torch.float8_e4m3fn, device=dev)
+    s = torch.empty((_blocks(D), T), dtype=torch.float32, device=dev)
+    a.q, a.scale = q.data_ptr(), s.data_ptr()
+    return q, s, rstd
+
+
+def rms_norm(x, weight, eps=1e-6, *, quantize=False, stream=None):
+    """The norm before a block: y = x rstd weight, rstd = (mean of x^2 over a row + eps)^-1/2, for x [T, D]
+    (bf16 or fp32; weight [D] of the same type).  Returns (y, rstd), or with quantize=True
+    (q, scale, rstd): y as E4M3 codes [T, D rounded up to 16] with scales [ceil(D/128), T], as
+    quantize_fp8_block(y, "row") of the fp32 y would give them, ready to be gemm_fp8_block's A."""
+    e, T, D, dev, types = _norm_shape(x, "x")
+    _need(x, "x", types, (T, D), dev)
+    a = _NormArgs(elem=e, eps=eps, residual=x.data_ptr(), T=T, D=D, stream=_stream(x, stream))
+    got = _norm_outputs(a, x, weight, quantize, T, D, types, dev)
+    _ok(load().sk_norm_forward(ctypes.byref(a)), "sk_norm_forward")
+    return got
+
+
+def gated_norm(h, residual, weight, gate=None, residual_scale=None, eps=1e-6, *, next_weight=None, quantize=False,
+               stream=None):
+    """The norm after a block, with its residual: out = residual_scale * residual + gate * (h rstd weight), for
+    h and residual [T, D] (bf16 or fp32, everything of one type).  gate is None, [D], or [G, D] with G a divisor
+    of T (each T / G consecutive tokens share a row); residual_scale None or [D].  Returns (out, rstd); with
+    next_weight also the next block's rms_norm of out as stored, from the same pass: (out, rstd, y, rstd_next),
+    or (out, rstd, q, scale, rstd_next) with quantize=True."""
+    torch = _torch()
+    e, T, D, dev, types = _norm_shape(h, "h")
+    _need(h, "h", types, (T, D), dev)
+    _need(residual, "residual", types, (T, D), dev)
+    _need(weight, "weight", types, (D,), dev)
+    if quantize and next_weight is None:
+        raise ValueError("quantize needs next_weight")
+    out = torch.empty_like(h)
+    rstd = torch.empty((T,), dtype=torch.float32, device=dev)
+    a = _NormArgs(elem=e, eps=eps, h=h.data_ptr(), residual=residual.data_ptr(), weight=weight.data_ptr(),
+                  out=out.data_ptr(), rstd=rstd.data_ptr(), T=T, D=D, stream=_stream(h, stream))
+    if gate is not None:
+        a.gates = _gates(gate, T, D, types, dev)
+        a.gate = gate.data_ptr()
+    if residual_scale is not None:
+        _need(residual_scale, "residual_scale", types, (D,), dev)
+        a.residual_scale = residual_scale.data_ptr()
+    more = () if next_weight is None else _norm_outputs(a, h, next_weight, quantize, T, D, types, dev)
+    _ok(load().sk_norm_forward(ctypes.byref(a)), "sk_norm_forward")
+    return (out, rstd, *more)
+
+
+def rms_norm_backward(dy, x, weight, rstd, dresidual=None, *, stream=None):
+    """Gradients of rms_norm: returns (dx, dweight).  dresidual, a gradient that reaches x by another way
+    (a residual branch), is added to dx in the same pass."""
+    torch = _torch()
+    e, T, D, dev, types = _norm_shape(x, "x")
+    for t, n in ((x, "x"), (dy, "dy")) + (((dresidual, "dresidual"),) if dresidual is not None else ()):
+        _need(t, n, types, (T, D), dev)
+    _need(weight, "weight", types, (D,), dev)
+    _need(rstd, "rstd", (torch.float32,), (T,), dev)
+    dx, dw = torch.empty_like(x), torch.empty_like(weight)
+    a = _NormGradArgs(elem=e, dout=_ptr(dresidual), dy=dy.data_ptr(), out=x.data_ptr(), next_weight=weight.data_ptr(),
+                      rstd_next=rstd.data_ptr(), dx=dx.data_ptr(), dnext_weight=dw.data_ptr(), T=T, D=D,
+                      stream=_stream(x, stream))
+    _ok(load().sk_norm_backward(ctypes.byref(a)), "sk_norm_backward")
+    return dx, dw
+
+
+def gated_norm_backward(dout, h, weight, rstd, gate=None, residual=None, residual_scale=None, *, dy=None, out=None,
+                        next_weight=None, rstd_next=None, stream=None):
+    """Gradients of gated_norm: returns (dh, dresidual, dweight, dgate, dresidual_scale, dnext_weight), None
+    where there is no such input.  dout is the gradient at out; where the forward also made the next block's norm,
+    dy is the gradient at y (for a quantised y too) and out, next_weight, rstd_next are that norm's input,
+    weight and statistic.  residual is needed only with residual_scale."""
+    torch = _torch()
+    e, T, D, dev, types = _norm_shape(h, "h")
+    _need(h, "h", types, (T, D), dev)
+    _need(dout, "dout", types, (T, D), dev)
+    _need(weight, "weight", types, (D,), dev)
+    _need(rstd, "rstd", (torch.float32,), (T,), dev)
+    dh, dres, dw = torch.empty_like(h), torch.empty_like(h), torch.empty_like(weight)
+    a = _NormGradArgs(elem=e, dout=dout.data_ptr(), h=h.data_ptr(), weight=weight.data_ptr(), rstd=rstd.data_ptr(),
+                      dx=dh.data_ptr(), dresidual=dres.data_ptr(), dweight=dw.data_ptr(), T=T, D=D,
+                      stream=_stream(h, stream))
+    dgate = drs = dnw = None
+    if gate is not None:
+        a.gates = _gates(gate, T, D, types, dev)
+        dgate = torch.empty_like(gate)
+        a.gate, a.dgate = gate.data_ptr(), dgate.data_ptr()
+    if residual_scale is not None:
+        _need(residual, "residual", types, (T, D), dev)
+        _need(residual_scale, "residual_scale", types, (D,), dev)
+        drs = torch.empty_like(residual_scale)
+        a.residual, a.residual_scale, a.dresidual_scale = residual.data_ptr(), residual_scale.data_ptr(), drs.data_ptr()
+    if dy is not None:
+        _need(dy, "dy", types, (T, D), dev)
+        _need(out, "out", types, (T, D), dev)
+        _need(next_weight, "next_weight", types, (D,), dev)
+        _need(rstd_next, "rstd_next", (torch.float32,), (T,), dev)
+        dnw = torch.empty_like(next_weight)
+        a.dy, a.out, a.next_weight = dy.data_ptr(), out.data_ptr(), next_weight.data_ptr()
+        a.rstd_next, a.dnext_weight = rstd_next.data_ptr(), dnw.data_ptr()
+    elif out is not None or next_weight is not None or rstd_next is not None:
+        raise ValueError("out, next_weight and rstd_next come with dy")
+    _ok(load().sk_norm_backward(ctypes.byref(a)), "sk_norm_backward")
+    return dh, dres, dw, dgate, drs, dnw
 
 
 def phase_summary(words, grid: int, plan: "Plan | None" = None) -> dict:

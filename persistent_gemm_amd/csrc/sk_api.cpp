@@ -21,6 +21,7 @@
 
 #include "../../include/sk_gemm.h"
 #include "sk_common.h"
+#include "sk_host.h"
 
 namespace {
 
@@ -46,7 +47,7 @@ struct Workspace {
   size_t p_bytes = 0;
   uint8_t* S = nullptr;       // MXFP4 scales of A and B, k-step-major
   size_t s_bytes = 0;
-  uint8_t* T = nullptr;       // bf16 backward: transposed operands, dbias partial sums
+  uint8_t* T = nullptr;       // backward passes: transposed or quantised operands, partial column sums
   size_t t_bytes = 0;
   uint32_t* flags = nullptr;  // kMaxGrid locks, then the error word
   uint32_t epoch = 0;         // last epoch used
@@ -635,6 +636,24 @@ sk_gemm_args base_args(int dtype, const void* A, const void* B, const void* sa, 
 }
 
 }  // namespace
+
+namespace sk {
+namespace host {
+
+sk_status device_for(hipStream_t stream, int* dev, int* cus) {
+  DeviceInfo info;
+  sk_status st = device_info(dev, &info);
+  if (st != SK_OK) return st;
+  if (!info.gfx950) return SK_ERR_UNSUPPORTED;
+  *cus = stream_cus(*dev, stream, info.cus);
+  return SK_OK;
+}
+sk_status refuse_capture(hipStream_t stream) { return ::refuse_capture(stream); }
+sk_status scratch(int dev, hipStream_t stream, size_t bytes, uint8_t** out) { return get_aux(dev, stream, bytes, out); }
+bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) { return ::overlaps(a, na, b, nb); }
+
+}  // namespace host
+}  // namespace sk
 
 extern "C" {
 

@@ -208,4 +208,87 @@ hipError_t launch_transpose_bf16(const uint16_t* src, uint16_t* dst, int rows, i
 int64_t colsum_scratch_bytes(int M, int N);
 hipError_t launch_colsum_bf16(const uint16_t* dc, float* part, uint16_t* dbias, int M, int N, hipStream_t s);
 
+// ---------------------------------------------------------------- fp32-block-scaled E4M3 and norms
+
+// The block quantiser (sk_quantize.hip).  x [R][C]; q [R][pitch] with scales [kb][R] (blocks of a row) or
+// [rb][kb] (128 x 128); qt [C][pitch_t] with scales [rb][C] or [kb][rb].  Either form may be absent.
+struct QuantArgs {
+  const void* x;
+  uint8_t* q;
+  float* scale;
+  uint8_t* qt;
+  float* scale_t;
+  float* part;        // NULL, or the column sums of each 128 rows, [rb][C] (bf16, blocks of a row only)
+  int R, C;
+  int pitch, pitch_t; // C and R rounded up to 16
+  int kb, rb;         // ceil(C / 128), ceil(R / 128)
+};
+hipError_t launch_quantize_block(const QuantArgs& a, bool f32, bool tile, hipStream_t s);
+
+// One block-scaled product C = A . B^T + bias (sk_gemm_block.hip).
+struct BlockGemm {
+  const uint8_t* A;       // [M][row_bytes]
+  const uint8_t* B;       // [N][row_bytes]
+  const float* SA;        // [kb][M]
+  const float* SB;        // [kb][N], or [ceil(N / 128)][kb] (b_tile)
+  const uint16_t* bias;   // bf16[N] or NULL
+  uint16_t* C;            // bf16[M][N]
+  int M, N;
+  int row_bytes;          // K, a multiple of 16
+  int kb;                 // ceil(K / 128)
+  int tiles_m, tiles_n;
+};
+hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int cus, hipStream_t s);
+
+// The norms (sk_norm.hip).  Pointers are NULL where a part is absent; T is one of bf16 / fp32.
+struct NormArgs {
+  const void* h;              // [T][D], NULL: no norm after a block
+  const void* residual;       // [T][D]: x itself when h is NULL
+  const void* weight;         // [D], with h
+  const void* gate;           // [T / gate_rows][D] or NULL
+  const void* residual_scale; // [D] or NULL
+  const void* next_weight;    // [D], NULL: no norm before a block
+  void* out;                  // [T][D], with h
+  float* rstd;                // [T], with h
+  void* y;                    // [T][D], or NULL when quantised
+  uint8_t* q;                 // [T][pitch]
+  float* scale;               // [blocks][T]
+  float* rstd_next;           // [T]
+  float eps;
+  int T, D;
+  int gate_rows;              // tokens that share a row of the gate
+  int pitch, blocks;
+};
+hipError_t launch_norm_forward(const NormArgs& a, bool f32, int cus, hipStream_t s);
+
+struct NormGradArgs {
+  const void* dout;           // [T][D], the gradient at out (at x when h is NULL; may then be NULL)
+  const void* dy;             // [T][D], NULL: no norm before the next block
+  const void* out;            // [T][D]: what that norm read
+  const void* next_weight;
+  const float* rstd_next;
+  const void* h;              // NULL: only the norm before a block
+  const void* residual;       // with residual_scale
+  const void* weight;
+  const void* gate;
+  const void* residual_scale;
+  const float* rstd;
+  void* dx;                   // [T][D]: dh, or dx when h is NULL
+  void* dresidual;            // [T][D], with h
+  void* dweight;              // [D]
+  void* dgate;                // [T / gate_rows][D]
+  void* dresidual_scale;      // [D]
+  void* dnext_weight;         // [D]
+  float* part;                // scratch
+  int T, D;
+  int gate_rows;
+  // set by the launcher
+  int rows_per_chunk, chunks_per_gate, chunks, groups;
+};
+int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus);
+hipError_t launch_norm_backward(const NormGradArgs& a, bool f32, hipStream_t s);
+constexpr int kMaxNormWidth = 32768;
+// out[d] = bf16 of the sum over `count` rows of part [count][D], in a fixed order.
+hipError_t launch_column_sums_bf16(const float* part, uint16_t* out, int count, int D, hipStream_t s);
+
 }  // namespace sk

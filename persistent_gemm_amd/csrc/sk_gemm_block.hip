@@ -1,0 +1,370 @@
+// The product of E4M3 operands with an fp32 scale for each block of 128 along K:
+//
+//   C[m][n] = bf16( sum_b SA[b][m] SB(b, n) sum_{k in b} A[m][k] B[n][k] + bias[n] )
+//
+// SB(b, n) is a scale of its own for each row of B, [b][n], or one for 128 rows, [n / 128][b].  A block's
+// inner sum is one v_mfma_f32_16x16x128_f8f6f4 from a zero accumulator; its 16 x 16 result is multiplied by
+// the scales and added to the fp32 accumulators on the vector ALU (they change from block to block, so the
+// MFMA cannot carry them, and its own scale operands are powers of two).  That is one fma per output and
+// block (and one product of the two scales more where B has a scale per row): 4 x 4 cycles beside an MFMA of
+// 32, issued by the same SIMD while the matrix core runs.
+//
+// Tiled kernels: k-steps of one block.  A's and B's 128 bytes per row and the step's scales go straight from
+// memory into LDS (16-byte and 4-byte direct loads), in a ring of STAGES; the 16-byte chunks of row r are
+// permuted by (r >> 1) & 7 so that 16 lanes reading a chunk of 16 rows meet all banks.  The accumulators are
+// ordinary registers (the ALU cannot reach AGPRs), which bounds a wave's tile to 64 x 128.
+// Skinny kernels (few rows of A): see sk_gemm_block_rows.
+
+#include "sk_fp8.h"
+#include "sk_kernel.h"
+
+namespace sk {
+
+namespace {
+
+// A tile's 128-byte k-step of BM rows of A and BN of B over WM x WN waves.
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
+struct BlockCfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int WTM = BM / WM, WTN = BN / WN;
+  static constexpr int FM = WTM / 16, FN = WTN / 16;
+  static constexpr int A_PT = BM / 8 / NW, B_PT = BN / 8 / NW;      // 1 KiB loads (8 rows) per wave
+  static constexpr int S_INST = (BM + BN) / 64;                     // 256-byte scale loads of a stage
+  static constexpr int PER_STAGE = A_PT + B_PT + 1;
+  static constexpr int B_OFF = BM * kBlock, S_OFF = (BM + BN) * kBlock;
+  static constexpr int STAGE = S_OFF + (BM + BN) * 4;
+  static constexpr int OUT_WAVE = WTM * WTN * 2;                    // a wave's bf16 outputs
+  static constexpr int CH = WTN / 8;                                // 16-byte chunks of an output row
+  static constexpr int LDS = STAGES * STAGE;
+  static_assert(A_PT * NW * 8 == BM && B_PT * NW * 8 == BN && NW % 2 == 0, "whole loads, 16-row periods");
+  static_assert(S_INST <= NW, "one scale load per wave and stage");
+  static_assert(WTM % 16 == 0 && WTN % 16 == 0 && WTN <= 128 && 128 % WTN == 0, "a wave's columns share a tile scale");
+  static_assert(NW * OUT_WAVE <= LDS && LDS <= 160 * 1024, "LDS");
+  static_assert((STAGES - 1) * PER_STAGE <= 63, "vmcnt range");
+};
+
+// Tile t of the launch as (tile row, tile column): workgroups are dealt to the eight XCDs in turn, so each
+// XCD gets a contiguous range of tiles, and within it patches of GROUP tile rows by whole columns,
+// whose operands its L2 then holds for several workgroups.
+template <int GROUP>
+__device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int* tm, int* tn) {
+  const int T = tiles_m * tiles_n, x = t & 7, per = T >> 3, rest = T & 7;
+  const int i = x * per + min(x, rest) + (t >> 3);
+  const int band = i / (GROUP * tiles_n), in = i - band * GROUP * tiles_n;
+  const int rows = min(GROUP, tiles_m - band * GROUP);
+  *tn = in / rows;
+  *tm = band * GROUP + (in - *tn * rows);
+}
+
+// Words that are the same in every lane, said so (the compiler keeps 64-bit products in vector registers).
+__device__ __forceinline__ v4u uniform(const v4u& x) {
+  v4u r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (uint32_t)__builtin_amdgcn_readfirstlane((int)x[i]);
+  return r;
+}
+
+// One block's inner products, transposed as elsewhere here (B first): lane l gets A row l % 16 and the four
+// B rows 4 (l / 16) .. +3.  The operand order within the 128 elements is the same for both, so any will do.
+__device__ __forceinline__ v4f block_mfma(const v4u (&b)[2], const v4u (&a)[2]) {
+  auto v = [](const v4u(&x)[2]) {
+    return v8i{(int)x[0][0], (int)x[0][1], (int)x[0][2], (int)x[0][3],
+               (int)x[1][0], (int)x[1][1], (int)x[1][2], (int)x[1][3]};
+  };
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v(b), v(a), v4f{}, FMT_E4M3, FMT_E4M3, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ v4f ld_v4f(const lds_u8* p) { return *(const __attribute__((address_space(3))) v4f*)p; }
+__device__ __forceinline__ v4u ld_v4u(const lds_u8* p) { return *(const __attribute__((address_space(3))) v4u*)p; }
+
+// Four outputs of a row: sums plus bias, rounded once to bf16 (the sum with the bias is one more fp32 addition).
+__device__ __forceinline__ v2u out4(const v4f& x, const float (&b)[4]) {
+  return v2u{pack_bf16(x[0] + b[0], x[1] + b[1]), pack_bf16(x[2] + b[2], x[3] + b[3])};
+}
+
+template <class C, bool BROW>
+__global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem_raw[C::LDS];
+  lds_u8* const smem = (lds_u8*)smem_raw;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int lr = lane & 15, lg = lane >> 4;
+  const uint32_t rb = (uint32_t)g.row_bytes;
+
+  // The lane's part of a direct load: slot lane % 8 of row lane / 8 of an 8-row group; every group of a wave
+  // is a whole number of 16-row periods from the first, so they share the chunk.
+  const int grow = wave * 8 + (lane >> 3);
+  const uint32_t chunk = (uint32_t)(((lane & 7) ^ ((grow >> 1) & 7)) * 16);
+  const uint32_t lim = chunk < rb ? rb - chunk : 0u;     // k-step offsets at which the chunk lies in the row
+  uint32_t off[C::A_PT > C::B_PT ? C::A_PT : C::B_PT];
+#pragma unroll
+  for (int i = 0; i < (C::A_PT > C::B_PT ? C::A_PT : C::B_PT); ++i) off[i] = (uint32_t)(grow + i * C::NW * 8) * rb + chunk;
+
+  // The lane's operand chunks 2 lg, 2 lg + 1 of row lr of each 16-row block.
+  const int sw = (lr >> 1) & 7;
+  const int c0 = ((2 * lg) ^ sw) * 16, c1 = ((2 * lg + 1) ^ sw) * 16;
+  const int arow = (wm * C::WTM + lr) * kBlock, brow = C::B_OFF + (wn * C::WTN + lr) * kBlock;
+
+  const int sidx = wave % C::S_INST;         // (waves past the last load repeat one: the same bytes to the same place)
+  const bool s_is_a = sidx < C::BM / 64;
+
+  const int T = g.tiles_m * g.tiles_n;
+  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    int tm, tn;
+    tile_of<C::BM >= 256 ? 4 : 8>(t, g.tiles_m, g.tiles_n, &tm, &tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    const int m0 = tm * C::BM, n0 = tn * C::BN;
+    const int rows = min(C::BM, g.M - m0), cols = min(C::BN, g.N - n0);
+    const v4u ra = rsrc_words(g.A + (int64_t)m0 * rb, (uint32_t)rows * rb);
+    const v4u rbw = rsrc_words(g.B + (int64_t)n0 * rb, (uint32_t)cols * rb);
+    // This wave's scale load of a stage, 64 floats: rows of A, or columns of B (element e of [A rows, B columns]),
+    // whose scale is their own or that of their 128 columns.  k-step d's are sstep floats after the last one's.
+    const int e = sidx * 64 + lane, j = e - C::BM, nb = n0 % kBlock;
+    const float* const sbase = s_is_a ? g.SA + m0 : BROW ? g.SB + n0 : g.SB + (int64_t)(n0 / kBlock) * g.kb;
+    const int64_t sstep = s_is_a ? g.M : BROW ? g.N : 1;
+    const uint32_t sbytes = (uint32_t)(s_is_a ? rows : BROW ? cols : g.kb * ((nb + cols - 1) / kBlock + 1)) * 4u;
+    const uint32_t svoff = s_is_a ? (e < rows ? (uint32_t)e * 4u : kOob)
+                         : j >= cols ? kOob : (uint32_t)(BROW ? j : (nb + j) / kBlock * g.kb) * 4u;
+
+    // k-step d into stage d % STAGES; past the last one every lane is out of range (zeros, no traffic)
+    auto issue = [&](int d) {
+      const uint32_t stage = (uint32_t)(uintptr_t)smem + (uint32_t)(d % C::STAGES) * C::STAGE;
+      const uint32_t kbyte = (uint32_t)d * kBlock;
+      const bool live = d < g.kb;
+      const bool in = live && kbyte < lim;
+#pragma unroll
+      for (int i = 0; i < C::A_PT; ++i)
+        dma_load16(ra, in ? off[i] : kOob, live ? kbyte : 0u, stage + (uint32_t)(wave + i * C::NW) * 1024u);
+#pragma unroll
+      for (int i = 0; i < C::B_PT; ++i)
+        dma_load16(rbw, in ? off[i] : kOob, live ? kbyte : 0u, stage + C::B_OFF + (uint32_t)(wave + i * C::NW) * 1024u);
+      const v4u rs = uniform(rsrc_words(sbase + (live ? d : 0) * sstep, sbytes));
+      dma_load4(rs, live ? svoff : kOob, 0u, stage + C::S_OFF + (uint32_t)sidx * 256u);
+    };
+
+    v4f acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{};
+
+#pragma unroll
+    for (int d = 0; d < C::STAGES - 1; ++d) issue(d);
+    for (int d = 0; d < g.kb; ++d) {
+      // stage d has landed (at most the later stages' loads are in flight), and stage d - 1 is read by all
+      wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE>();
+      lds_barrier();
+      issue(d + C::STAGES - 1);
+      const lds_u8* const st = smem + (d % C::STAGES) * C::STAGE;
+      v4u a[C::FM][2];
+      float sa[C::FM];
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        a[i][0] = ld_v4u(st + arow + i * 16 * kBlock + c0);
+        a[i][1] = ld_v4u(st + arow + i * 16 * kBlock + c1);
+        sa[i] = *(const __attribute__((address_space(3))) float*)(st + C::S_OFF + (wm * C::WTM + i * 16 + lr) * 4);
+      }
+      if constexpr (!BROW) {
+        const float sb = *(const __attribute__((address_space(3))) float*)(st + C::S_OFF + (C::BM + wn * C::WTN) * 4);
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) sa[i] *= sb;
+      }
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        v4u b[2];
+        b[0] = ld_v4u(st + brow + j * 16 * kBlock + c0);
+        b[1] = ld_v4u(st + brow + j * 16 * kBlock + c1);
+        v4f sb;
+        if constexpr (BROW) sb = ld_v4f(st + C::S_OFF + (C::BM + wn * C::WTN + j * 16 + 4 * lg) * 4);
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+          const v4f p = block_mfma(b, a[i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            acc[i][j][k] = __builtin_fmaf(BROW ? sa[i] * sb[k] : sa[i], p[k], acc[i][j][k]);
+        }
+      }
+    }
+
+    // outputs: each wave's through its own part of LDS, so that a store fills whole lines
+    wait_vmcnt_n<0>();
+    lds_barrier();
+    const __amdgpu_buffer_rsrc_t rc = make_rsrc(g.C + (int64_t)m0 * g.N, (uint32_t)rows * (uint32_t)g.N * 2u);
+    const bool staged = (g.N & 7) == 0;
+    lds_u8* const so = smem + wave * C::OUT_WAVE;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int col = n0 + wn * C::WTN + j * 16 + 4 * lg;
+      float bias[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        bias[k] = g.bias && col + k < g.N ? bits_f((uint32_t)g.bias[col + k] << 16) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const v2u h = out4(acc[i][j], bias);
+        const int row = i * 16 + lr;
+        if (staged) {
+          const int c = (2 * j + (lg >> 1)) ^ (row & (C::CH - 1));
+          *(__attribute__((address_space(3))) v2u*)(so + row * (C::WTN * 2) + c * 16 + (lg & 1) * 8) = h;
+        } else {
+          const uint32_t at = ((uint32_t)(wm * C::WTM + row) * (uint32_t)g.N + (uint32_t)col) * 2u;
+          const uint32_t v[4] = {h[0] & 0xffffu, h[0] >> 16, h[1] & 0xffffu, h[1] >> 16};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v[k], rc, col + k < g.N ? at + 2u * k : kOob, 0, 0);
+        }
+      }
+    }
+    if (staged) {
+      asm volatile("" ::: "memory");   // (one wave's LDS operations execute in order)
+      constexpr int RPI = 64 / C::CH;  // rows per store
+#pragma unroll
+      for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
+        const int row = r0 + lane / C::CH, c = lane % C::CH;
+        const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
+        const int col = n0 + wn * C::WTN + c * 8;
+        const uint32_t at = ((uint32_t)(wm * C::WTM + row) * (uint32_t)g.N + (uint32_t)col) * 2u;
+        __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < g.N ? at : kOob, 0, 0);
+      }
+    }
+    if (t + (int)gridDim.x < T) lds_barrier();   // the next tile's loads go where the outputs were read from
+  }
+}
+
+// Few rows of A: a workgroup takes 16 NB columns and 16 MB rows, and its NWK waves share out the blocks of K
+// in turn (wave w: blocks w, w + NWK, ...), so that together they read whole stretches of each row of B.  The
+// operands go straight to registers, U blocks at a time, with no barrier before the end, where the waves' sums
+// are added in LDS in wave order.  Bound by reading B once.
+template <int MB, int NB, int NWK, int U, bool BROW>
+__global__ __launch_bounds__(64 * NWK) void sk_gemm_block_rows(BlockGemm g) {
+  __shared__ __attribute__((aligned(16))) float red[NWK][MB * NB][64][4];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int lr = lane & 15, lg = lane >> 4;
+  const int tn = blockIdx.x % g.tiles_n, tm = blockIdx.x / g.tiles_n;
+  const int m0 = tm * 16 * MB, n0 = tn * 16 * NB;
+  const int rows = min(16 * MB, g.M - m0), cols = min(16 * NB, g.N - n0);
+  const uint32_t rb = (uint32_t)g.row_bytes;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.A + (int64_t)m0 * rb, (uint32_t)rows * rb);
+  const __amdgpu_buffer_rsrc_t rbr = make_rsrc(g.B + (int64_t)n0 * rb, (uint32_t)cols * rb);
+  v4f acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = v4f{};
+
+  for (int k0 = wave; k0 < g.kb; k0 += NWK * U) {
+    v4u a[U][MB][2], b[U][NB][2];
+    float sa[U][MB];
+    v4f sb[U][NB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * NWK;
+      const uint32_t at = (uint32_t)(k * kBlock + 32 * lg);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c = at + 16u * h;
+        const bool in = k < g.kb && c < rb;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          b[u][j][h] = __builtin_amdgcn_raw_buffer_load_b128(rbr, in ? (uint32_t)(j * 16 + lr) * rb + c : kOob, 0, 0);
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+          a[u][i][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? (uint32_t)(i * 16 + lr) * rb + c : kOob, 0, 0);
+      }
+      const int ks = min(k, g.kb - 1);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const float s = g.SA[(int64_t)ks * g.M + min(m0 + i * 16 + lr, g.M - 1)];
+        sa[u][i] = k < g.kb ? s : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if constexpr (BROW) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sb[u][j][q] = g.SB[(int64_t)ks * g.N + min(n0 + j * 16 + 4 * lg + q, g.N - 1)];
+        } else {
+          // (columns past N may start the next 128: their outputs are not stored)
+          const int n = min(n0 + j * 16, g.N - 1);
+          sb[u][j][0] = g.SB[(int64_t)(n / kBlock) * g.kb + ks];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          const v4f p = block_mfma(b[u][j], a[u][i]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            acc[i][j][q] = __builtin_fmaf(sa[u][i] * sb[u][j][BROW ? q : 0], p[q], acc[i][j][q]);
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) *(v4f*)red[wave][i * NB + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int run = threadIdx.x; run < 64 * MB * NB; run += 64 * NWK) {
+    const int blk = run >> 6, l = run & 63;
+    v4f x = *(const v4f*)red[0][blk][l];
+#pragma unroll
+    for (int w = 1; w < NWK; ++w) x += *(const v4f*)red[w][blk][l];
+    const int row = m0 + (blk / NB) * 16 + (l & 15), col = n0 + (blk % NB) * 16 + 4 * (l >> 4);
+    if (row >= g.M || col >= g.N) continue;
+    float bias[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bias[k] = g.bias && col + k < g.N ? bits_f((uint32_t)g.bias[col + k] << 16) : 0.0f;
+    const v2u h = out4(x, bias);
+    uint16_t* const o = g.C + (int64_t)row * g.N + col;
+    if ((g.N & 3) == 0) {
+      *(v2u*)o = h;
+    } else {
+      const uint32_t v[4] = {h[0] & 0xffffu, h[0] >> 16, h[1] & 0xffffu, h[1] >> 16};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (col + k < g.N) o[k] = (uint16_t)v[k];
+    }
+  }
+}
+
+template <class C>
+hipError_t launch_tiled(BlockGemm g, bool b_tile, int grid_cap, int cus, hipStream_t s) {
+  g.tiles_m = cdiv(g.M, C::BM);
+  g.tiles_n = cdiv(g.N, C::BN);
+  const int64_t T = (int64_t)g.tiles_m * g.tiles_n;
+  if (T > 0x7fffffff) return hipErrorInvalidValue;
+  const int grid = grid_cap > 0 && grid_cap < T ? grid_cap : (int)T;
+  if (b_tile) hipLaunchKernelGGL((sk_gemm_block<C, false>), dim3(grid), dim3(C::NT), 0, s, g);
+  else hipLaunchKernelGGL((sk_gemm_block<C, true>), dim3(grid), dim3(C::NT), 0, s, g);
+  return hipGetLastError();
+}
+
+template <int MB, int NB, int NWK, int U>
+hipError_t launch_rows(BlockGemm g, bool b_tile, hipStream_t s) {
+  g.tiles_m = cdiv(g.M, 16 * MB);
+  g.tiles_n = cdiv(g.N, 16 * NB);
+  const dim3 grid((unsigned)(g.tiles_m * g.tiles_n)), block(64 * NWK);
+  if (b_tile) hipLaunchKernelGGL((sk_gemm_block_rows<MB, NB, NWK, U, false>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((sk_gemm_block_rows<MB, NB, NWK, U, true>), grid, block, 0, s, g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int cus, hipStream_t s) {
+  if (grid_cap <= 0) {
+    if (g.M <= 16) return launch_rows<1, 1, 8, 4>(g, b_tile, s);
+    if (g.M <= 32) return launch_rows<2, 1, 8, 4>(g, b_tile, s);
+    if (g.M <= 64) return launch_rows<4, 2, 8, 2>(g, b_tile, s);
+  }
+  auto tiles = [&](int bm, int bn) { return (int64_t)cdiv(g.M, bm) * cdiv(g.N, bn); };
+  if (tiles(256, 256) * 4 >= (int64_t)cus * 3) return launch_tiled<BlockCfg<256, 256, 4, 2, 2>>(g, b_tile, grid_cap, cus, s);
+  if (tiles(128, 128) * 2 >= cus) return launch_tiled<BlockCfg<128, 128, 2, 2, 4>>(g, b_tile, grid_cap, cus, s);
+  return launch_tiled<BlockCfg<64, 64, 2, 2, 4>>(g, b_tile, grid_cap, cus, s);
+}
+
+}  // namespace sk

@@ -1,0 +1,421 @@
+// Root-mean-square norms before and after a block, with what stands next to them in one pass:
+//
+//   after a block:   out = residual_scale * residual + gate * (h rstd weight)      (h given)
+//   before a block:  y = v rstd_next next_weight, v = out as stored (or x)         (next_weight given)
+//                    as it is, or as E4M3 codes with a scale per 128 for the product that follows
+//   rstd = (mean of squares + eps)^-1/2
+//
+// and their gradients.  A row is held in registers by TPR threads (a wave, with four rows to a workgroup, or
+// a workgroup), CH pieces of eight elements each, so every tensor is read once and written once: all of it
+// is bound by HBM (by latency for few rows).  Statistics and sums are fp32.  Rows need no alignment beyond
+// their elements' (a row of odd length starts anywhere).
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sk_common.h"
+#include "sk_fp8.h"
+
+namespace sk {
+
+namespace {
+
+constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The sum over the TPR threads of a row, in each of them.  `red`: two areas of 16 floats, used in turn, so that
+// one barrier a sum is enough (whoever writes an area again has passed the barrier after its last reading).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, float (*red)[16], int& turn) {
+  x = wave_sum(x);
+  if constexpr (TPR > 64) {
+    float* const r = red[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = r[0];
+#pragma unroll
+    for (int w = 1; w < TPR / 64; ++w) x += r[w];
+  }
+  return x;
+}
+
+template <int TPR>
+constexpr int rows_per_wg() { return TPR == 64 ? 4 : 1; }
+
+// ---------------------------------------------------------------- forward
+
+template <class T, bool POST, bool PRE, bool FP8, int TPR, int CH>
+__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_forward(NormArgs a) {
+  __shared__ float red[2][16];
+  int turn = 0;
+  constexpr int RPW = rows_per_wg<TPR>();
+  const int t = threadIdx.x % TPR, D = a.D;
+  const float inv = 1.0f / (float)D;
+  for (int row = blockIdx.x * RPW + threadIdx.x / TPR; row < a.T; row += gridDim.x * RPW) {
+    const int64_t at = (int64_t)row * D;
+    float v[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = 8 * (t + c * TPR);
+      load8<T>((const T*)a.residual + at + col, min(8, max(0, D - col)), v[c]);
+    }
+    if constexpr (POST) {
+      float h[CH][8], ss = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = 8 * (t + c * TPR);
+        load8<T>((const T*)a.h + at + col, min(8, max(0, D - col)), h[c]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(h[c][k], h[c][k], ss);
+      }
+      const float r = 1.0f / __builtin_sqrtf(row_sum<TPR>(ss, red, turn) * inv + a.eps);
+      if (t == 0) a.rstd[row] = r;
+      const T* const gate = a.gate ? (const T*)a.gate + (int64_t)(row / a.gate_rows) * D : nullptr;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
+        float w[8], x[8];
+        load8<T>((const T*)a.weight + col, n, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[c][k] *= r * w[k];
+        if (gate) {
+          load8<T>(gate + col, n, x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[c][k] *= x[k];
+        }
+        if (a.residual_scale) {
+          load8<T>((const T*)a.residual_scale + col, n, x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[c][k] = __builtin_fmaf(v[c][k], x[k], h[c][k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[c][k] += h[c][k];
+        }
+        store8((T*)a.out + at + col, n, v[c]);
+        // the next norm reads what is stored
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[c][k] = rounded<T>(v[c][k]);
+      }
+    }
+    if constexpr (PRE) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(v[c][k], v[c][k], ss);
+      const float r = 1.0f / __builtin_sqrtf(row_sum<TPR>(ss, red, turn) * inv + a.eps);
+      if (t == 0) a.rstd_next[row] = r;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
+        float w[8];
+        load8<T>((const T*)a.next_weight + col, n, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[c][k] = v[c][k] * r * w[k];
+        if constexpr (FP8) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m = max(m, f_bits(v[c][k]) & kAbs);
+          const BlockScale b = Coder<float>::scale(max16(m));     // 16 lanes hold a block of 128
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[c][k] = Coder<float>::nudged(v[c][k], b);
+          // rows hold D rounded up to 16 codes: a piece of eight is inside or outside as a whole
+          if (col < a.pitch)
+            *(u32x2*)(a.q + (int64_t)row * a.pitch + col) = u32x2{codes4(v[c][0], v[c][1], v[c][2], v[c][3], b.s),
+                                                                codes4(v[c][4], v[c][5], v[c][6], v[c][7], b.s)};
+          if ((t & 15) == 0 && col < D) a.scale[(int64_t)(col / kBlock) * a.T + row] = b.s;
+        } else {
+          store8((T*)a.y + at + col, n, v[c]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+// Workers (a workgroup, or a wave of four) take runs of consecutive rows and keep the column sums of the
+// weights' gradients in registers; each run lies within the tokens that share a row of the gate.  A second
+// kernel adds the workers' sums in worker order, so the results repeat bit for bit.
+//
+// part: [3][workers][D] (weight, next_weight, residual_scale), then [chunks][D] of the gate
+// where a gate row has more than one chunk.
+template <class T, bool POST, bool PRE, int TPR, int CH>
+__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_backward(NormGradArgs a) {
+  __shared__ float red[2][16];
+  int turn = 0;
+  constexpr int RPW = rows_per_wg<TPR>();
+  const int t = threadIdx.x % TPR, D = a.D;
+  const float inv = 1.0f / (float)D;
+  const int worker = blockIdx.x * RPW + threadIdx.x / TPR, workers = gridDim.x * RPW;
+  const bool gate_sums = POST && a.gate && a.gate_rows > 1;
+  const int group_rows = a.T / a.groups;
+  float dw[POST ? CH : 1][8] = {}, dnw[PRE ? CH : 1][8] = {}, drs[POST ? CH : 1][8] = {}, dg[POST ? CH : 1][8] = {};
+
+  const int per = ceil_div(a.chunks, workers);
+  const int chunk1 = min(a.chunks, (worker + 1) * per);
+  for (int chunk = worker * per; chunk < chunk1; ++chunk) {
+    const int group = chunk / a.chunks_per_gate, part = chunk - group * a.chunks_per_gate;
+    const int row0 = group * group_rows + part * a.rows_per_chunk;
+    const int row1 = min(row0 + a.rows_per_chunk, (group + 1) * group_rows);
+    for (int row = row0; row < row1; ++row) {
+      const int64_t at = (int64_t)row * D;
+      float dv[CH][8];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = 8 * (t + c * TPR);
+        load8<T>((const T*)a.dout + at + col, a.dout ? min(8, max(0, D - col)) : 0, dv[c]);
+      }
+      float h[POST ? CH : 1][8];
+      if constexpr (POST) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int col = 8 * (t + c * TPR);
+          load8<T>((const T*)a.h + at + col, min(8, max(0, D - col)), h[c]);
+        }
+      }
+      if constexpr (PRE) {
+        const float r = a.rstd_next[row];
+        float x[CH][8], g[CH][8], s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
+          float w[8];
+          load8<T>((const T*)a.out + at + col, n, x[c]);
+          load8<T>((const T*)a.dy + at + col, n, g[c]);
+          load8<T>((const T*)a.next_weight + col, n, w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x[c][k] *= r;
+            dnw[c][k] = __builtin_fmaf(g[c][k], x[c][k], dnw[c][k]);
+            g[c][k] *= w[k];
+            s = __builtin_fmaf(g[c][k], x[c][k], s);
+          }
+        }
+        s = row_sum<TPR>(s, red, turn) * inv;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dv[c][k] = __builtin_fmaf(r, __builtin_fmaf(-s, x[c][k], g[c][k]), dv[c][k]);
+      }
+      if constexpr (!POST) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int col = 8 * (t + c * TPR);
+          store8((T*)a.dx + at + col, min(8, max(0, D - col)), dv[c]);
+        }
+      } else {
+        const float r = a.rstd[row];
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
+          float w[8], x[8];
+          if (a.residual_scale) {
+            load8<T>((const T*)a.residual + at + col, n, w);
+            load8<T>((const T*)a.residual_scale + col, n, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              drs[c][k] = __builtin_fmaf(dv[c][k], w[k], drs[c][k]);
+              x[k] *= dv[c][k];
+            }
+            store8((T*)a.dresidual + at + col, n, x);
+          } else {
+            store8((T*)a.dresidual + at + col, n, dv[c]);
+          }
+          load8<T>((const T*)a.weight + col, n, w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[c][k] *= r;
+          if (a.gate) {
+            load8<T>((const T*)a.gate + (int64_t)(row / a.gate_rows) * D + col, n, x);
+            if (gate_sums) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) dg[c][k] = __builtin_fmaf(dv[c][k] * h[c][k], w[k], dg[c][k]);
+            } else {
+              float own[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) own[k] = dv[c][k] * h[c][k] * w[k];
+              store8((T*)a.dgate + at + col, n, own);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dv[c][k] *= x[k];
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            dw[c][k] = __builtin_fmaf(dv[c][k], h[c][k], dw[c][k]);
+            dv[c][k] *= w[k];
+            s = __builtin_fmaf(dv[c][k], h[c][k], s);
+          }
+        }
+        s = row_sum<TPR>(s, red, turn) * inv;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int col = 8 * (t + c * TPR);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dv[c][k] = r * __builtin_fmaf(-s, h[c][k], dv[c][k]);
+          store8((T*)a.dx + at + col, min(8, max(0, D - col)), dv[c]);
+        }
+      }
+    }
+    if constexpr (POST) {
+      if (gate_sums) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
+          if (a.chunks_per_gate == 1) store8((T*)a.dgate + (int64_t)group * D + col, n, dg[c]);
+          else store8(a.part + ((int64_t)3 * workers + chunk) * D + col, n, dg[c]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dg[c][k] = 0.0f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
+    if constexpr (POST) {
+      store8(a.part + (int64_t)worker * D + col, n, dw[c]);
+      if (a.residual_scale) store8(a.part + (int64_t)(2 * workers + worker) * D + col, n, drs[c]);
+    }
+    if constexpr (PRE) store8(a.part + (int64_t)(workers + worker) * D + col, n, dnw[c]);
+  }
+}
+
+// out[d] = the sum of `count` rows of part, in a fixed order: thread (column, slice) of 32 x 8 adds the slice's
+// run of rows in turn, then the eight runs are added in turn.
+template <class T>
+__device__ __forceinline__ void column_sum(const float* __restrict__ part, T* __restrict__ out, int count, int D,
+                                           int block) {
+  __shared__ float run[8][32];
+  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5, d = block * 32 + col;
+  const int per = ceil_div(count, 8), c0 = slice * per, c1 = min(count, c0 + per);
+  float s = 0.0f;
+  if (d < D) {
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) s += part[(int64_t)c * D + d];
+  }
+  run[slice][col] = s;
+  __syncthreads();
+  if (slice || d >= D) return;
+  float x = run[0][col];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) x += run[k][col];
+  if constexpr (sizeof(T) == 2) out[d] = (T)pack_bf16(x, x);
+  else out[d] = x;
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void sk_column_sums(const float* part, T* out, int count, int D) {
+  column_sum<T>(part, out, count, D, blockIdx.x);
+}
+
+// The norms' sums: blockIdx.y 0, 1, 2 the three vectors, then the rows of the gate.
+template <class T>
+__global__ __launch_bounds__(256) void sk_norm_sums(NormGradArgs a, int workers) {
+  const int y = blockIdx.y;
+  if (y < 3) {
+    T* const out = (T*)(y == 0 ? a.dweight : y == 1 ? a.dnext_weight : a.dresidual_scale);
+    if (out) column_sum<T>(a.part + (int64_t)y * workers * a.D, out, workers, a.D, blockIdx.x);
+  } else {
+    const int group = y - 3;
+    column_sum<T>(a.part + ((int64_t)3 * workers + (int64_t)group * a.chunks_per_gate) * a.D,
+                  (T*)a.dgate + (int64_t)group * a.D, a.chunks_per_gate, a.D, blockIdx.x);
+  }
+}
+
+template <class T, bool POST, bool PRE, bool FP8, int TPR, int CH>
+hipError_t forward(const NormArgs& a, int cus, hipStream_t s) {
+  const int rpw = rows_per_wg<TPR>(), threads = TPR == 64 ? 256 : TPR;
+  const int wgs = ceil_div(a.T, rpw), most = cus * (2048 / threads) * 4;
+  hipLaunchKernelGGL((sk_norm_forward<T, POST, PRE, FP8, TPR, CH>), dim3(min(wgs, most)), dim3(threads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <class T, bool POST, bool PRE, bool FP8>
+hipError_t forward_width(const NormArgs& a, int cus, hipStream_t s) {
+  // Few rows: more threads to each, to shorten the call.  Many: as few as hold the row.
+  if (a.T <= 2 * cus && a.D > 512) {
+    if (a.D <= 2048) return forward<T, POST, PRE, FP8, 256, 1>(a, cus, s);
+    if (a.D <= 8192) return forward<T, POST, PRE, FP8, 1024, 1>(a, cus, s);
+  }
+  if (a.D <= 512) return forward<T, POST, PRE, FP8, 64, 1>(a, cus, s);
+  if (a.D <= 1024) return forward<T, POST, PRE, FP8, 64, 2>(a, cus, s);
+  if (a.D <= 2048) return forward<T, POST, PRE, FP8, 256, 1>(a, cus, s);
+  if (a.D <= 4096) return forward<T, POST, PRE, FP8, 256, 2>(a, cus, s);
+  if (a.D <= 8192) return forward<T, POST, PRE, FP8, 256, 4>(a, cus, s);
+  return forward<T, POST, PRE, FP8, 1024, 4>(a, cus, s);
+}
+
+template <class T>
+hipError_t forward_form(const NormArgs& a, int cus, hipStream_t s) {
+  if (!a.h) return a.q ? forward_width<T, false, true, true>(a, cus, s) : forward_width<T, false, true, false>(a, cus, s);
+  if (!a.next_weight) return forward_width<T, true, false, false>(a, cus, s);
+  return a.q ? forward_width<T, true, true, true>(a, cus, s) : forward_width<T, true, true, false>(a, cus, s);
+}
+
+// Threads of a row in the backward, and workers of a workgroup.
+int grad_threads(int D) { return D <= 512 ? 64 : D <= 2048 ? 256 : D <= 4096 ? 512 : 1024; }
+int grad_rpw(int D) { return D <= 512 ? 4 : 1; }
+int grad_wgs(const NormGradArgs& a) { return ceil_div(a.chunks, grad_rpw(a.D) * ceil_div(a.chunks, 4096)); }
+
+template <class T, bool POST, bool PRE, int TPR, int CH>
+hipError_t backward(const NormGradArgs& a, hipStream_t s) {
+  const int wgs = grad_wgs(a);
+  hipLaunchKernelGGL((sk_norm_backward<T, POST, PRE, TPR, CH>), dim3(wgs), dim3(TPR == 64 ? 256 : TPR), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const bool gate = a.dgate && a.gate_rows > 1 && a.chunks_per_gate > 1;
+  hipLaunchKernelGGL((sk_norm_sums<T>), dim3(ceil_div(a.D, 32), 3 + (gate ? a.groups : 0)), dim3(256), 0, s, a,
+                     wgs * grad_rpw(a.D));
+  return hipGetLastError();
+}
+
+template <class T, bool POST, bool PRE>
+hipError_t backward_width(const NormGradArgs& a, hipStream_t s) {
+  switch (grad_threads(a.D)) {
+    case 64: return backward<T, POST, PRE, 64, 1>(a, s);
+    case 256: return backward<T, POST, PRE, 256, 1>(a, s);
+    case 512: return backward<T, POST, PRE, 512, 1>(a, s);
+    default: break;
+  }
+  return a.D <= 8192 ? backward<T, POST, PRE, 1024, 1>(a, s) : backward<T, POST, PRE, 1024, 4>(a, s);
+}
+
+template <class T>
+hipError_t backward_form(const NormGradArgs& a, hipStream_t s) {
+  if (!a.h) return backward_width<T, false, true>(a, s);
+  return a.dy ? backward_width<T, true, true>(a, s) : backward_width<T, true, false>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm_forward(const NormArgs& a, bool f32, int cus, hipStream_t s) {
+  if (a.D > kMaxNormWidth) return hipErrorInvalidValue;
+  return f32 ? forward_form<float>(a, cus, s) : forward_form<uint16_t>(a, cus, s);
+}
+
+// Sets the partition of the rows and returns the bytes of `part`.
+int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus) {
+  const bool grouped = a->h && a->gate && a->gate_rows > 1;
+  a->groups = grouped ? a->T / a->gate_rows : 1;
+  const int group_rows = a->T / a->groups;
+  const int want = 4 * cus * grad_rpw(a->D) * 256 / (grad_threads(a->D) < 256 ? 256 : grad_threads(a->D));
+  a->chunks_per_gate = a->groups >= want ? 1 : ceil_div(want, a->groups);
+  a->rows_per_chunk = ceil_div(group_rows, a->chunks_per_gate);
+  a->chunks_per_gate = ceil_div(group_rows, a->rows_per_chunk);
+  a->chunks = a->groups * a->chunks_per_gate;
+  const int64_t workers = (int64_t)grad_wgs(*a) * grad_rpw(a->D);
+  return (3 * workers + (grouped && a->chunks_per_gate > 1 ? a->chunks : 0)) * (int64_t)a->D * (int64_t)sizeof(float);
+}
+
+hipError_t launch_norm_backward(const NormGradArgs& a, bool f32, hipStream_t s) {
+  if (a.D > kMaxNormWidth) return hipErrorInvalidValue;
+  return f32 ? backward_form<float>(a, s) : backward_form<uint16_t>(a, s);
+}
+
+hipError_t launch_column_sums_bf16(const float* part, uint16_t* out, int count, int D, hipStream_t s) {
+  hipLaunchKernelGGL((sk_column_sums<uint16_t>), dim3((unsigned)ceil_div(D, 32)), dim3(256), 0, s, part, out, count, D);
+  return hipGetLastError();
+}
+
+}  // namespace sk

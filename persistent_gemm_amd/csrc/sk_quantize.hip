@@ -1,0 +1,200 @@
+// The block quantiser: E4M3 codes and fp32 scales of blocks of 128 along a row, or of 128 x 128,
+// of a bf16 or fp32 matrix, of its transpose, or of both in one pass over it.
+//
+//   s = max(fl(max|x| / 448), 2^-126) over the block,   q = E4M3 nearest to x / s, ties to even.
+//
+// A workgroup takes one 128 x 128 tile: thread (tr, tc) of 16 x 16 holds rows 8 tr .. +7, columns
+// 8 tc .. +7 in registers, so a row's block is 16 neighbouring lanes (their maximum is four lane
+// rotations) and a column's block is one thread's eight rows and 16 threads, joined in LDS.  x is read once
+// for both forms.  The transposed codes go through LDS so that each column's 128 codes leave as one line.
+// The pass is bound by HBM: 2 or 4 bytes in and 1 or 2 out per element.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sk_common.h"
+#include "sk_fp8.h"
+
+namespace sk {
+
+namespace {
+
+constexpr int kPitch = 136;   // LDS bytes between two columns' transposed codes: 34 banks
+
+// Byte of 8-row piece `piece` of column c: pieces are moved by columns / 32, so that the 64 lanes of a
+// store (columns 8 apart, four pieces) meet each bank twice, which is what 512 bytes need.
+__device__ __forceinline__ int t_at(int c, int piece) { return c * kPitch + 8 * (piece ^ (4 * ((c >> 5) & 3))); }
+
+// 8 rows x 8 columns of codes (row i: w[i][0], w[i][1]) to 8 columns of 8 codes.
+__device__ __forceinline__ void transpose8(const uint32_t (&w)[8][2], uint32_t (&o)[8][2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)        // columns 4 h .. +3
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {    // rows 4 v .. +3
+      const uint32_t a = w[4 * v][h], b = w[4 * v + 1][h], c = w[4 * v + 2][h], d = w[4 * v + 3][h];
+      // perm(hi, lo): selector bytes 0-3 pick from lo, 4-7 from hi
+      const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+      const uint32_t cd0 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd1 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+      o[4 * h][v] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100u);
+      o[4 * h + 1][v] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302u);
+      o[4 * h + 2][v] = __builtin_amdgcn_perm(cd1, ab1, 0x05040100u);
+      o[4 * h + 3][v] = __builtin_amdgcn_perm(cd1, ab1, 0x07060302u);
+    }
+}
+
+// TILE: one scale per 128 x 128.  PLAIN / TRANS: which forms are written (with SUMS: perhaps neither).  SUMS: also the column sums of the
+// tile's rows, part[row block][column], in a fixed order (the first pass of a bias gradient).
+template <class T, bool TILE, bool PLAIN, bool TRANS, bool SUMS>
+__global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
+  constexpr bool COLS = TRANS && !TILE;
+  __shared__ __attribute__((aligned(16))) uint8_t codes_t[TRANS ? 128 * kPitch : 16];
+  __shared__ __attribute__((aligned(16))) uint32_t tops[COLS ? 16 : 1][128];
+  __shared__ __attribute__((aligned(16))) float col_scale[COLS ? 3 : 1][128];
+  __shared__ __attribute__((aligned(16))) float col_sum[SUMS ? 16 : 1][128];
+  const int rb = blockIdx.x / a.kb, cb = blockIdx.x - rb * a.kb;
+  const int t = threadIdx.x, tr = t >> 4, tc = t & 15;
+  const int R = a.R, C = a.C;
+  const int row0 = rb * 128 + 8 * tr, col0 = cb * 128 + 8 * tc;
+  const int n = min(8, max(0, C - col0));
+  float x[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    load8<T>((const T*)a.x + (int64_t)(row0 + i) * C + col0, row0 + i < R ? n : 0, x[i]);
+
+  if constexpr (SUMS) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float s = x[0][k];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) s += x[i][k];
+      col_sum[tr][8 * tc + k] = s;
+    }
+  }
+  if constexpr (COLS) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, f_bits(x[i][k]) & kAbs);
+      tops[tr][8 * tc + k] = m;
+    }
+  }
+  BlockScale tile;
+  if constexpr (TILE) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max(m, f_bits(x[i][k]) & kAbs);
+    m = max16(m);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    if ((t & 63) == 0) tops[0][t >> 6] = m;
+    __syncthreads();
+    m = max(max(tops[0][0], tops[0][1]), max(tops[0][2], tops[0][3]));
+    tile = Coder<T>::scale(m);
+    if (t == 0) {
+      if (PLAIN) a.scale[(int64_t)rb * a.kb + cb] = tile.s;
+      if (TRANS) a.scale_t[(int64_t)cb * a.rb + rb] = tile.s;
+    }
+  } else if constexpr (COLS || SUMS) {
+    __syncthreads();
+    if (t < 128) {
+      const int c = cb * 128 + t;
+      if constexpr (COLS) {
+        uint32_t m = tops[0][t];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) m = max(m, tops[i][t]);
+        const BlockScale b = Coder<T>::scale(m);
+        col_scale[0][t] = b.s;
+        col_scale[1][t] = b.r;
+        col_scale[2][t] = b.c;
+        if (c < C) a.scale_t[(int64_t)rb * C + c] = b.s;
+      }
+      if constexpr (SUMS) {
+        float s = col_sum[0][t];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += col_sum[i][t];
+        if (c < C) a.part[(int64_t)rb * C + c] = s;
+      }
+    }
+    if constexpr (COLS) __syncthreads();
+  }
+
+  // the rows' codes, eight bytes a lane: 16 lanes write a row's 128
+  [[maybe_unused]] uint32_t w[8][2];
+  if constexpr (PLAIN || TILE) {
+    float own = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      BlockScale b;
+      if constexpr (TILE) {
+        b = tile;
+      } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max(m, f_bits(x[i][k]) & kAbs);
+        b = Coder<T>::scale(max16(m));
+        own = tc == i ? b.s : own;
+      }
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = Coder<T>::nudged(x[i][k], b);
+      w[i][0] = codes4(v[0], v[1], v[2], v[3], b.s);
+      w[i][1] = codes4(v[4], v[5], v[6], v[7], b.s);
+      // rows hold C rounded up to 16 codes, so a piece of eight is inside or outside as a whole
+      if (PLAIN && row0 + i < R && col0 < a.pitch)
+        *(u32x2*)(a.q + (int64_t)(row0 + i) * a.pitch + col0) = u32x2{w[i][0], w[i][1]};
+    }
+    if (!TILE && tc < 8 && row0 + tc < R) a.scale[(int64_t)cb * R + row0 + tc] = own;
+  }
+
+  if constexpr (TRANS) {
+    uint32_t o[8][2];
+    if constexpr (TILE) {
+      transpose8(w, o);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const BlockScale b{col_scale[0][8 * tc + k], col_scale[1][8 * tc + k], col_scale[2][8 * tc + k]};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = Coder<T>::nudged(x[i][k], b);
+        o[k][0] = codes4(v[0], v[1], v[2], v[3], b.s);
+        o[k][1] = codes4(v[4], v[5], v[6], v[7], b.s);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) *(u32x2*)(codes_t + t_at(8 * tc + k, tr)) = u32x2{o[k][0], o[k][1]};
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = (t >> 3) + 32 * i, p = t & 7;     // column of the tile, 16 of its rows
+      const uint8_t* from = codes_t + t_at(c, 2 * p);
+      const u32x2 lo = *(const u32x2*)from, hi = *(const u32x2*)(from + 8);
+      if (cb * 128 + c < C && rb * 128 + 16 * p < a.pitch_t)
+        *(u32x4*)(a.qt + (int64_t)(cb * 128 + c) * a.pitch_t + rb * 128 + 16 * p) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+  }
+}
+
+template <class T, bool TILE, bool SUMS>
+hipError_t launch_form(const QuantArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.kb * (unsigned)a.rb), block(256);
+  if (a.q && a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, true, SUMS>), grid, block, 0, s, a);
+  else if (a.q) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, false, SUMS>), grid, block, 0, s, a);
+  else if (a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, true, SUMS>), grid, block, 0, s, a);
+  else if constexpr (SUMS) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, false, SUMS>), grid, block, 0, s, a);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_block(const QuantArgs& a, bool f32, bool tile, hipStream_t s) {
+  if (a.part) return !f32 && !tile ? launch_form<uint16_t, false, true>(a, s) : hipErrorInvalidValue;
+  if (f32) return tile ? launch_form<float, true, false>(a, s) : launch_form<float, false, false>(a, s);
+  return tile ? launch_form<uint16_t, true, false>(a, s) : launch_form<uint16_t, false, false>(a, s);
+}
+
+}  // namespace sk
