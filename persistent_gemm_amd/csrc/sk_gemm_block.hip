@@ -97,9 +97,8 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
   const int grow = wave * 8 + (lane >> 3);
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ ((grow >> 1) & 7)) * 16);
   const uint32_t lim = chunk < rb ? rb - chunk : 0u;     // k-step offsets at which the chunk lies in the row
-  uint32_t off[C::A_PT > C::B_PT ? C::A_PT : C::B_PT];
-#pragma unroll
-  for (int i = 0; i < (C::A_PT > C::B_PT ? C::A_PT : C::B_PT); ++i) off[i] = (uint32_t)(grow + i * C::NW * 8) * rb + chunk;
+  const uint32_t off = (uint32_t)grow * rb + chunk;
+  const uint32_t gstep = (uint32_t)(C::NW * 8) * rb;     // to the wave's next group, in the scalar offset
 
   // The lane's operand chunks 2 lg, 2 lg + 1 of row lr of each 16-row block.
   const int sw = (lr >> 1) & 7;
@@ -128,21 +127,24 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     const uint32_t svoff = s_is_a ? (e < rows ? (uint32_t)e * 4u : kOob)
                          : j >= cols ? kOob : (uint32_t)(BROW ? j : (nb + j) / kBlock * g.kb) * 4u;
 
-    // k-step d into stage d % STAGES; past the last one every lane is out of range (zeros, no traffic)
-    auto issue = [&](int d) {
+    // Load l of k-step d into stage d % STAGES; past the last one every lane is out of range (zeros, no traffic).
+    auto issue_one = [&](int d, auto lc) {
+      constexpr int l = decltype(lc)::value;
       const uint32_t stage = (uint32_t)(uintptr_t)smem + (uint32_t)(d % C::STAGES) * C::STAGE;
-      const uint32_t kbyte = (uint32_t)d * kBlock;
       const bool live = d < g.kb;
+      const uint32_t kbyte = live ? (uint32_t)d * kBlock : 0u;
       const bool in = live && kbyte < lim;
-#pragma unroll
-      for (int i = 0; i < C::A_PT; ++i)
-        dma_load16(ra, in ? off[i] : kOob, live ? kbyte : 0u, stage + (uint32_t)(wave + i * C::NW) * 1024u);
-#pragma unroll
-      for (int i = 0; i < C::B_PT; ++i)
-        dma_load16(rbw, in ? off[i] : kOob, live ? kbyte : 0u, stage + C::B_OFF + (uint32_t)(wave + i * C::NW) * 1024u);
-      const v4u rs = uniform(rsrc_words(sbase + (live ? d : 0) * sstep, sbytes));
-      dma_load4(rs, live ? svoff : kOob, 0u, stage + C::S_OFF + (uint32_t)sidx * 256u);
+      if constexpr (l < C::A_PT) {
+        dma_load16(ra, in ? off : kOob, kbyte + l * gstep, stage + (uint32_t)(wave + l * C::NW) * 1024u);
+      } else if constexpr (l < C::A_PT + C::B_PT) {
+        constexpr int i = l - C::A_PT;
+        dma_load16(rbw, in ? off : kOob, kbyte + i * gstep, stage + C::B_OFF + (uint32_t)(wave + i * C::NW) * 1024u);
+      } else {
+        const v4u rs = uniform(rsrc_words(sbase + (live ? d : 0) * sstep, sbytes));
+        dma_load4(rs, live ? svoff : kOob, 0u, stage + C::S_OFF + (uint32_t)sidx * 256u);
+      }
     };
+    auto issue = [&](int d) { static_for<C::PER_STAGE>([&](auto lc) { issue_one(d, lc); }); };
 
     v4f acc[C::FM][C::FN];
 #pragma unroll
@@ -150,42 +152,83 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{};
 
+    // The k-steps as one stream.  Slot n = j FM + i of a k-step starts block (i, j)'s MFMA and adds the result of
+    // slot n - LAG, so the ALU never waits for the MFMA just started.  B's fragments go round a ring of RING
+    // registers sets, read DIST columns of blocks ahead; A's are refilled in place after their last use.  At
+    // column JB every read of the stage has been issued: there the waves wait for the next stage's loads
+    // (a whole k-step old) and meet, the loads of the stage after go out into the one just read, and
+    // the reads run on into the next stage.  sched_barrier(0) keeps the slots in this order.
+    constexpr int RING = C::FN < 4 || C::FM * C::FN > 16 ? 2 : 4, DIST = RING / 2, JB = C::FN - DIST, LAG = 2, NS = C::FM * C::FN;
+    v4u a[C::FM][2], b[RING][2];
+    v4f sbv[RING];                 // (BROW) the four columns' scales
+    float sa[C::FM], sbt = 0.0f;
+    auto stage_of = [&](int d) -> const lds_u8* { return smem + (uint32_t)(d % C::STAGES) * C::STAGE; };
+    auto read_a = [&](const lds_u8* st, auto ic) {
+      constexpr int i = decltype(ic)::value;
+      a[i][0] = ld_v4u(st + arow + i * 16 * kBlock + c0);
+      a[i][1] = ld_v4u(st + arow + i * 16 * kBlock + c1);
+    };
+    auto read_b = [&](const lds_u8* st, auto jc) {
+      constexpr int j = decltype(jc)::value;
+      b[j % RING][0] = ld_v4u(st + brow + j * 16 * kBlock + c0);
+      b[j % RING][1] = ld_v4u(st + brow + j * 16 * kBlock + c1);
+      if constexpr (BROW) sbv[j % RING] = ld_v4f(st + C::S_OFF + (C::BM + wn * C::WTN + j * 16 + 4 * lg) * 4);
+    };
+    auto read_scales = [&](const lds_u8* st) {
 #pragma unroll
-    for (int d = 0; d < C::STAGES - 1; ++d) issue(d);
-    for (int d = 0; d < g.kb; ++d) {
-      // stage d has landed (at most the later stages' loads are in flight), and stage d - 1 is read by all
-      wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE>();
-      lds_barrier();
-      issue(d + C::STAGES - 1);
-      const lds_u8* const st = smem + (d % C::STAGES) * C::STAGE;
-      v4u a[C::FM][2];
-      float sa[C::FM];
-#pragma unroll
-      for (int i = 0; i < C::FM; ++i) {
-        a[i][0] = ld_v4u(st + arow + i * 16 * kBlock + c0);
-        a[i][1] = ld_v4u(st + arow + i * 16 * kBlock + c1);
+      for (int i = 0; i < C::FM; ++i)
         sa[i] = *(const __attribute__((address_space(3))) float*)(st + C::S_OFF + (wm * C::WTM + i * 16 + lr) * 4);
-      }
-      if constexpr (!BROW) {
-        const float sb = *(const __attribute__((address_space(3))) float*)(st + C::S_OFF + (C::BM + wn * C::WTN) * 4);
+      if constexpr (!BROW) sbt = *(const __attribute__((address_space(3))) float*)(st + C::S_OFF + (C::BM + wn * C::WTN) * 4);
+    };
+
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) sa[i] *= sb;
-      }
+    for (int d = 0; d < C::STAGES; ++d) issue(d);
+    wait_vmcnt_n<(C::STAGES - 1) * C::PER_STAGE>();
+    lds_barrier();
+    read_scales(smem);
+    static_for<C::FM>([&](auto ic) { read_a(smem, ic); });
+    static_for<DIST>([&](auto jc) { read_b(smem, jc); });
+    for (int d = 0; d < g.kb; ++d) {
+      const lds_u8* const st = stage_of(d);
+      const lds_u8* const nx = stage_of(d + 1);
+      float s[C::FM];
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        v4u b[2];
-        b[0] = ld_v4u(st + brow + j * 16 * kBlock + c0);
-        b[1] = ld_v4u(st + brow + j * 16 * kBlock + c1);
-        v4f sb;
-        if constexpr (BROW) sb = ld_v4f(st + C::S_OFF + (C::BM + wn * C::WTN + j * 16 + 4 * lg) * 4);
+      for (int i = 0; i < C::FM; ++i) s[i] = BROW ? sa[i] : sa[i] * sbt;
+      v4f p[LAG + 1], sk[LAG + 1];
+      auto add = [&](auto nc) {
+        constexpr int n = decltype(nc)::value, i = n % C::FM, j = n / C::FM;
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-          const v4f p = block_mfma(b, a[i]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            acc[i][j][k] = __builtin_fmaf(BROW ? sa[i] * sb[k] : sa[i], p[k], acc[i][j][k]);
+        for (int k = 0; k < 4; ++k)
+          acc[i][j][k] = __builtin_fmaf(BROW ? sk[n % (LAG + 1)][k] : s[i], p[n % (LAG + 1)][k], acc[i][j][k]);
+      };
+      static_for<NS>([&](auto nc) {
+        constexpr int n = decltype(nc)::value, i = n % C::FM, j = n / C::FM;
+        if constexpr (i == 0 && j == JB) {
+          wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE>();
+          lds_barrier();
         }
-      }
+        if constexpr (i == 0) {
+          if constexpr (j < JB) read_b(st, std::integral_constant<int, j + DIST>{});
+          else read_b(nx, std::integral_constant<int, j - JB>{});
+        }
+        p[n % (LAG + 1)] = block_mfma(b[j % RING], a[i]);
+        if constexpr (BROW) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sk[n % (LAG + 1)][k] = s[i] * sbv[j % RING][k];
+        }
+        if constexpr (j == C::FN - 1) read_a(nx, std::integral_constant<int, i>{});
+        if constexpr (n >= LAG) add(std::integral_constant<int, n - LAG>{});
+        if constexpr (j >= JB) {
+          constexpr int q = n - JB * C::FM, QN = DIST * C::FM;   // this slot's share of the next loads
+          static_for<C::PER_STAGE>([&](auto lc) {
+            constexpr int l = decltype(lc)::value;
+            if constexpr (l * QN / C::PER_STAGE == q) issue_one(d + C::STAGES, lc);
+          });
+        }
+        if constexpr (n == NS - 1) read_scales(nx);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      static_for<LAG>([&](auto lc) { add(std::integral_constant<int, NS - LAG + decltype(lc)::value>{}); });
     }
 
     // outputs: each wave's through its own part of LDS, so that a store fills whole lines
