@@ -57,12 +57,11 @@ __device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int* tm
   *tm = band * GROUP + (in - *tn * rows);
 }
 
-// Words that are the same in every lane, said so (the compiler keeps 64-bit products in vector registers).
-__device__ __forceinline__ v4u uniform(const v4u& x) {
-  v4u r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = (uint32_t)__builtin_amdgcn_readfirstlane((int)x[i]);
-  return r;
+// A value that is the same in every lane, said so (a choice between 64-bit values goes to vector registers otherwise).
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
 // One block's inner products, transposed as elsewhere here (B first): lane l gets A row l % 16 and the four
@@ -100,9 +99,12 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
   const uint32_t off = (uint32_t)grow * rb + chunk;
   const uint32_t gstep = (uint32_t)(C::NW * 8) * rb;     // to the wave's next group, in the scalar offset
 
-  // The lane's operand chunks 2 lg, 2 lg + 1 of row lr of each 16-row block.
+  // The lane's operand chunks lg and 4 + lg of row lr of each 16-row block.  (Any four a half will do that are the
+  // same for A and B; a 16-byte read serves lanes 0-3, 12-15, 20-23 and 24-27 together, then the four other
+  // quads, so lane groups 0 and 1 have to differ in the chunk's lowest bit: chunks 2 lg, 2 lg + 1 met
+  // every bank twice.)
   const int sw = (lr >> 1) & 7;
-  const int c0 = ((2 * lg) ^ sw) * 16, c1 = ((2 * lg + 1) ^ sw) * 16;
+  const int c0 = (lg ^ sw) * 16, c1 = ((4 + lg) ^ sw) * 16;
   const int arow = (wm * C::WTM + lr) * kBlock, brow = C::B_OFF + (wn * C::WTN + lr) * kBlock;
 
   const int sidx = wave % C::S_INST;         // (waves past the last load repeat one: the same bytes to the same place)
@@ -122,26 +124,28 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     // whose scale is their own or that of their 128 columns.  k-step d's are sstep floats after the last one's.
     const int e = sidx * 64 + lane, j = e - C::BM, nb = n0 % kBlock;
     const float* const sbase = s_is_a ? g.SA + m0 : BROW ? g.SB + n0 : g.SB + (int64_t)(n0 / kBlock) * g.kb;
-    const int64_t sstep = s_is_a ? g.M : BROW ? g.N : 1;
-    const uint32_t sbytes = (uint32_t)(s_is_a ? rows : BROW ? cols : g.kb * ((nb + cols - 1) / kBlock + 1)) * 4u;
+    const int64_t sstep = 4 * uniform(s_is_a ? g.M : BROW ? g.N : 1);
+    const uint32_t sbytes = (uint32_t)uniform(s_is_a ? rows : BROW ? cols : g.kb * ((nb + cols - 1) / kBlock + 1)) * 4u;
     const uint32_t svoff = s_is_a ? (e < rows ? (uint32_t)e * 4u : kOob)
                          : j >= cols ? kOob : (uint32_t)(BROW ? j : (nb + j) / kBlock * g.kb) * 4u;
 
     // Load l of k-step d into stage d % STAGES; past the last one every lane is out of range (zeros, no traffic).
+    // (The k-steps are issued in order: sat is the step's scales, advanced with its last load.)
+    int64_t sat = uniform((int64_t)(uintptr_t)sbase);
     auto issue_one = [&](int d, auto lc) {
       constexpr int l = decltype(lc)::value;
       const uint32_t stage = (uint32_t)(uintptr_t)smem + (uint32_t)(d % C::STAGES) * C::STAGE;
       const bool live = d < g.kb;
       const uint32_t kbyte = live ? (uint32_t)d * kBlock : 0u;
-      const bool in = live && kbyte < lim;
+      const uint32_t voff = live && kbyte < lim ? off : kOob;
       if constexpr (l < C::A_PT) {
-        dma_load16(ra, in ? off : kOob, kbyte + l * gstep, stage + (uint32_t)(wave + l * C::NW) * 1024u);
+        dma_load16(ra, voff, kbyte + l * gstep, stage + (uint32_t)(wave + l * C::NW) * 1024u);
       } else if constexpr (l < C::A_PT + C::B_PT) {
         constexpr int i = l - C::A_PT;
-        dma_load16(rbw, in ? off : kOob, kbyte + i * gstep, stage + C::B_OFF + (uint32_t)(wave + i * C::NW) * 1024u);
+        dma_load16(rbw, voff, kbyte + i * gstep, stage + C::B_OFF + (uint32_t)(wave + i * C::NW) * 1024u);
       } else {
-        const v4u rs = uniform(rsrc_words(sbase + (live ? d : 0) * sstep, sbytes));
-        dma_load4(rs, live ? svoff : kOob, 0u, stage + C::S_OFF + (uint32_t)sidx * 256u);
+        dma_load4(rsrc_words((const void*)(uintptr_t)sat, sbytes), live ? svoff : kOob, 0u, stage + C::S_OFF + (uint32_t)sidx * 256u);
+        sat += live ? sstep : 0;
       }
     };
     auto issue = [&](int d) { static_for<C::PER_STAGE>([&](auto lc) { issue_one(d, lc); }); };
@@ -152,14 +156,19 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{};
 
-    // The k-steps as one stream.  Slot n = j FM + i of a k-step starts block (i, j)'s MFMA and adds the result of
-    // slot n - LAG, so the ALU never waits for the MFMA just started.  B's fragments go round a ring of RING
-    // registers sets, read DIST columns of blocks ahead; A's are refilled in place after their last use.  At
-    // column JB every read of the stage has been issued: there the waves wait for the next stage's loads
-    // (a whole k-step old) and meet, the loads of the stage after go out into the one just read, and
-    // the reads run on into the next stage.  sched_barrier(0) keeps the slots in this order.
-    constexpr int RING = C::FN < 4 || C::FM * C::FN > 16 ? 2 : 4, DIST = RING / 2, JB = C::FN - DIST, LAG = 2, NS = C::FM * C::FN;
-    v4u a[C::FM][2], b[RING][2];
+    // The k-steps as one stream of FM x FN slots, each starting a block's MFMA and adding the result of LAG slots
+    // before, so that the ALU does not wait for the MFMA just started.  Columns of blocks go in pairs,
+    // (i, j), (i, j + 1), (i + 1, j), ...: A's fragment i is used twice in a row, which spreads its refill for
+    // the next stage (in place, after its last use) over the whole last pair of a k-step, and its first
+    // use there over the whole first pair.  B's fragments go round a ring of two pairs, each read
+    // during the pair before.  At the last pair every read of the stage has been issued: there the
+    // waves wait for the next stage's loads (a whole k-step old) and meet, the loads of the stage after
+    // go out into the one just read, and the reads run on into the next stage.  sched_barrier(0) keeps the
+    // slots, and each MFMA before its slot's fmas, in this order.
+    constexpr int NP = C::FN / 2, PS = 2 * C::FM, NS = C::FM * C::FN, LAG = 2;   // pairs; slots of a pair, of a k-step
+    constexpr int RING = NP == 1 ? 2 : 4;
+    static_assert(C::FN % 2 == 0 && (NP == 1 || NP % 2 == 0) && C::FM >= 2, "pairs of columns");
+    v4u a[C::FM][2], b[RING][2];   // column j in b[j % RING]
     v4f sbv[RING];                 // (BROW) the four columns' scales
     float sa[C::FM], sbt = 0.0f;
     auto stage_of = [&](int d) -> const lds_u8* { return smem + (uint32_t)(d % C::STAGES) * C::STAGE; };
@@ -187,48 +196,46 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     lds_barrier();
     read_scales(smem);
     static_for<C::FM>([&](auto ic) { read_a(smem, ic); });
-    static_for<DIST>([&](auto jc) { read_b(smem, jc); });
+    static_for<2>([&](auto jc) { read_b(smem, jc); });
     for (int d = 0; d < g.kb; ++d) {
       const lds_u8* const st = stage_of(d);
       const lds_u8* const nx = stage_of(d + 1);
       float s[C::FM];
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) s[i] = BROW ? sa[i] : sa[i] * sbt;
-      v4f p[LAG + 1], sk[LAG + 1];
+      v4f p[LAG + 1];
       auto add = [&](auto nc) {
-        constexpr int n = decltype(nc)::value, i = n % C::FM, j = n / C::FM;
+        constexpr int n = decltype(nc)::value, i = n % PS / 2, j = n / PS * 2 + n % 2;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          acc[i][j][k] = __builtin_fmaf(BROW ? sk[n % (LAG + 1)][k] : s[i], p[n % (LAG + 1)][k], acc[i][j][k]);
+          acc[i][j][k] = __builtin_fmaf(BROW ? s[i] * sbv[j % RING][k] : s[i], p[n % (LAG + 1)][k], acc[i][j][k]);
       };
       static_for<NS>([&](auto nc) {
-        constexpr int n = decltype(nc)::value, i = n % C::FM, j = n / C::FM;
-        if constexpr (i == 0 && j == JB) {
+        constexpr int n = decltype(nc)::value, r = n % PS, i = r / 2, pair = n / PS, j = pair * 2 + n % 2;
+        if constexpr (r == 0 && pair == NP - 1) {
           wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE>();
           lds_barrier();
-        }
-        if constexpr (i == 0) {
-          if constexpr (j < JB) read_b(st, std::integral_constant<int, j + DIST>{});
-          else read_b(nx, std::integral_constant<int, j - JB>{});
+          read_scales(nx);   // (first: everything read later may still be on its way when the next k-step starts)
         }
         p[n % (LAG + 1)] = block_mfma(b[j % RING], a[i]);
-        if constexpr (BROW) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sk[n % (LAG + 1)][k] = s[i] * sbv[j % RING][k];
-        }
-        if constexpr (j == C::FN - 1) read_a(nx, std::integral_constant<int, i>{});
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (n >= LAG) add(std::integral_constant<int, n - LAG>{});
-        if constexpr (j >= JB) {
-          constexpr int q = n - JB * C::FM, QN = DIST * C::FM;   // this slot's share of the next loads
+        // the next pair's columns, once the last pair's are done with (a stage of one pair: in place)
+        if constexpr (NP > 1 && (r == 2 || r == 3)) {
+          if constexpr (pair < NP - 1) read_b(st, std::integral_constant<int, j + 2>{});
+          else read_b(nx, std::integral_constant<int, j % 2>{});
+        }
+        if constexpr (pair == NP - 1) {
+          if constexpr (n % 2 == 1) read_a(nx, std::integral_constant<int, i>{});
           static_for<C::PER_STAGE>([&](auto lc) {
             constexpr int l = decltype(lc)::value;
-            if constexpr (l * QN / C::PER_STAGE == q) issue_one(d + C::STAGES, lc);
+            if constexpr (l * PS / C::PER_STAGE == r) issue_one(d + C::STAGES, lc);
           });
         }
-        if constexpr (n == NS - 1) read_scales(nx);
         __builtin_amdgcn_sched_barrier(0);
       });
       static_for<LAG>([&](auto lc) { add(std::integral_constant<int, NS - LAG + decltype(lc)::value>{}); });
+      if constexpr (NP == 1) static_for<2>([&](auto jc) { read_b(nx, jc); });
     }
 
     // outputs: each wave's through its own part of LDS, so that a store fills whole lines
