@@ -104,8 +104,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
   // quads, so lane groups 0 and 1 have to differ in the chunk's lowest bit: chunks 2 lg, 2 lg + 1 met
   // every bank twice.)
   const int sw = (lr >> 1) & 7;
-  const int c0 = (lg ^ sw) * 16, c1 = ((4 + lg) ^ sw) * 16;
-  const int arow = (wm * C::WTM + lr) * kBlock, brow = C::B_OFF + (wn * C::WTN + lr) * kBlock;
+  const int c0 = (lg ^ sw) * 16;
 
   const int sidx = wave % C::S_INST;         // (waves past the last load repeat one: the same bytes to the same place)
   const bool s_is_a = sidx < C::BM / 64;
@@ -171,35 +170,38 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     v4u a[C::FM][2], b[RING][2];   // column j in b[j % RING]
     v4f sbv[RING];                 // (BROW) the four columns' scales
     float sa[C::FM], sbt = 0.0f;
-    auto stage_of = [&](int d) -> const lds_u8* { return smem + (uint32_t)(d % C::STAGES) * C::STAGE; };
-    auto read_a = [&](const lds_u8* st, auto ic) {
+    // LDS addresses in the stage being read, moved on behind each barrier.  (Chunk 4 + lg is 64 bytes from chunk lg,
+    // with the sign of one of the permutation's bits: an exclusive or, since rows are 128 bytes.)
+    const uint32_t base = (uint32_t)(uintptr_t)smem;
+    uint32_t la = base + (wm * C::WTM + lr) * kBlock + c0, lb = base + C::B_OFF + (wn * C::WTN + lr) * kBlock + c0;
+    uint32_t lsa = base + C::S_OFF + (wm * C::WTM + lr) * 4;
+    uint32_t lsb = base + C::S_OFF + (C::BM + wn * C::WTN + (BROW ? 4 * lg : 0)) * 4;
+    auto at = [](uint32_t x) { return (const lds_u8*)(uintptr_t)x; };
+    auto read_a = [&](auto ic) {
       constexpr int i = decltype(ic)::value;
-      a[i][0] = ld_v4u(st + arow + i * 16 * kBlock + c0);
-      a[i][1] = ld_v4u(st + arow + i * 16 * kBlock + c1);
+      a[i][0] = ld_v4u(at(la) + i * 16 * kBlock);
+      a[i][1] = ld_v4u(at(la ^ 64u) + i * 16 * kBlock);
     };
-    auto read_b = [&](const lds_u8* st, auto jc) {
+    auto read_b = [&](auto jc) {
       constexpr int j = decltype(jc)::value;
-      b[j % RING][0] = ld_v4u(st + brow + j * 16 * kBlock + c0);
-      b[j % RING][1] = ld_v4u(st + brow + j * 16 * kBlock + c1);
-      if constexpr (BROW) sbv[j % RING] = ld_v4f(st + C::S_OFF + (C::BM + wn * C::WTN + j * 16 + 4 * lg) * 4);
+      b[j % RING][0] = ld_v4u(at(lb) + j * 16 * kBlock);
+      b[j % RING][1] = ld_v4u(at(lb ^ 64u) + j * 16 * kBlock);
+      if constexpr (BROW) sbv[j % RING] = ld_v4f(at(lsb) + j * 64);
     };
-    auto read_scales = [&](const lds_u8* st) {
+    auto read_scales = [&]() {
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i)
-        sa[i] = *(const __attribute__((address_space(3))) float*)(st + C::S_OFF + (wm * C::WTM + i * 16 + lr) * 4);
-      if constexpr (!BROW) sbt = *(const __attribute__((address_space(3))) float*)(st + C::S_OFF + (C::BM + wn * C::WTN) * 4);
+      for (int i = 0; i < C::FM; ++i) sa[i] = *(const __attribute__((address_space(3))) float*)(at(lsa) + i * 64);
+      if constexpr (!BROW) sbt = *(const __attribute__((address_space(3))) float*)at(lsb);
     };
 
 #pragma unroll
     for (int d = 0; d < C::STAGES; ++d) issue(d);
     wait_vmcnt_n<(C::STAGES - 1) * C::PER_STAGE>();
     lds_barrier();
-    read_scales(smem);
-    static_for<C::FM>([&](auto ic) { read_a(smem, ic); });
-    static_for<2>([&](auto jc) { read_b(smem, jc); });
+    read_scales();
+    static_for<C::FM>(read_a);
+    static_for<2>(read_b);
     for (int d = 0; d < g.kb; ++d) {
-      const lds_u8* const st = stage_of(d);
-      const lds_u8* const nx = stage_of(d + 1);
       float s[C::FM];
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) s[i] = BROW ? sa[i] : sa[i] * sbt;
@@ -215,18 +217,22 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
         if constexpr (r == 0 && pair == NP - 1) {
           wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE>();
           lds_barrier();
-          read_scales(nx);   // (first: everything read later may still be on its way when the next k-step starts)
+          const uint32_t move = (uint32_t)((d + 1) % C::STAGES ? C::STAGE : -(C::STAGES - 1) * C::STAGE);
+          la += move;
+          lb += move;
+          lsa += move;
+          lsb += move;
+          read_scales();   // (first: everything read later may still be on its way when the next k-step starts)
         }
         p[n % (LAG + 1)] = block_mfma(b[j % RING], a[i]);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (n >= LAG) add(std::integral_constant<int, n - LAG>{});
         // the next pair's columns, once the last pair's are done with (a stage of one pair: in place)
         if constexpr (NP > 1 && (r == 2 || r == 3)) {
-          if constexpr (pair < NP - 1) read_b(st, std::integral_constant<int, j + 2>{});
-          else read_b(nx, std::integral_constant<int, j % 2>{});
+          read_b(std::integral_constant<int, (j + 2) % C::FN>{});
         }
         if constexpr (pair == NP - 1) {
-          if constexpr (n % 2 == 1) read_a(nx, std::integral_constant<int, i>{});
+          if constexpr (n % 2 == 1) read_a(std::integral_constant<int, i>{});
           static_for<C::PER_STAGE>([&](auto lc) {
             constexpr int l = decltype(lc)::value;
             if constexpr (l * PS / C::PER_STAGE == r) issue_one(d + C::STAGES, lc);
@@ -235,18 +241,22 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
         __builtin_amdgcn_sched_barrier(0);
       });
       static_for<LAG>([&](auto lc) { add(std::integral_constant<int, NS - LAG + decltype(lc)::value>{}); });
-      if constexpr (NP == 1) static_for<2>([&](auto jc) { read_b(nx, jc); });
+      if constexpr (NP == 1) static_for<2>(read_b);
     }
 
-    // outputs: each wave's through its own part of LDS, so that a store fills whole lines
+    // outputs: each wave's through its own part of LDS, so that a store fills whole lines.  (The lane is read
+    // afresh: offsets worked out from it would otherwise be kept, in spilled registers, through every k-step.)
     wait_vmcnt_n<0>();
     lds_barrier();
+    int ol = lane;
+    asm volatile("" : "+v"(ol));
+    const int olr = ol & 15, olg = ol >> 4;
     const __amdgpu_buffer_rsrc_t rc = make_rsrc(g.C + (int64_t)m0 * g.N, (uint32_t)rows * (uint32_t)g.N * 2u);
     const bool staged = (g.N & 7) == 0;
     lds_u8* const so = smem + wave * C::OUT_WAVE;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
-      const int col = n0 + wn * C::WTN + j * 16 + 4 * lg;
+      const int col = n0 + wn * C::WTN + j * 16 + 4 * olg;
       float bias[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -254,29 +264,29 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) {
         const v2u h = out4(acc[i][j], bias);
-        const int row = i * 16 + lr;
+        const int row = i * 16 + olr;
         if (staged) {
-          const int c = (2 * j + (lg >> 1)) ^ (row & (C::CH - 1));
-          *(__attribute__((address_space(3))) v2u*)(so + row * (C::WTN * 2) + c * 16 + (lg & 1) * 8) = h;
+          const int c = (2 * j + (olg >> 1)) ^ (row & (C::CH - 1));
+          *(__attribute__((address_space(3))) v2u*)(so + row * (C::WTN * 2) + c * 16 + (olg & 1) * 8) = h;
         } else {
-          const uint32_t at = ((uint32_t)(wm * C::WTM + row) * (uint32_t)g.N + (uint32_t)col) * 2u;
+          const uint32_t to = ((uint32_t)(wm * C::WTM + row) * (uint32_t)g.N + (uint32_t)col) * 2u;
           const uint32_t v[4] = {h[0] & 0xffffu, h[0] >> 16, h[1] & 0xffffu, h[1] >> 16};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v[k], rc, col + k < g.N ? at + 2u * k : kOob, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v[k], rc, col + k < g.N ? to + 2u * k : kOob, 0, 0);
         }
       }
     }
     if (staged) {
       asm volatile("" ::: "memory");   // (one wave's LDS operations execute in order)
       constexpr int RPI = 64 / C::CH;  // rows per store
+      const int c = ol % C::CH, col = n0 + wn * C::WTN + c * 8;
+      const uint32_t to = ((uint32_t)(wm * C::WTM + ol / C::CH) * (uint32_t)g.N + (uint32_t)col) * 2u;
 #pragma unroll
       for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
-        const int row = r0 + lane / C::CH, c = lane % C::CH;
+        const int row = r0 + ol / C::CH;
         const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
-        const int col = n0 + wn * C::WTN + c * 8;
-        const uint32_t at = ((uint32_t)(wm * C::WTM + row) * (uint32_t)g.N + (uint32_t)col) * 2u;
-        __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < g.N ? at : kOob, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < g.N ? to + (uint32_t)r0 * (uint32_t)g.N * 2u : kOob, 0, 0);
       }
     }
     if (t + (int)gridDim.x < T) lds_barrier();   // the next tile's loads go where the outputs were read from
