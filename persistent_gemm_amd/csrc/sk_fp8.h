@@ -28,38 +28,67 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), b2));
 }
 
-// Eight consecutive elements of a row as floats.  n: how many of them lie inside the row (the rest are 0).
+// Eight consecutive elements of a row as they lie in memory: what a load in flight occupies.
 template <class T>
-__device__ __forceinline__ void load8(const T* __restrict__ p, int n, float (&x)[8]);
+struct Raw8 {
+  u32x4 w[sizeof(T) / 2];
+};
 
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t* __restrict__ p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    const u32x4 v = *(const u32x4_any*)p;
+// Elements col .. col + 7 of a row of D.  Past D - 8 the last eight are loaded instead, to be moved into place by
+// settle8 once they are needed: a branch around the load would make every later load wait for this one.  The
+// column is an unsigned 32-bit offset from an address that all lanes share.  SHORT: D < 8, element by element.
+template <bool SHORT, class T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* __restrict__ row, int col, int D) {
+  Raw8<T> r;
+  if constexpr (!SHORT) {
+    const T* const p = row + (uint32_t)min(col, D - 8);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_lo(v[i]);
-      x[2 * i + 1] = bf16_hi(v[i]);
-    }
+    for (unsigned i = 0; i < sizeof(T) / 2; ++i) r.w[i] = *(const u32x4_any*)(p + 8 / (sizeof(T) / 2) * i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n ? bits_f((uint32_t)p[i] << 16) : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      const bool in = col + i < D;
+      if constexpr (sizeof(T) == 4) {
+        r.w[i / 4][i % 4] = in ? f_bits(row[col + i]) : 0u;
+      } else {
+        const uint32_t x = in ? (uint32_t)row[col + i] : 0u;
+        if (i % 2 == 0) r.w[0][i / 2] = x;
+        else r.w[0][i / 2] |= x << 16;
+      }
+    }
+  }
+  return r;
+}
+
+// The loaded elements moved to their places, zeros behind the row's end.
+template <bool SHORT, class T>
+__device__ __forceinline__ void settle8(Raw8<T>& r, int col, int D) {
+  if constexpr (!SHORT) {
+    const int s = col - (D - 8);     // how far back they were taken
+    if (s > 0) {
+      constexpr int W = 2 * sizeof(T);   // words
+      uint32_t x[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = s < 8 ? r.w[i / 4][i % 4] : 0u;
+      constexpr int PER = 4 / sizeof(T);   // elements of a word
+#pragma unroll
+      for (int h = 4; h >= PER; h /= 2)
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = s & h ? (i + h / PER < W ? x[i + h / PER] : 0u) : x[i];
+      if constexpr (PER == 2) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = s & 1 ? (x[i] >> 16) | (i + 1 < W ? x[i + 1] << 16 : 0u) : x[i];
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) r.w[i / 4][i % 4] = x[i];
+    }
   }
 }
 
-template <>
-__device__ __forceinline__ void load8<float>(const float* __restrict__ p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    const u32x4 a = *(const u32x4_any*)p, b = *(const u32x4_any*)(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = bits_f(a[i]);
-      x[4 + i] = bits_f(b[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n ? p[i] : 0.0f;
-  }
+template <class T>
+__device__ __forceinline__ float raw_at(const Raw8<T>& r, int i) {
+  if constexpr (sizeof(T) == 4) return bits_f(r.w[i / 4][i % 4]);
+  else return i % 2 ? bf16_hi(r.w[0][i / 2]) : bf16_lo(r.w[0][i / 2]);
 }
 
 // Stores the first n of eight values, rounded to the element type.

@@ -42,62 +42,137 @@ __device__ __forceinline__ float row_sum(float x, float (*red)[16], int& turn) {
 template <int TPR>
 constexpr int rows_per_wg() { return TPR == 64 ? 4 : 1; }
 
+// Column `col` of the row at p: p is the same in every lane and the column an unsigned 32-bit offset, which is one
+// register for all of a row's tensors (instead of a 64-bit address for each).
+template <class T>
+__device__ __forceinline__ T* at_col(T* p, int col) { return p + (uint32_t)col; }
+
+// The thread's row of the workgroup's, the same for a whole wave.
+template <int TPR>
+__device__ __forceinline__ int sub_row() { return TPR == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0; }
+
+// One piece of eight of each of a row's CH.
+template <class T, int CH>
+struct RawRow {
+  Raw8<T> c[CH];
+};
+// Row `row` of base, asked for; settle_row() where it is first used.  (base is the same in every lane, NULL for none)
+template <bool SHORT, class T, int TPR, int CH>
+__device__ __forceinline__ RawRow<T, CH> load_row(const void* base, int row, int t, int D) {
+  RawRow<T, CH> r = {};
+  if (base) {
+    const T* const p = (const T*)base + (int64_t)row * D;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) r.c[c] = load_raw8<SHORT>(p, 8 * (t + c * TPR), D);
+  }
+  return r;
+}
+template <bool SHORT, int TPR, class T, int CH>
+__device__ __forceinline__ void settle_row(RawRow<T, CH>& r, int t, int D) {
+#pragma unroll
+  for (int c = 0; c < CH; ++c) settle8<SHORT>(r.c[c], 8 * (t + c * TPR), D);
+}
+
+// Has the row unpacked again where it is next used, instead of kept as floats from before: twice the registers.
+template <class T, int CH>
+__device__ __forceinline__ void repack(RawRow<T, CH>& r) {
+  if constexpr (sizeof(T) == 2 && CH > 1) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) asm volatile("" : "+v"(r.c[c].w[0]));
+  }
+}
+
 // ---------------------------------------------------------------- forward
 
-template <class T, bool POST, bool PRE, bool FP8, int TPR, int CH>
+// A workgroup takes consecutive rows (a wave of four: every fourth of them).  Each row's tensors are asked for one
+// row ahead and kept as they lie in memory, and the vectors shared by the rows stay in registers where they
+// fit (HOLD), so that the two sums of a row, which wait for all its threads, do not wait for memory.
+// The scales of eight rows leave together: one row's are T apart, 4 bytes in a line each.
+template <class T, bool POST, bool PRE, bool FP8, int TPR, int CH, bool SHORT>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_forward(NormArgs a) {
-  __shared__ float red[2][16];
-  int turn = 0;
   constexpr int RPW = rows_per_wg<TPR>();
+  constexpr bool HOLD = CH * sizeof(T) <= 4, AHEAD = CH < 4;   // (a wide row's registers hold little else)
+  constexpr bool BATCH = FP8 && TPR > 64;
+  constexpr int ROWS = 8;                       // rows whose scales leave together
+  constexpr int BLOCKS = BATCH ? TPR * CH / 16 : 1;
+  __shared__ float red[2][16];
+  __shared__ float scales[BLOCKS][ROWS + 1];
+  int turn = 0;
   const int t = threadIdx.x % TPR, D = a.D;
   const float inv = 1.0f / (float)D;
-  for (int row = blockIdx.x * RPW + threadIdx.x / TPR; row < a.T; row += gridDim.x * RPW) {
+  const int first = (int)((int64_t)a.T * blockIdx.x / gridDim.x), last = (int)((int64_t)a.T * (blockIdx.x + 1) / gridDim.x);
+  typedef RawRow<T, CH> Row;
+  auto load = [&](const void* p, int row) { return load_row<SHORT, T, TPR, CH>(p, row, t, D); };
+  auto settle = [&](Row& r) { settle_row<SHORT, TPR>(r, t, D); };
+
+  Row w, rs, nw;
+  auto load_post = [&]() {
+    w = load(a.weight, 0);
+    rs = load(a.residual_scale, 0);
+    settle(w);
+    settle(rs);
+  };
+  auto load_pre = [&]() {
+    nw = load(a.next_weight, 0);
+    settle(nw);
+  };
+  if constexpr (HOLD && POST) load_post();
+  if constexpr (HOLD && PRE) load_pre();
+  int row = first + sub_row<TPR>();
+  Row x0, h0;
+  // (past the last row, the last one again)
+  auto ask = [&](int r) {
+    x0 = load(a.residual, min(r, last - 1));
+    if constexpr (POST) h0 = load(a.h, min(r, last - 1));
+  };
+  if constexpr (AHEAD) ask(row);
+  for (; row < last; row += RPW) {
     const int64_t at = (int64_t)row * D;
+    const bool more = row + RPW < last;
     float v[CH][8];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = 8 * (t + c * TPR);
-      load8<T>((const T*)a.residual + at + col, min(8, max(0, D - col)), v[c]);
-    }
+    if constexpr (!AHEAD) ask(row);
+    Row g;
     if constexpr (POST) {
-      float h[CH][8], ss = 0.0f;
+      if constexpr (!HOLD) load_post();
+      g = load(a.gate, row / a.gate_rows);
+      settle(h0);
+      float ss = 0.0f;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = 8 * (t + c * TPR);
-        load8<T>((const T*)a.h + at + col, min(8, max(0, D - col)), h[c]);
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(h[c][k], h[c][k], ss);
-      }
+        for (int k = 0; k < 8; ++k) {
+          const float h = raw_at(h0.c[c], k);
+          ss = __builtin_fmaf(h, h, ss);
+        }
       const float r = 1.0f / __builtin_sqrtf(row_sum<TPR>(ss, red, turn) * inv + a.eps);
       if (t == 0) a.rstd[row] = r;
-      const T* const gate = a.gate ? (const T*)a.gate + (int64_t)(row / a.gate_rows) * D : nullptr;
+      settle(x0);
+      settle(g);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
-        float w[8], x[8];
-        load8<T>((const T*)a.weight + col, n, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[c][k] *= r * w[k];
-        if (gate) {
-          load8<T>(gate + col, n, x);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[c][k] *= x[k];
+        for (int k = 0; k < 8; ++k) {
+          float y = raw_at(h0.c[c], k) * (r * raw_at(w.c[c], k));
+          if (a.gate) y *= raw_at(g.c[c], k);
+          const float x = raw_at(x0.c[c], k);
+          v[c][k] = a.residual_scale ? __builtin_fmaf(x, raw_at(rs.c[c], k), y) : x + y;
         }
-        if (a.residual_scale) {
-          load8<T>((const T*)a.residual_scale + col, n, x);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[c][k] = __builtin_fmaf(v[c][k], x[k], h[c][k]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[c][k] += h[c][k];
-        }
-        store8((T*)a.out + at + col, n, v[c]);
+        store8(at_col((T*)a.out + at, col), n, v[c]);
         // the next norm reads what is stored
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[c][k] = rounded<T>(v[c][k]);
       }
+    } else {
+      settle(x0);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[c][k] = raw_at(x0.c[c], k);
     }
+    if constexpr (AHEAD) ask(row + RPW);
     if constexpr (PRE) {
+      if constexpr (!HOLD) load_pre();
       float ss = 0.0f;
 #pragma unroll
       for (int c = 0; c < CH; ++c)
@@ -108,10 +183,8 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_forward(NormArg
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
-        float w[8];
-        load8<T>((const T*)a.next_weight + col, n, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[c][k] = v[c][k] * r * w[k];
+        for (int k = 0; k < 8; ++k) v[c][k] = v[c][k] * r * raw_at(nw.c[c], k);
         if constexpr (FP8) {
           uint32_t m = 0;
 #pragma unroll
@@ -121,11 +194,24 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_forward(NormArg
           for (int k = 0; k < 8; ++k) v[c][k] = Coder<float>::nudged(v[c][k], b);
           // rows hold D rounded up to 16 codes: a piece of eight is inside or outside as a whole
           if (col < a.pitch)
-            *(u32x2*)(a.q + (int64_t)row * a.pitch + col) = u32x2{codes4(v[c][0], v[c][1], v[c][2], v[c][3], b.s),
+            *(u32x2*)at_col(a.q + (int64_t)row * a.pitch, col) = u32x2{codes4(v[c][0], v[c][1], v[c][2], v[c][3], b.s),
                                                                 codes4(v[c][4], v[c][5], v[c][6], v[c][7], b.s)};
-          if ((t & 15) == 0 && col < D) a.scale[(int64_t)(col / kBlock) * a.T + row] = b.s;
+          if ((t & 15) == 0) {
+            if constexpr (BATCH) scales[(t + c * TPR) / 16][row % ROWS] = b.s;
+            else if (col < D) a.scale[(int64_t)(col / kBlock) * a.T + row] = b.s;
+          }
         } else {
-          store8((T*)a.y + at + col, n, v[c]);
+          store8(at_col((T*)a.y + at, col), n, v[c]);
+        }
+      }
+      if constexpr (BATCH) {
+        if (row % ROWS == ROWS - 1 || !more) {
+          // (the next row's sums stand between this reading and the next writing)
+          const int row0 = max(first, row - row % ROWS), k = t % ROWS;
+          __syncthreads();
+          for (int blk = t / ROWS; blk < a.blocks; blk += TPR / ROWS)
+            if (row - row % ROWS + k >= row0 && row - row % ROWS + k <= row)
+              a.scale[(int64_t)blk * a.T + row - row % ROWS + k] = scales[blk][k];
         }
       }
     }
@@ -136,21 +222,62 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_forward(NormArg
 
 // Workers (a workgroup, or a wave of four) take runs of consecutive rows and keep the column sums of the
 // weights' gradients in registers; each run lies within the tokens that share a row of the gate.  A second
-// kernel adds the workers' sums in worker order, so the results repeat bit for bit.
+// kernel adds the workers' sums in worker order, so the results repeat bit for bit.  A row's tensors are
+// asked for one row ahead (AHEAD), and the shared vectors kept (HOLD), where the registers allow it.
 //
 // part: [3][workers][D] (weight, next_weight, residual_scale), then [chunks][D] of the gate
 // where a gate row has more than one chunk.
-template <class T, bool POST, bool PRE, int TPR, int CH>
+template <class T, bool POST, bool PRE, int TPR, int CH, bool SHORT>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_backward(NormGradArgs a) {
   __shared__ float red[2][16];
   int turn = 0;
   constexpr int RPW = rows_per_wg<TPR>();
+  // registers of a lane: a row's tensors as they lie in memory, the column sums, the shared vectors, and the rest
+  constexpr int RAW = CH * (int)sizeof(T) * 2, ROW = RAW * (1 + 2 * POST + 2 * PRE), SUM = 8 * CH * (3 * POST + PRE);
+  constexpr int VEC = RAW * (2 * POST + PRE), REST = 60 + 28 * CH, MOST = TPR == 1024 ? 128 : 256;
+  constexpr bool AHEAD = 2 * ROW + SUM + VEC + REST <= MOST, HOLD = AHEAD || ROW + SUM + VEC + REST <= MOST;
   const int t = threadIdx.x % TPR, D = a.D;
   const float inv = 1.0f / (float)D;
-  const int worker = blockIdx.x * RPW + threadIdx.x / TPR, workers = gridDim.x * RPW;
+  const int worker = blockIdx.x * RPW + sub_row<TPR>(), workers = gridDim.x * RPW;
   const bool gate_sums = POST && a.gate && a.gate_rows > 1;
   const int group_rows = a.T / a.groups;
+  typedef RawRow<T, CH> Row;
+  auto load = [&](const void* p, int row) { return load_row<SHORT, T, TPR, CH>(p, row, t, D); };
+  auto settle = [&](Row& r) { settle_row<SHORT, TPR>(r, t, D); };
+  struct Rows {
+    Row dout, h, res, out, dy;
+    float r, rn;
+  };
+  const void* const res = a.residual_scale ? a.residual : nullptr;
+  auto ask = [&](int row) {
+    Rows x;
+    x.dout = load(a.dout, row);
+    if constexpr (PRE) {
+      x.out = load(a.out, row);
+      x.dy = load(a.dy, row);
+      x.rn = a.rstd_next[row];
+    }
+    if constexpr (POST) {
+      x.h = load(a.h, row);
+      x.res = load(res, row);
+      x.r = a.rstd[row];
+    }
+    return x;
+  };
   float dw[POST ? CH : 1][8] = {}, dnw[PRE ? CH : 1][8] = {}, drs[POST ? CH : 1][8] = {}, dg[POST ? CH : 1][8] = {};
+  Row w, rs, nw;
+  auto load_post = [&]() {
+    w = load(a.weight, 0);
+    rs = load(a.residual_scale, 0);
+    settle(w);
+    settle(rs);
+  };
+  auto load_pre = [&]() {
+    nw = load(a.next_weight, 0);
+    settle(nw);
+  };
+  if constexpr (HOLD && POST) load_post();
+  if constexpr (HOLD && PRE) load_pre();
 
   const int per = ceil_div(a.chunks, workers);
   const int chunk1 = min(a.chunks, (worker + 1) * per);
@@ -158,103 +285,103 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_backward(NormGr
     const int group = chunk / a.chunks_per_gate, part = chunk - group * a.chunks_per_gate;
     const int row0 = group * group_rows + part * a.rows_per_chunk;
     const int row1 = min(row0 + a.rows_per_chunk, (group + 1) * group_rows);
+    Rows ahead;
+    if constexpr (AHEAD) ahead = ask(min(row0, a.T - 1));
     for (int row = row0; row < row1; ++row) {
       const int64_t at = (int64_t)row * D;
+      Rows x;
+      if constexpr (AHEAD) {
+        x = ahead;
+        ahead = ask(min(row + 1, row1 - 1));
+      } else {
+        x = ask(row);
+      }
+      if constexpr (HOLD && POST) {
+        repack(w);
+        repack(rs);
+      }
+      if constexpr (HOLD && PRE) repack(nw);
+      Row g;
+      if constexpr (POST) g = load(a.gate, row / a.gate_rows);
+      settle(x.dout);
       float dv[CH][8];
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = 8 * (t + c * TPR);
-        load8<T>((const T*)a.dout + at + col, a.dout ? min(8, max(0, D - col)) : 0, dv[c]);
-      }
-      float h[POST ? CH : 1][8];
-      if constexpr (POST) {
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int col = 8 * (t + c * TPR);
-          load8<T>((const T*)a.h + at + col, min(8, max(0, D - col)), h[c]);
-        }
-      }
+        for (int k = 0; k < 8; ++k) dv[c][k] = raw_at(x.dout.c[c], k);
       if constexpr (PRE) {
-        const float r = a.rstd_next[row];
-        float x[CH][8], g[CH][8], s = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
-          float w[8];
-          load8<T>((const T*)a.out + at + col, n, x[c]);
-          load8<T>((const T*)a.dy + at + col, n, g[c]);
-          load8<T>((const T*)a.next_weight + col, n, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x[c][k] *= r;
-            dnw[c][k] = __builtin_fmaf(g[c][k], x[c][k], dnw[c][k]);
-            g[c][k] *= w[k];
-            s = __builtin_fmaf(g[c][k], x[c][k], s);
-          }
-        }
-        s = row_sum<TPR>(s, red, turn) * inv;
+        if constexpr (!HOLD) load_pre();
+        settle(x.out);
+        settle(x.dy);
+        float s = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dv[c][k] = __builtin_fmaf(r, __builtin_fmaf(-s, x[c][k], g[c][k]), dv[c][k]);
-      }
-      if constexpr (!POST) {
+          for (int k = 0; k < 8; ++k) {
+            const float xh = raw_at(x.out.c[c], k) * x.rn, gy = raw_at(x.dy.c[c], k);
+            dnw[c][k] = __builtin_fmaf(gy, xh, dnw[c][k]);
+            s = __builtin_fmaf(gy * raw_at(nw.c[c], k), xh, s);
+          }
+        s = row_sum<TPR>(s, red, turn) * inv;
+        repack(x.out);
+        repack(x.dy);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int col = 8 * (t + c * TPR);
-          store8((T*)a.dx + at + col, min(8, max(0, D - col)), dv[c]);
-        }
-      } else {
-        const float r = a.rstd[row];
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float xh = raw_at(x.out.c[c], k) * x.rn, gn = raw_at(x.dy.c[c], k) * raw_at(nw.c[c], k);
+            dv[c][k] = __builtin_fmaf(x.rn, __builtin_fmaf(-s, xh, gn), dv[c][k]);
+          }
+      }
+      if constexpr (POST) {
+        if constexpr (!HOLD) load_post();
+        settle(x.h);
+        settle(x.res);
+        settle(g);
         float s = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
-          float w[8], x[8];
-          if (a.residual_scale) {
-            load8<T>((const T*)a.residual + at + col, n, w);
-            load8<T>((const T*)a.residual_scale + col, n, x);
+          float y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              drs[c][k] = __builtin_fmaf(dv[c][k], w[k], drs[c][k]);
-              x[k] *= dv[c][k];
-            }
-            store8((T*)a.dresidual + at + col, n, x);
-          } else {
-            store8((T*)a.dresidual + at + col, n, dv[c]);
+          for (int k = 0; k < 8; ++k) {
+            drs[c][k] = __builtin_fmaf(dv[c][k], raw_at(x.res.c[c], k), drs[c][k]);
+            y[k] = a.residual_scale ? dv[c][k] * raw_at(rs.c[c], k) : dv[c][k];
           }
-          load8<T>((const T*)a.weight + col, n, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[c][k] *= r;
+          store8(at_col((T*)a.dresidual + at, col), n, y);
           if (a.gate) {
-            load8<T>((const T*)a.gate + (int64_t)(row / a.gate_rows) * D + col, n, x);
             if (gate_sums) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) dg[c][k] = __builtin_fmaf(dv[c][k] * h[c][k], w[k], dg[c][k]);
+              for (int k = 0; k < 8; ++k)
+                dg[c][k] = __builtin_fmaf(dv[c][k] * (raw_at(x.h.c[c], k) * x.r), raw_at(w.c[c], k), dg[c][k]);
             } else {
-              float own[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) own[k] = dv[c][k] * h[c][k] * w[k];
-              store8((T*)a.dgate + at + col, n, own);
+              for (int k = 0; k < 8; ++k) y[k] = dv[c][k] * (raw_at(x.h.c[c], k) * x.r) * raw_at(w.c[c], k);
+              store8(at_col((T*)a.dgate + at, col), n, y);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dv[c][k] *= x[k];
+            for (int k = 0; k < 8; ++k) dv[c][k] *= raw_at(g.c[c], k);
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            dw[c][k] = __builtin_fmaf(dv[c][k], h[c][k], dw[c][k]);
-            dv[c][k] *= w[k];
-            s = __builtin_fmaf(dv[c][k], h[c][k], s);
+            const float hh = raw_at(x.h.c[c], k) * x.r;
+            dw[c][k] = __builtin_fmaf(dv[c][k], hh, dw[c][k]);
+            dv[c][k] *= raw_at(w.c[c], k);
+            s = __builtin_fmaf(dv[c][k], hh, s);
           }
         }
         s = row_sum<TPR>(s, red, turn) * inv;
+        repack(x.h);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int col = 8 * (t + c * TPR);
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dv[c][k] = r * __builtin_fmaf(-s, h[c][k], dv[c][k]);
-          store8((T*)a.dx + at + col, min(8, max(0, D - col)), dv[c]);
-        }
+          for (int k = 0; k < 8; ++k)
+            dv[c][k] = x.r * __builtin_fmaf(-s, raw_at(x.h.c[c], k) * x.r, dv[c][k]);
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = 8 * (t + c * TPR);
+        store8(at_col((T*)a.dx + at, col), min(8, max(0, D - col)), dv[c]);
       }
     }
     if constexpr (POST) {
@@ -281,14 +408,15 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_backward(NormGr
   }
 }
 
-// out[d] = the sum of `count` rows of part, in a fixed order: thread (column, slice) of 32 x 8 adds the slice's
-// run of rows in turn, then the eight runs are added in turn.
+// out[d] = the sum of `count` rows of part, in a fixed order: thread (column, slice) of 32 x 32 adds the slice's
+// run of rows in turn, then the runs are added in turn.
+constexpr int kSlices = 32;
 template <class T>
 __device__ __forceinline__ void column_sum(const float* __restrict__ part, T* __restrict__ out, int count, int D,
                                            int block) {
-  __shared__ float run[8][32];
+  __shared__ float run[kSlices][32];
   const int col = threadIdx.x & 31, slice = threadIdx.x >> 5, d = block * 32 + col;
-  const int per = ceil_div(count, 8), c0 = slice * per, c1 = min(count, c0 + per);
+  const int per = ceil_div(count, kSlices), c0 = slice * per, c1 = min(count, c0 + per);
   float s = 0.0f;
   if (d < D) {
 #pragma unroll 8
@@ -299,19 +427,19 @@ __device__ __forceinline__ void column_sum(const float* __restrict__ part, T* __
   if (slice || d >= D) return;
   float x = run[0][col];
 #pragma unroll
-  for (int k = 1; k < 8; ++k) x += run[k][col];
+  for (int k = 1; k < kSlices; ++k) x += run[k][col];
   if constexpr (sizeof(T) == 2) out[d] = (T)pack_bf16(x, x);
   else out[d] = x;
 }
 
 template <class T>
-__global__ __launch_bounds__(256) void sk_column_sums(const float* part, T* out, int count, int D) {
+__global__ __launch_bounds__(32 * kSlices) void sk_column_sums(const float* part, T* out, int count, int D) {
   column_sum<T>(part, out, count, D, blockIdx.x);
 }
 
 // The norms' sums: blockIdx.y 0, 1, 2 the three vectors, then the rows of the gate.
 template <class T>
-__global__ __launch_bounds__(256) void sk_norm_sums(NormGradArgs a, int workers) {
+__global__ __launch_bounds__(32 * kSlices) void sk_norm_sums(NormGradArgs a, int workers) {
   const int y = blockIdx.y;
   if (y < 3) {
     T* const out = (T*)(y == 0 ? a.dweight : y == 1 ? a.dnext_weight : a.dresidual_scale);
@@ -323,16 +451,18 @@ __global__ __launch_bounds__(256) void sk_norm_sums(NormGradArgs a, int workers)
   }
 }
 
-template <class T, bool POST, bool PRE, bool FP8, int TPR, int CH>
+template <class T, bool POST, bool PRE, bool FP8, int TPR, int CH, bool SHORT = false>
 hipError_t forward(const NormArgs& a, int cus, hipStream_t s) {
   const int rpw = rows_per_wg<TPR>(), threads = TPR == 64 ? 256 : TPR;
-  const int wgs = ceil_div(a.T, rpw), most = cus * (2048 / threads) * 4;
-  hipLaunchKernelGGL((sk_norm_forward<T, POST, PRE, FP8, TPR, CH>), dim3(min(wgs, most)), dim3(threads), 0, s, a);
+  // as many workgroups as run at once (about 1024 threads to a compute unit), each on a run of rows
+  const int wgs = ceil_div(a.T, rpw), most = cus * (1024 / threads);
+  hipLaunchKernelGGL((sk_norm_forward<T, POST, PRE, FP8, TPR, CH, SHORT>), dim3(min(wgs, most)), dim3(threads), 0, s, a);
   return hipGetLastError();
 }
 
 template <class T, bool POST, bool PRE, bool FP8>
 hipError_t forward_width(const NormArgs& a, int cus, hipStream_t s) {
+  if (a.D < 8) return forward<T, POST, PRE, FP8, 64, 1, true>(a, cus, s);
   // Few rows: more threads to each, to shorten the call.  Many: as few as hold the row.
   if (a.T <= 2 * cus && a.D > 512) {
     if (a.D <= 2048) return forward<T, POST, PRE, FP8, 256, 1>(a, cus, s);
@@ -342,7 +472,8 @@ hipError_t forward_width(const NormArgs& a, int cus, hipStream_t s) {
   if (a.D <= 1024) return forward<T, POST, PRE, FP8, 64, 2>(a, cus, s);
   if (a.D <= 2048) return forward<T, POST, PRE, FP8, 256, 1>(a, cus, s);
   if (a.D <= 4096) return forward<T, POST, PRE, FP8, 256, 2>(a, cus, s);
-  if (a.D <= 8192) return forward<T, POST, PRE, FP8, 256, 4>(a, cus, s);
+  if (a.D <= 8192) return forward<T, POST, PRE, FP8, 512, 2>(a, cus, s);
+  if (a.D <= 16384) return forward<T, POST, PRE, FP8, 1024, 2>(a, cus, s);
   return forward<T, POST, PRE, FP8, 1024, 4>(a, cus, s);
 }
 
@@ -354,31 +485,31 @@ hipError_t forward_form(const NormArgs& a, int cus, hipStream_t s) {
 }
 
 // Threads of a row in the backward, and workers of a workgroup.
-int grad_threads(int D) { return D <= 512 ? 64 : D <= 2048 ? 256 : D <= 4096 ? 512 : 1024; }
+int grad_threads(int D) { return D <= 512 ? 64 : D <= 2048 ? 256 : D <= 8192 ? 512 : 1024; }
 int grad_rpw(int D) { return D <= 512 ? 4 : 1; }
 int grad_wgs(const NormGradArgs& a) { return ceil_div(a.chunks, grad_rpw(a.D) * ceil_div(a.chunks, 4096)); }
 
-template <class T, bool POST, bool PRE, int TPR, int CH>
+template <class T, bool POST, bool PRE, int TPR, int CH, bool SHORT = false>
 hipError_t backward(const NormGradArgs& a, hipStream_t s) {
   const int wgs = grad_wgs(a);
-  hipLaunchKernelGGL((sk_norm_backward<T, POST, PRE, TPR, CH>), dim3(wgs), dim3(TPR == 64 ? 256 : TPR), 0, s, a);
+  hipLaunchKernelGGL((sk_norm_backward<T, POST, PRE, TPR, CH, SHORT>), dim3(wgs), dim3(TPR == 64 ? 256 : TPR), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool gate = a.dgate && a.gate_rows > 1 && a.chunks_per_gate > 1;
-  hipLaunchKernelGGL((sk_norm_sums<T>), dim3(ceil_div(a.D, 32), 3 + (gate ? a.groups : 0)), dim3(256), 0, s, a,
+  hipLaunchKernelGGL((sk_norm_sums<T>), dim3(ceil_div(a.D, 32), 3 + (gate ? a.groups : 0)), dim3(32 * kSlices), 0, s, a,
                      wgs * grad_rpw(a.D));
   return hipGetLastError();
 }
 
 template <class T, bool POST, bool PRE>
 hipError_t backward_width(const NormGradArgs& a, hipStream_t s) {
+  if (a.D < 8) return backward<T, POST, PRE, 64, 1, true>(a, s);
   switch (grad_threads(a.D)) {
     case 64: return backward<T, POST, PRE, 64, 1>(a, s);
     case 256: return backward<T, POST, PRE, 256, 1>(a, s);
-    case 512: return backward<T, POST, PRE, 512, 1>(a, s);
-    default: break;
+    case 512: return a.D <= 4096 ? backward<T, POST, PRE, 512, 1>(a, s) : backward<T, POST, PRE, 512, 2>(a, s);
+    default: return a.D <= 16384 ? backward<T, POST, PRE, 1024, 2>(a, s) : backward<T, POST, PRE, 1024, 4>(a, s);
   }
-  return a.D <= 8192 ? backward<T, POST, PRE, 1024, 1>(a, s) : backward<T, POST, PRE, 1024, 4>(a, s);
 }
 
 template <class T>
@@ -399,7 +530,7 @@ int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus) {
   const bool grouped = a->h && a->gate && a->gate_rows > 1;
   a->groups = grouped ? a->T / a->gate_rows : 1;
   const int group_rows = a->T / a->groups;
-  const int want = 4 * cus * grad_rpw(a->D) * 256 / (grad_threads(a->D) < 256 ? 256 : grad_threads(a->D));
+  const int want = 2 * cus * grad_rpw(a->D) * 256 / (grad_threads(a->D) < 256 ? 256 : grad_threads(a->D));
   a->chunks_per_gate = a->groups >= want ? 1 : ceil_div(want, a->groups);
   a->rows_per_chunk = ceil_div(group_rows, a->chunks_per_gate);
   a->chunks_per_gate = ceil_div(group_rows, a->rows_per_chunk);
@@ -414,7 +545,7 @@ hipError_t launch_norm_backward(const NormGradArgs& a, bool f32, hipStream_t s) 
 }
 
 hipError_t launch_column_sums_bf16(const float* part, uint16_t* out, int count, int D, hipStream_t s) {
-  hipLaunchKernelGGL((sk_column_sums<uint16_t>), dim3((unsigned)ceil_div(D, 32)), dim3(256), 0, s, part, out, count, D);
+  hipLaunchKernelGGL((sk_column_sums<uint16_t>), dim3((unsigned)ceil_div(D, 32)), dim3(32 * kSlices), 0, s, part, out, count, D);
   return hipGetLastError();
 }
 

@@ -12,6 +12,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sk_common.h"
 #include "sk_fp8.h"
 
@@ -44,7 +46,7 @@ __device__ __forceinline__ void transpose8(const uint32_t (&w)[8][2], uint32_t (
 
 // TILE: one scale per 128 x 128.  PLAIN / TRANS: which forms are written (with SUMS: perhaps neither).  SUMS: also the column sums of the
 // tile's rows, part[row block][column], in a fixed order (the first pass of a bias gradient).
-template <class T, bool TILE, bool PLAIN, bool TRANS, bool SUMS>
+template <class T, bool TILE, bool PLAIN, bool TRANS, bool SUMS, bool SHORT>
 __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
   constexpr bool COLS = TRANS && !TILE;
   __shared__ __attribute__((aligned(16))) uint8_t codes_t[TRANS ? 128 * kPitch : 16];
@@ -55,11 +57,18 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
   const int t = threadIdx.x, tr = t >> 4, tc = t & 15;
   const int R = a.R, C = a.C;
   const int row0 = rb * 128 + 8 * tr, col0 = cb * 128 + 8 * tc;
-  const int n = min(8, max(0, C - col0));
   float x[8][8];
+  {
+    Raw8<T> raw[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    load8<T>((const T*)a.x + (int64_t)(row0 + i) * C + col0, row0 + i < R ? n : 0, x[i]);
+    for (int i = 0; i < 8; ++i) raw[i] = load_raw8<SHORT>((const T*)a.x + (int64_t)min(row0 + i, R - 1) * C, col0, C);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      settle8<SHORT>(raw[i], col0, C);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[i][k] = row0 + i < R ? raw_at(raw[i], k) : 0.0f;
+    }
+  }
 
   if constexpr (SUMS) {
 #pragma unroll
@@ -178,13 +187,13 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
   }
 }
 
-template <class T, bool TILE, bool SUMS>
+template <class T, bool TILE, bool SUMS, bool SHORT>
 hipError_t launch_form(const QuantArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.kb * (unsigned)a.rb), block(256);
-  if (a.q && a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, true, SUMS>), grid, block, 0, s, a);
-  else if (a.q) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, false, SUMS>), grid, block, 0, s, a);
-  else if (a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, true, SUMS>), grid, block, 0, s, a);
-  else if constexpr (SUMS) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, false, SUMS>), grid, block, 0, s, a);
+  if (a.q && a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, true, SUMS, SHORT>), grid, block, 0, s, a);
+  else if (a.q) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, false, SUMS, SHORT>), grid, block, 0, s, a);
+  else if (a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, true, SUMS, SHORT>), grid, block, 0, s, a);
+  else if constexpr (SUMS) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, false, SUMS, SHORT>), grid, block, 0, s, a);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
@@ -192,9 +201,17 @@ hipError_t launch_form(const QuantArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_quantize_block(const QuantArgs& a, bool f32, bool tile, hipStream_t s) {
-  if (a.part) return !f32 && !tile ? launch_form<uint16_t, false, true>(a, s) : hipErrorInvalidValue;
-  if (f32) return tile ? launch_form<float, true, false>(a, s) : launch_form<float, false, false>(a, s);
-  return tile ? launch_form<uint16_t, true, false>(a, s) : launch_form<uint16_t, false, false>(a, s);
+  if (a.part && (f32 || tile)) return hipErrorInvalidValue;
+  auto go = [&](auto elem, auto tiled, auto sums) {
+    typedef decltype(elem) T;
+    constexpr bool TILE = decltype(tiled)::value, SUMS = decltype(sums)::value;
+    return a.C < 8 ? launch_form<T, TILE, SUMS, true>(a, s) : launch_form<T, TILE, SUMS, false>(a, s);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  if (a.part) return go(uint16_t{}, no, yes);
+  if (f32) return tile ? go(float{}, yes, no) : go(float{}, no, no);
+  return tile ? go(uint16_t{}, yes, no) : go(uint16_t{}, no, no);
 }
 
 }  // namespace sk
