@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 __all__ = [
@@ -107,6 +108,11 @@ class _NormGradArgs(ctypes.Structure):
             (n, ctypes.c_int64) for n in ("T", "D", "gates")] + [("stream", ctypes.c_void_p)]
 
 
+# The same structures as bytes: filling a ctypes structure field by field takes longer than a small norm.
+_NORM_PACK = struct.Struct("=if12Q3qQ").pack
+_NORM_GRAD_PACK = struct.Struct("=ii17Q3qQ").pack
+
+
 @dataclass(frozen=True)
 class Plan:
     tile_m: int
@@ -157,8 +163,8 @@ def load():
     lib.sk_quantize_fp8_block.argtypes = [vp, i32, i32, vp, vp, vp, vp, i64, i64, vp]
     lib.sk_gemm_fp8_block.argtypes = [vp, vp, vp, vp, i32, vp, vp, i64, i64, i64, i32, vp]
     lib.sk_gemm_fp8_block_backward.argtypes = [vp] * 8 + [i64, i64, i64, i32, vp]
-    lib.sk_norm_forward.argtypes = [ctypes.POINTER(_NormArgs)]
-    lib.sk_norm_backward.argtypes = [ctypes.POINTER(_NormGradArgs)]
+    lib.sk_norm_forward.argtypes = [vp]      # a structure by reference, or its bytes
+    lib.sk_norm_backward.argtypes = [vp]
     lib.sk_gemm_ex.argtypes = [ctypes.POINTER(_Args)]
     lib.sk_plan.argtypes = [ctypes.POINTER(_PlanQuery), ctypes.POINTER(_PlanInfo)]
     lib.sk_plan_wg_range.argtypes = [ctypes.POINTER(_PlanInfo), ctypes.c_int32,
@@ -195,9 +201,15 @@ def _ok(status: int, where: str):
 
 # ---------------------------------------------------------------- tensor marshalling
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t):
@@ -208,10 +220,11 @@ def _stream(t, stream):
     if stream is not None:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     torch = _torch()
+    dev = t.device
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None and t.device.type == "cuda":
-        return raw(t.device.index if t.device.index is not None else torch.cuda.current_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
+    if raw is not None and dev.type == "cuda":
+        return raw(dev.index if dev.index is not None else torch.cuda.current_device())
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _need(t, name, dtypes, shape, device):
@@ -445,12 +458,14 @@ def _elem(t, name):
     """SK_ELEM_* of a tensor."""
     torch = _torch()
     try:
-        e = {torch.bfloat16: 0, torch.float32: 1}.get(t.dtype)
+        dtype = t.dtype
     except AttributeError:
         raise TypeError(f"{name} must be a tensor") from None
-    if e is None:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected bfloat16 or float32")
-    return e
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name} has dtype {dtype}, expected bfloat16 or float32")
 
 
 def _up16(n):
@@ -581,21 +596,17 @@ def _gates(gate, T, D, types, dev):
     return G
 
 
-def _norm_outputs(a, like, next_weight, quantize, T, D, types, dev):
-    """Allocates the outputs of the norm before a block; returns them in order."""
+def _norm_outputs(like, next_weight, name, quantize, T, D, types, dev):
+    """The outputs of the norm before a block: (returned tensors, y, q, scale, rstd_next pointers)."""
     torch = _torch()
-    _need(next_weight, "weight" if a.h is None else "next_weight", types, (D,), dev)
-    a.next_weight = next_weight.data_ptr()
+    _need(next_weight, name, types, (D,), dev)
     rstd = torch.empty((T,), dtype=torch.float32, device=dev)
-    a.rstd_next = rstd.data_ptr()
     if not quantize:
         y = torch.empty_like(like)
-        a.y = y.data_ptr()
-        return y, rstd
+        return (y, rstd), y.data_ptr(), 0, 0, rstd.data_ptr()
     q = torch.empty((T, _up16(D)), dtype=torch.float8_e4m3fn, device=dev)
     s = torch.empty((_blocks(D), T), dtype=torch.float32, device=dev)
-    a.q, a.scale = q.data_ptr(), s.data_ptr()
-    return q, s, rstd
+    return (q, s, rstd), 0, q.data_ptr(), s.data_ptr(), rstd.data_ptr()
 
 
 def rms_norm(x, weight, eps=1e-6, *, quantize=False, stream=None):
@@ -605,9 +616,9 @@ def rms_norm(x, weight, eps=1e-6, *, quantize=False, stream=None):
     quantize_fp8_block(y, "row") of the fp32 y would give them, ready to be gemm_fp8_block's A."""
     e, T, D, dev, types = _norm_shape(x, "x")
     _need(x, "x", types, (T, D), dev)
-    a = _NormArgs(elem=e, eps=eps, residual=x.data_ptr(), T=T, D=D, stream=_stream(x, stream))
-    got = _norm_outputs(a, x, weight, quantize, T, D, types, dev)
-    _ok(load().sk_norm_forward(ctypes.byref(a)), "sk_norm_forward")
+    got, y, q, s, rn = _norm_outputs(x, weight, "weight", quantize, T, D, types, dev)
+    _ok(load().sk_norm_forward(_NORM_PACK(e, eps, 0, x.data_ptr(), 0, 0, 0, weight.data_ptr(), 0, 0, y, q, s, rn,
+                                          T, D, 0, _stream(x, stream))), "sk_norm_forward")
     return got
 
 
@@ -625,18 +636,17 @@ def gated_norm(h, residual, weight, gate=None, residual_scale=None, eps=1e-6, *,
     _need(weight, "weight", types, (D,), dev)
     if quantize and next_weight is None:
         raise ValueError("quantize needs next_weight")
-    out = torch.empty_like(h)
-    rstd = torch.empty((T,), dtype=torch.float32, device=dev)
-    a = _NormArgs(elem=e, eps=eps, h=h.data_ptr(), residual=residual.data_ptr(), weight=weight.data_ptr(),
-                  out=out.data_ptr(), rstd=rstd.data_ptr(), T=T, D=D, stream=_stream(h, stream))
-    if gate is not None:
-        a.gates = _gates(gate, T, D, types, dev)
-        a.gate = gate.data_ptr()
+    gates = 0 if gate is None else _gates(gate, T, D, types, dev)
     if residual_scale is not None:
         _need(residual_scale, "residual_scale", types, (D,), dev)
-        a.residual_scale = residual_scale.data_ptr()
-    more = () if next_weight is None else _norm_outputs(a, h, next_weight, quantize, T, D, types, dev)
-    _ok(load().sk_norm_forward(ctypes.byref(a)), "sk_norm_forward")
+    out = torch.empty_like(h)
+    rstd = torch.empty((T,), dtype=torch.float32, device=dev)
+    more, y, q, s, rn = ((), 0, 0, 0, 0) if next_weight is None else \
+        _norm_outputs(h, next_weight, "next_weight", quantize, T, D, types, dev)
+    _ok(load().sk_norm_forward(_NORM_PACK(
+        e, eps, h.data_ptr(), residual.data_ptr(), weight.data_ptr(), _ptr(gate) or 0, _ptr(residual_scale) or 0,
+        _ptr(next_weight) or 0, out.data_ptr(), rstd.data_ptr(), y, q, s, rn, T, D, gates, _stream(h, stream))),
+        "sk_norm_forward")
     return (out, rstd, *more)
 
 
@@ -650,10 +660,9 @@ def rms_norm_backward(dy, x, weight, rstd, dresidual=None, *, stream=None):
     _need(weight, "weight", types, (D,), dev)
     _need(rstd, "rstd", (torch.float32,), (T,), dev)
     dx, dw = torch.empty_like(x), torch.empty_like(weight)
-    a = _NormGradArgs(elem=e, dout=_ptr(dresidual), dy=dy.data_ptr(), out=x.data_ptr(), next_weight=weight.data_ptr(),
-                      rstd_next=rstd.data_ptr(), dx=dx.data_ptr(), dnext_weight=dw.data_ptr(), T=T, D=D,
-                      stream=_stream(x, stream))
-    _ok(load().sk_norm_backward(ctypes.byref(a)), "sk_norm_backward")
+    _ok(load().sk_norm_backward(_NORM_GRAD_PACK(
+        e, 0, _ptr(dresidual) or 0, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), rstd.data_ptr(), 0, 0, 0, 0, 0, 0,
+        dx.data_ptr(), 0, 0, 0, 0, dw.data_ptr(), T, D, 0, _stream(x, stream))), "sk_norm_backward")
     return dx, dw
 
 
@@ -669,31 +678,31 @@ def gated_norm_backward(dout, h, weight, rstd, gate=None, residual=None, residua
     _need(dout, "dout", types, (T, D), dev)
     _need(weight, "weight", types, (D,), dev)
     _need(rstd, "rstd", (torch.float32,), (T,), dev)
-    dh, dres, dw = torch.empty_like(h), torch.empty_like(h), torch.empty_like(weight)
-    a = _NormGradArgs(elem=e, dout=dout.data_ptr(), h=h.data_ptr(), weight=weight.data_ptr(), rstd=rstd.data_ptr(),
-                      dx=dh.data_ptr(), dresidual=dres.data_ptr(), dweight=dw.data_ptr(), T=T, D=D,
-                      stream=_stream(h, stream))
+    gates = 0
     dgate = drs = dnw = None
     if gate is not None:
-        a.gates = _gates(gate, T, D, types, dev)
+        gates = _gates(gate, T, D, types, dev)
         dgate = torch.empty_like(gate)
-        a.gate, a.dgate = gate.data_ptr(), dgate.data_ptr()
     if residual_scale is not None:
         _need(residual, "residual", types, (T, D), dev)
         _need(residual_scale, "residual_scale", types, (D,), dev)
         drs = torch.empty_like(residual_scale)
-        a.residual, a.residual_scale, a.dresidual_scale = residual.data_ptr(), residual_scale.data_ptr(), drs.data_ptr()
+    else:
+        residual = None
     if dy is not None:
         _need(dy, "dy", types, (T, D), dev)
         _need(out, "out", types, (T, D), dev)
         _need(next_weight, "next_weight", types, (D,), dev)
         _need(rstd_next, "rstd_next", (torch.float32,), (T,), dev)
         dnw = torch.empty_like(next_weight)
-        a.dy, a.out, a.next_weight = dy.data_ptr(), out.data_ptr(), next_weight.data_ptr()
-        a.rstd_next, a.dnext_weight = rstd_next.data_ptr(), dnw.data_ptr()
     elif out is not None or next_weight is not None or rstd_next is not None:
         raise ValueError("out, next_weight and rstd_next come with dy")
-    _ok(load().sk_norm_backward(ctypes.byref(a)), "sk_norm_backward")
+    dh, dres, dw = torch.empty_like(h), torch.empty_like(h), torch.empty_like(weight)
+    p = lambda t: 0 if t is None else t.data_ptr()
+    _ok(load().sk_norm_backward(_NORM_GRAD_PACK(
+        e, 0, p(dout), p(dy), p(out), p(next_weight), p(rstd_next), p(h), p(residual), p(weight), p(gate),
+        p(residual_scale), p(rstd), p(dh), p(dres), p(dw), p(dgate), p(drs), p(dnw), T, D, gates,
+        _stream(h, stream))), "sk_norm_backward")
     return dh, dres, dw, dgate, drs, dnw
 
 
