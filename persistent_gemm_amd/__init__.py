@@ -449,6 +449,33 @@ def gemm_ex(dtype, A, B, A_scale=None, B_scale=None, bias=None, C=None, *, grid_
     return C
 
 
+# ---------------------------------------------------------------- the short way (csrc/sk_native.cpp)
+
+_NATIVE = None
+
+
+def _native():
+    """The module that takes the calls below whose arguments are all right, and returns None for the others."""
+    global _NATIVE
+    if _NATIVE is None:
+        lib = load()
+        torch = _torch()
+        try:
+            from . import _sknative as native
+        except ImportError as e:
+            raise RuntimeError(f"the native binding is missing or does not load ({e}): build it with "
+                               "`python persistent_gemm_amd/build.py`") from e
+        native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "sk_quantize_fp8_block", "sk_gemm_fp8_block", "sk_gemm_fp8_block_backward", "sk_norm_forward",
+            "sk_norm_backward")), torch._C._cuda_getCurrentRawStream)
+        _NATIVE = native
+    return _NATIVE
+
+
+def _handle(stream):
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 # ---------------------------------------------------------------- E4M3 with a scale for each block of 128
 
 _BLOCKS = {"row": 0, "tile": 1}
@@ -484,6 +511,13 @@ def quantize_fp8_block(x, block="row", *, transpose=False, stream=None):
     float8_e4m3fn [R, C rounded up to 16] (zeros past C) and scale [ceil(C/128), R].  block "tile":
     128 x 128 elements do; scale [ceil(R/128), ceil(C/128)].  transpose=True gives the same of x^T (blocks
     along R) instead, transpose="both" gives (q, scale, qt, scale_t) from one pass over x."""
+    if block in _BLOCKS and transpose in (False, True, "both"):
+        got = (_NATIVE or _native()).quantize(x, _BLOCKS[block], 3 if transpose == "both" else 2 if transpose else 1,
+                                              None if stream is None else _handle(stream))
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            raise SkError(got, "sk_quantize_fp8_block")
     torch = _torch()
     e = _elem(x, "x")
     if block not in _BLOCKS:
@@ -514,6 +548,11 @@ def gemm_fp8_block(A, B, A_scale, B_scale, bias=None, C=None, grid_cap=0, stream
     """C = A . B^T (+ bias) of E4M3 operands with an fp32 scale for each block of 128 along K; returns C
     (bf16 [M, N]).  Operands as quantize_fp8_block gives them: A [M, K] with A_scale [ceil(K/128), M],
     B [N, K] with B_scale [ceil(K/128), N] (block "row") or [ceil(N/128), ceil(K/128)] (block "tile")."""
+    got = (_NATIVE or _native()).gemm(A, B, A_scale, B_scale, bias, C, grid_cap, None if stream is None else _handle(stream))
+    if got.__class__ is int:
+        raise SkError(got, "sk_gemm_fp8_block")
+    if got is not None:
+        return got
     torch = _torch()
     M, K = A.shape
     N = B.shape[0]
@@ -543,6 +582,14 @@ def gemm_fp8_block_backward(dC, At=None, At_scale=None, Bt=None, Bt_scale=None, 
     At_scale [ceil(M/128), K] is A's transposed form from quantize_fp8_block(a, "row", transpose=...),
     needed for dB; Bt [K, N rounded up to 16] with Bt_scale [ceil(K/128), ceil(N/128)] is B's from
     quantize_fp8_block(b, "tile", transpose=...), needed for dA."""
+    if (need_dA or need_dB) and (Bt is not None or not need_dA) and (At is not None or not need_dB):
+        a, b = (At, At_scale) if need_dB else (None, None), (Bt, Bt_scale) if need_dA else (None, None)
+        got = (_NATIVE or _native()).gemm_backward(dC, *a, *b, need_dbias, grid_cap,
+                                                   None if stream is None else _handle(stream))
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            raise SkError(got, "sk_gemm_fp8_block_backward")
     torch = _torch()
     if dC.dim() != 2:
         raise ValueError(f"dC has shape {tuple(dC.shape)}, expected two dimensions")
@@ -614,6 +661,12 @@ def rms_norm(x, weight, eps=1e-6, *, quantize=False, stream=None):
     (bf16 or fp32; weight [D] of the same type).  Returns (y, rstd), or with quantize=True
     (q, scale, rstd): y as E4M3 codes [T, D rounded up to 16] with scales [ceil(D/128), T], as
     quantize_fp8_block(y, "row") of the fp32 y would give them, ready to be gemm_fp8_block's A."""
+    got = (_NATIVE or _native()).norm_forward(None, x, None, None, None, weight, eps, quantize,
+                                              None if stream is None else _handle(stream))
+    if got.__class__ is tuple:
+        return got
+    if got is not None:
+        raise SkError(got, "sk_norm_forward")
     e, T, D, dev, types = _norm_shape(x, "x")
     _need(x, "x", types, (T, D), dev)
     got, y, q, s, rn = _norm_outputs(x, weight, "weight", quantize, T, D, types, dev)
@@ -629,6 +682,13 @@ def gated_norm(h, residual, weight, gate=None, residual_scale=None, eps=1e-6, *,
     of T (each T / G consecutive tokens share a row); residual_scale None or [D].  Returns (out, rstd); with
     next_weight also the next block's rms_norm of out as stored, from the same pass: (out, rstd, y, rstd_next),
     or (out, rstd, q, scale, rstd_next) with quantize=True."""
+    if h is not None:
+        got = (_NATIVE or _native()).norm_forward(h, residual, weight, gate, residual_scale, next_weight, eps, quantize,
+                                                  None if stream is None else _handle(stream))
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            raise SkError(got, "sk_norm_forward")
     torch = _torch()
     e, T, D, dev, types = _norm_shape(h, "h")
     _need(h, "h", types, (T, D), dev)
@@ -653,6 +713,12 @@ def gated_norm(h, residual, weight, gate=None, residual_scale=None, eps=1e-6, *,
 def rms_norm_backward(dy, x, weight, rstd, dresidual=None, *, stream=None):
     """Gradients of rms_norm: returns (dx, dweight).  dresidual, a gradient that reaches x by another way
     (a residual branch), is added to dx in the same pass."""
+    got = (_NATIVE or _native()).norm_backward(dresidual, None, None, None, None, None, None, dy, x, weight, rstd,
+                                               None if stream is None else _handle(stream))
+    if got.__class__ is tuple:
+        return got
+    if got is not None:
+        raise SkError(got, "sk_norm_backward")
     torch = _torch()
     e, T, D, dev, types = _norm_shape(x, "x")
     for t, n in ((x, "x"), (dy, "dy")) + (((dresidual, "dresidual"),) if dresidual is not None else ()):
@@ -672,6 +738,13 @@ def gated_norm_backward(dout, h, weight, rstd, gate=None, residual=None, residua
     where there is no such input.  dout is the gradient at out; where the forward also made the next block's norm,
     dy is the gradient at y (for a quantised y too) and out, next_weight, rstd_next are that norm's input,
     weight and statistic.  residual is needed only with residual_scale."""
+    if h is not None:
+        got = (_NATIVE or _native()).norm_backward(dout, h, weight, rstd, gate, residual, residual_scale, dy, out,
+                                                   next_weight, rstd_next, None if stream is None else _handle(stream))
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            raise SkError(got, "sk_norm_backward")
     torch = _torch()
     e, T, D, dev, types = _norm_shape(h, "h")
     _need(h, "h", types, (T, D), dev)

@@ -11,7 +11,11 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libskgemm.so")
 # device-ceiling probes for the roofline (bench.py --ceiling), a library of their own
 PROBE_LIB = os.path.join(HERE, "libskprobe.so")
-PROBE_SOURCES = ["sk_probe.hip"]
+PROBE_# the native binding of the block-scaled and norm calls: host code against torch's headers
+NATIVE = os.path.join(HERE, "_sknative.so")
+CXX = os.environ.get("CXX", "g++")
+
+SOURCES = ["sk_probe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["sk_kernels.hip", "sk_kernels_mx.hip", "sk_kernels_ksplit.hip", "sk_backward.hip", "sk_quantize.hip",
@@ -35,15 +39,30 @@ def build(verbose: bool = False) -> str:
             cmd.insert(2, "hip")
         cmds.append(cmd)
         objs.append(obj)
+    cmds.append(_native_command(NATIVE + ".tmp"))
     with ThreadPoolExecutor(max_workers=min(len(cmds), 5)) as ex:
         for f in [ex.submit(_run, c, verbose) for c in cmds]:
             f.result()
+    os.replace(NATIVE + ".tmp", NATIVE)
     n = len(SOURCES)
     for lib, lib_objs in ((LIB, objs[:n]), (PROBE_LIB, objs[n:])):
         tmp = lib + ".tmp"
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *lib_objs, "-o", tmp], verbose)
         os.replace(tmp, lib)
     return LIB
+
+
+def _native_command(out):
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    root = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + sysconfig.get_paths()["include"]]
+    for p in include_paths():
+        cmd += ["-isystem", p]
+    return cmd + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "sk_native.cpp"),
+                  "-o", out, "-L" + root, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def _run(cmd, verbose):

@@ -318,17 +318,26 @@ __global__ __launch_bounds__(64 * NWK) void sk_gemm_block_rows(BlockGemm g) {
     v4u a[U][MB][2], b[U][NB][2];
     float sa[U][MB];
     v4f sb[U][NB];
+    // all of B's first: they come from memory, A's from the caches
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * NWK;
-      const uint32_t at = (uint32_t)(k * kBlock + 32 * lg);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t c = at + 16u * h;
+        const int k = k0 + u * NWK;
+        const uint32_t c = (uint32_t)(k * kBlock + 16 * lg + 64 * h);
         const bool in = k < g.kb && c < rb;
 #pragma unroll
         for (int j = 0; j < NB; ++j)
           b[u][j][h] = __builtin_amdgcn_raw_buffer_load_b128(rbr, in ? (uint32_t)(j * 16 + lr) * rb + c : kOob, 0, 0);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * NWK;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c = (uint32_t)(k * kBlock + 16 * lg + 64 * h);
+        const bool in = k < g.kb && c < rb;
 #pragma unroll
         for (int i = 0; i < MB; ++i)
           a[u][i][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? (uint32_t)(i * 16 + lr) * rb + c : kOob, 0, 0);
