@@ -36,11 +36,11 @@ struct BlockCfg {
   static constexpr int STAGE = S_OFF + (BM + BN) * 4;
   static constexpr int OUT_WAVE = WTM * WTN * 2;                    // a wave's bf16 outputs
   static constexpr int CH = WTN / 8;                                // 16-byte chunks of an output row
-  static constexpr int LDS = STAGES * STAGE;
+  static constexpr int BIAS_OFF = STAGES * STAGE, LDS = BIAS_OFF + (BN < 128 ? 256 : 2 * BN);
   static_assert(A_PT * NW * 8 == BM && B_PT * NW * 8 == BN && NW % 2 == 0, "whole loads, 16-row periods");
   static_assert(S_INST <= NW, "one scale load per wave and stage");
   static_assert(WTM % 16 == 0 && WTN % 16 == 0 && WTN <= 128 && 128 % WTN == 0, "a wave's columns share a tile scale");
-  static_assert(NW * OUT_WAVE <= LDS && LDS <= 160 * 1024, "LDS");
+  static_assert(NW * OUT_WAVE <= BIAS_OFF && LDS <= 160 * 1024, "LDS");
   static_assert((STAGES - 1) * PER_STAGE <= 63, "vmcnt range");
 };
 
@@ -194,6 +194,14 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
       if constexpr (!BROW) sbt = *(const __attribute__((address_space(3))) float*)at(lsb);
     };
 
+    // the tile's bias goes the same way, two columns a lane (a lone last column, or a bias not on four bytes, would
+    // not: it is read when the outputs are made)
+    const bool bias_staged = (((uintptr_t)g.bias | (uintptr_t)(2 * g.N)) & 3) == 0;
+    const uint32_t bias_bytes = g.bias ? (uint32_t)cols * 2u : 0u;
+    constexpr int BI = (C::BN + 127) / 128;
+    if (bias_staged)
+      dma_load4(rsrc_words(g.bias + n0, bias_bytes), (uint32_t)((wave % BI) * 64 + lane) * 4u, 0u,
+                (uint32_t)(uintptr_t)smem + C::BIAS_OFF + (uint32_t)(wave % BI) * 256u);
 #pragma unroll
     for (int d = 0; d < C::STAGES; ++d) issue(d);
     wait_vmcnt_n<(C::STAGES - 1) * C::PER_STAGE>();
@@ -251,42 +259,60 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     int ol = lane;
     asm volatile("" : "+v"(ol));
     const int olr = ol & 15, olg = ol >> 4;
-    const __amdgpu_buffer_rsrc_t rc = make_rsrc(g.C + (int64_t)m0 * g.N, (uint32_t)rows * (uint32_t)g.N * 2u);
-    const bool staged = (g.N & 7) == 0;
     lds_u8* const so = smem + wave * C::OUT_WAVE;
+    v2u bias[C::FN];
+    if (bias_staged) {
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-      const int col = n0 + wn * C::WTN + j * 16 + 4 * olg;
-      float bias[4];
+      for (int j = 0; j < C::FN; ++j)
+        bias[j] = *(const __attribute__((address_space(3))) v2u*)(smem + C::BIAS_OFF + (wn * C::WTN + j * 16 + 4 * olg) * 2);
+    } else {
+      const __amdgpu_buffer_rsrc_t rbias = make_rsrc(g.bias + n0, bias_bytes);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        bias[k] = g.bias && col + k < g.N ? bits_f((uint32_t)g.bias[col + k] << 16) : 0.0f;
+      for (int j = 0; j < C::FN; ++j) {
+        uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i) {
-        const v2u h = out4(acc[i][j], bias);
-        const int row = i * 16 + olr;
-        if (staged) {
-          const int c = (2 * j + (olg >> 1)) ^ (row & (C::CH - 1));
-          *(__attribute__((address_space(3))) v2u*)(so + row * (C::WTN * 2) + c * 16 + (olg & 1) * 8) = h;
-        } else {
-          const uint32_t to = ((uint32_t)(wm * C::WTM + row) * (uint32_t)g.N + (uint32_t)col) * 2u;
-          const uint32_t v[4] = {h[0] & 0xffffu, h[0] >> 16, h[1] & 0xffffu, h[1] >> 16};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v[k], rc, col + k < g.N ? to + 2u * k : kOob, 0, 0);
-        }
+        for (int k = 0; k < 4; ++k)
+          w[k] = __builtin_amdgcn_raw_buffer_load_b16(rbias, (uint32_t)(wn * C::WTN + j * 16 + 4 * olg + k) * 2u, 0, 0);
+        bias[j] = v2u{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
       }
     }
-    if (staged) {
-      asm volatile("" ::: "memory");   // (one wave's LDS operations execute in order)
-      constexpr int RPI = 64 / C::CH;  // rows per store
-      const int c = ol % C::CH, col = n0 + wn * C::WTN + c * 8;
-      const uint32_t to = ((uint32_t)(wm * C::WTM + ol / C::CH) * (uint32_t)g.N + (uint32_t)col) * 2u;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const float b4[4] = {bf16_lo(bias[j][0]), bf16_hi(bias[j][0]), bf16_lo(bias[j][1]), bf16_hi(bias[j][1])};
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const int row = i * 16 + olr, c = (2 * j + (olg >> 1)) ^ (row & (C::CH - 1));
+        *(__attribute__((address_space(3))) v2u*)(so + row * (C::WTN * 2) + c * 16 + (olg & 1) * 8) = out4(acc[i][j], b4);
+      }
+    }
+    asm volatile("" ::: "memory");   // (one wave's LDS operations execute in order)
+    constexpr int RPI = 64 / C::CH;  // rows per store
+    const int c = ol % C::CH, col = n0 + wn * C::WTN + c * 8, orow = wm * C::WTM + ol / C::CH;
+    if ((g.N & 7) == 0) {
+      const __amdgpu_buffer_rsrc_t rc = make_rsrc(g.C + (int64_t)m0 * g.N, (uint32_t)rows * (uint32_t)g.N * 2u);
+      const uint32_t to = ((uint32_t)orow * (uint32_t)g.N + (uint32_t)col) * 2u;
 #pragma unroll
       for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
         const int row = r0 + ol / C::CH;
         const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
         __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < g.N ? to + (uint32_t)r0 * (uint32_t)g.N * 2u : kOob, 0, 0);
+      }
+    } else {
+      // rows that start anywhere: the same sixteen bytes to any element's address, the row's last piece by elements
+      uint16_t* const to = g.C + (int64_t)(m0 + orow) * g.N + col;
+#pragma unroll
+      for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
+        const int row = r0 + ol / C::CH;
+        const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
+        if (orow + r0 >= rows) continue;
+        uint16_t* const p = to + (int64_t)r0 * g.N;
+        if (col + 8 <= g.N) {
+          *(u32x4_any*)p = v;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (col + k < g.N) p[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
+        }
       }
     }
     if (t + (int)gridDim.x < T) lds_barrier();   // the next tile's loads go where the outputs were read from
