@@ -22,11 +22,12 @@ namespace sk {
 
 namespace {
 
-// A tile's 128-byte k-step of BM rows of A and BN of B over WM x WN waves.
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
+// A tile's 128-byte k-step of BM rows of A and BN of B over WM x WN waves; WK such groups of waves take every WK-th
+// block of K, each with a ring of its own, and their sums are added in group order at the end.
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int WK_ = 1>
 struct BlockCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
-  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_, WK = WK_;
+  static constexpr int NW = WM * WN, NT = 64 * NW * WK;             // waves of a group, threads of a workgroup
   static constexpr int WTM = BM / WM, WTN = BN / WN;
   static constexpr int FM = WTM / 16, FN = WTN / 16;
   static constexpr int A_PT = BM / 8 / NW, B_PT = BN / 8 / NW;      // 1 KiB loads (8 rows) per wave
@@ -36,12 +37,13 @@ struct BlockCfg {
   static constexpr int STAGE = S_OFF + (BM + BN) * 4;
   static constexpr int OUT_WAVE = WTM * WTN * 2;                    // a wave's bf16 outputs
   static constexpr int CH = WTN / 8;                                // 16-byte chunks of an output row
-  static constexpr int BIAS_OFF = STAGES * STAGE, LDS = BIAS_OFF + (BN < 128 ? 256 : 2 * BN);
+  static constexpr int RING = STAGES * STAGE, BIAS_OFF = WK * RING, LDS = BIAS_OFF + (BN < 128 ? 256 : 2 * BN);
   static_assert(A_PT * NW * 8 == BM && B_PT * NW * 8 == BN && NW % 2 == 0, "whole loads, 16-row periods");
   static_assert(S_INST <= NW, "one scale load per wave and stage");
   static_assert(WTM % 16 == 0 && WTN % 16 == 0 && WTN <= 128 && 128 % WTN == 0, "a wave's columns share a tile scale");
   static_assert(NW * OUT_WAVE <= BIAS_OFF && LDS <= 160 * 1024, "LDS");
   static_assert((STAGES - 1) * PER_STAGE <= 63, "vmcnt range");
+  static_assert(WK == 1 || NW * OUT_WAVE + (WK - 1) * BM * BN * 4 <= BIAS_OFF, "sums passed between the groups");
 };
 
 // Tile t of the launch as (tile row, tile column): workgroups are dealt to the eight XCDs in turn, so each
@@ -86,10 +88,12 @@ template <class C, bool BROW>
 __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
   __shared__ __attribute__((aligned(16))) uint8_t smem_raw[C::LDS];
   lds_u8* const smem = (lds_u8*)smem_raw;
-  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int lane = threadIdx.x & 63, wave = wave_id() % C::NW, group = wave_id() / C::NW;
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int lr = lane & 15, lg = lane >> 4;
   const uint32_t rb = (uint32_t)g.row_bytes;
+  const uint32_t ring = (uint32_t)(uintptr_t)smem + (uint32_t)group * C::RING;
+  const int steps = (g.kb + C::WK - 1) / C::WK;          // k-steps; step d of a group is block d WK + group
 
   // The lane's part of a direct load: slot lane % 8 of row lane / 8 of an 8-row group; every group of a wave
   // is a whole number of 16-row periods from the first, so they share the chunk.
@@ -130,12 +134,12 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
 
     // Load l of k-step d into stage d % STAGES; past the last one every lane is out of range (zeros, no traffic).
     // (The k-steps are issued in order: sat is the step's scales, advanced with its last load.)
-    int64_t sat = uniform((int64_t)(uintptr_t)sbase);
+    int64_t sat = uniform((int64_t)(uintptr_t)sbase) + group * sstep;
     auto issue_one = [&](int d, auto lc) {
       constexpr int l = decltype(lc)::value;
-      const uint32_t stage = (uint32_t)(uintptr_t)smem + (uint32_t)(d % C::STAGES) * C::STAGE;
-      const bool live = d < g.kb;
-      const uint32_t kbyte = live ? (uint32_t)d * kBlock : 0u;
+      const uint32_t stage = ring + (uint32_t)(d % C::STAGES) * C::STAGE;
+      const bool live = d * C::WK + group < g.kb;
+      const uint32_t kbyte = live ? (uint32_t)(d * C::WK + group) * kBlock : 0u;
       const uint32_t voff = live && kbyte < lim ? off : kOob;
       if constexpr (l < C::A_PT) {
         dma_load16(ra, voff, kbyte + l * gstep, stage + (uint32_t)(wave + l * C::NW) * 1024u);
@@ -144,7 +148,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
         dma_load16(rbw, voff, kbyte + i * gstep, stage + C::B_OFF + (uint32_t)(wave + i * C::NW) * 1024u);
       } else {
         dma_load4(rsrc_words((const void*)(uintptr_t)sat, sbytes), live ? svoff : kOob, 0u, stage + C::S_OFF + (uint32_t)sidx * 256u);
-        sat += live ? sstep : 0;
+        sat += live ? C::WK * sstep : 0;
       }
     };
     auto issue = [&](int d) { static_for<C::PER_STAGE>([&](auto lc) { issue_one(d, lc); }); };
@@ -172,7 +176,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     float sa[C::FM], sbt = 0.0f;
     // LDS addresses in the stage being read, moved on behind each barrier.  (Chunk 4 + lg is 64 bytes from chunk lg,
     // with the sign of one of the permutation's bits: an exclusive or, since rows are 128 bytes.)
-    const uint32_t base = (uint32_t)(uintptr_t)smem;
+    const uint32_t base = ring;
     uint32_t la = base + (wm * C::WTM + lr) * kBlock + c0, lb = base + C::B_OFF + (wn * C::WTN + lr) * kBlock + c0;
     uint32_t lsa = base + C::S_OFF + (wm * C::WTM + lr) * 4;
     uint32_t lsb = base + C::S_OFF + (C::BM + wn * C::WTN + (BROW ? 4 * lg : 0)) * 4;
@@ -186,6 +190,9 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
       constexpr int j = decltype(jc)::value;
       b[j % RING][0] = ld_v4u(at(lb) + j * 16 * kBlock);
       b[j % RING][1] = ld_v4u(at(lb ^ 64u) + j * 16 * kBlock);
+    };
+    auto read_sb = [&](auto jc) {
+      constexpr int j = decltype(jc)::value;
       if constexpr (BROW) sbv[j % RING] = ld_v4f(at(lsb) + j * 64);
     };
     auto read_scales = [&]() {
@@ -209,7 +216,8 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     read_scales();
     static_for<C::FM>(read_a);
     static_for<2>(read_b);
-    for (int d = 0; d < g.kb; ++d) {
+    static_for<2>(read_sb);
+    for (int d = 0; d < steps; ++d) {
       float s[C::FM];
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) s[i] = BROW ? sa[i] : sa[i] * sbt;
@@ -238,7 +246,9 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
         // the next pair's columns, once the last pair's are done with (a stage of one pair: in place)
         if constexpr (NP > 1 && (r == 2 || r == 3)) {
           read_b(std::integral_constant<int, (j + 2) % C::FN>{});
+          read_sb(std::integral_constant<int, (j + 2) % C::FN>{});
         }
+        if constexpr (NP == 1 && i == C::FM - 1) read_b(std::integral_constant<int, j>{});
         if constexpr (pair == NP - 1) {
           if constexpr (n % 2 == 1) read_a(std::integral_constant<int, i>{});
           static_for<C::PER_STAGE>([&](auto lc) {
@@ -249,7 +259,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
         __builtin_amdgcn_sched_barrier(0);
       });
       static_for<LAG>([&](auto lc) { add(std::integral_constant<int, NS - LAG + decltype(lc)::value>{}); });
-      if constexpr (NP == 1) static_for<2>(read_b);
+      if constexpr (NP == 1) static_for<2>(read_sb);
     }
 
     // outputs: each wave's through its own part of LDS, so that a store fills whole lines.  (The lane is read
@@ -259,7 +269,26 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     int ol = lane;
     asm volatile("" : "+v"(ol));
     const int olr = ol & 15, olg = ol >> 4;
+    if constexpr (C::WK > 1) {
+      // the other groups' sums through LDS (behind the output staging), added in group order by the first, which stores
+      lds_u8* const red = smem + C::NW * C::OUT_WAVE + (wave * C::FM * C::FN * 64 + lane) * 16;
+      if (group > 0) {
+        static_for<C::FM * C::FN>([&](auto nc) {
+          constexpr int n = decltype(nc)::value;
+          *(__attribute__((address_space(3))) v4f*)(red + (group - 1) * (C::BM * C::BN * 4) + n * 1024) = acc[n / C::FN][n % C::FN];
+        });
+      }
+      lds_barrier();
+      if (group == 0) {
+        static_for<C::FM * C::FN>([&](auto nc) {
+          constexpr int n = decltype(nc)::value;
+#pragma unroll
+          for (int k = 1; k < C::WK; ++k) acc[n / C::FN][n % C::FN] += ld_v4f(red + (k - 1) * (C::BM * C::BN * 4) + n * 1024);
+        });
+      }
+    }
     lds_u8* const so = smem + wave * C::OUT_WAVE;
+    if (group == 0) {
     v2u bias[C::FN];
     if (bias_staged) {
 #pragma unroll
@@ -314,6 +343,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
             if (col + k < g.N) p[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
         }
       }
+    }
     }
     if (t + (int)gridDim.x < T) lds_barrier();   // the next tile's loads go where the outputs were read from
   }
@@ -458,7 +488,8 @@ hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int 
   }
   auto tiles = [&](int bm, int bn) { return (int64_t)cdiv(g.M, bm) * cdiv(g.N, bn); };
   if (tiles(256, 256) * 4 >= (int64_t)cus * 3) return launch_tiled<BlockCfg<256, 256, 4, 2, 2>>(g, b_tile, grid_cap, cus, s);
-  if (tiles(128, 128) * 2 >= cus) return launch_tiled<BlockCfg<128, 128, 2, 2, 4>>(g, b_tile, grid_cap, cus, s);
+  if (tiles(128, 128) * 2 >= cus) return launch_tiled<BlockCfg<128, 128, 4, 2, 4>>(g, b_tile, grid_cap, cus, s);
+  if (tiles(64, 64) <= cus && g.kb >= 16) return launch_tiled<BlockCfg<64, 64, 2, 2, 4, 2>>(g, b_tile, grid_cap, cus, s);
   return launch_tiled<BlockCfg<64, 64, 2, 2, 4>>(g, b_tile, grid_cap, cus, s);
 }
 
