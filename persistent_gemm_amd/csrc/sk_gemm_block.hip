@@ -31,15 +31,15 @@ struct BlockCfg {
   static constexpr int WTM = BM / WM, WTN = BN / WN;
   static constexpr int FM = WTM / 16, FN = WTN / 16;
   static constexpr int A_PT = BM / 8 / NW, B_PT = BN / 8 / NW;      // 1 KiB loads (8 rows) per wave
-  static constexpr int S_INST = (BM + BN) / 64;                     // 256-byte scale loads of a stage
-  static constexpr int PER_STAGE = A_PT + B_PT + 1;
-  static constexpr int B_OFF = BM * kBlock, S_OFF = (BM + BN) * kBlock;
-  static constexpr int STAGE = S_OFF + (BM + BN) * 4;
+  static constexpr int S_A = (BM + 63) / 64, S_B = (BN + 63) / 64;  // 256-byte scale loads of a stage
+  static constexpr int S_PT = (S_A + S_B + NW - 1) / NW;            // ... per wave (past the last, one again)
+  static constexpr int PER_STAGE = A_PT + B_PT + S_PT;
+  static constexpr int B_OFF = BM * kBlock, S_OFF = (BM + BN) * kBlock, SB_OFF = S_OFF + S_A * 256;
+  static constexpr int STAGE = SB_OFF + S_B * 256;
   static constexpr int OUT_WAVE = WTM * WTN * 2;                    // a wave's bf16 outputs
   static constexpr int CH = WTN / 8;                                // 16-byte chunks of an output row
   static constexpr int RING = STAGES * STAGE, BIAS_OFF = WK * RING, LDS = BIAS_OFF + (BN < 128 ? 256 : 2 * BN);
-  static_assert(A_PT * NW * 8 == BM && B_PT * NW * 8 == BN && NW % 2 == 0, "whole loads, 16-row periods");
-  static_assert(S_INST <= NW, "one scale load per wave and stage");
+  static_assert(A_PT * NW * 8 == BM && B_PT * NW * 8 == BN, "whole loads");
   static_assert(WTM % 16 == 0 && WTN % 16 == 0 && WTN <= 128 && 128 % WTN == 0, "a wave's columns share a tile scale");
   static_assert(NW * OUT_WAVE <= BIAS_OFF && LDS <= 160 * 1024, "LDS");
   static_assert((STAGES - 1) * PER_STAGE <= 63, "vmcnt range");
@@ -95,12 +95,11 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
   const uint32_t ring = (uint32_t)(uintptr_t)smem + (uint32_t)group * C::RING;
   const int steps = (g.kb + C::WK - 1) / C::WK;          // k-steps; step d of a group is block d WK + group
 
-  // The lane's part of a direct load: slot lane % 8 of row lane / 8 of an 8-row group; every group of a wave
-  // is a whole number of 16-row periods from the first, so they share the chunk.
+  // The lane's part of a direct load: slot lane % 8 of row lane / 8 of an 8-row group.  A wave's next group is NW
+  // of them on: whole 16-row periods, the same chunk again, or with one wave half a period, the chunk 64 bytes away.
   const int grow = wave * 8 + (lane >> 3);
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ ((grow >> 1) & 7)) * 16);
-  const uint32_t lim = chunk < rb ? rb - chunk : 0u;     // k-step offsets at which the chunk lies in the row
-  const uint32_t off = (uint32_t)grow * rb + chunk;
+  const uint32_t row_off = (uint32_t)grow * rb;
   const uint32_t gstep = (uint32_t)(C::NW * 8) * rb;     // to the wave's next group, in the scalar offset
 
   // The lane's operand chunks lg and 4 + lg of row lr of each 16-row block.  (Any four a half will do that are the
@@ -109,9 +108,6 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
   // every bank twice.)
   const int sw = (lr >> 1) & 7;
   const int c0 = (lg ^ sw) * 16;
-
-  const int sidx = wave % C::S_INST;         // (waves past the last load repeat one: the same bytes to the same place)
-  const bool s_is_a = sidx < C::BM / 64;
 
   const int T = g.tiles_m * g.tiles_n;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
@@ -123,35 +119,49 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     const int rows = min(C::BM, g.M - m0), cols = min(C::BN, g.N - n0);
     const v4u ra = rsrc_words(g.A + (int64_t)m0 * rb, (uint32_t)rows * rb);
     const v4u rbw = rsrc_words(g.B + (int64_t)n0 * rb, (uint32_t)cols * rb);
-    // This wave's scale load of a stage, 64 floats: rows of A, or columns of B (element e of [A rows, B columns]),
-    // whose scale is their own or that of their 128 columns.  k-step d's are sstep floats after the last one's.
-    const int e = sidx * 64 + lane, j = e - C::BM, nb = n0 % kBlock;
-    const float* const sbase = s_is_a ? g.SA + m0 : BROW ? g.SB + n0 : g.SB + (int64_t)(n0 / kBlock) * g.kb;
-    const int64_t sstep = 4 * uniform(s_is_a ? g.M : BROW ? g.N : 1);
-    const uint32_t sbytes = (uint32_t)uniform(s_is_a ? rows : BROW ? cols : g.kb * ((nb + cols - 1) / kBlock + 1)) * 4u;
-    const uint32_t svoff = s_is_a ? (e < rows ? (uint32_t)e * 4u : kOob)
-                         : j >= cols ? kOob : (uint32_t)(BROW ? j : (nb + j) / kBlock * g.kb) * 4u;
+    // This wave's scale loads of a stage, 64 floats each: rows of A, or columns of B, whose scale is their own or
+    // that of their 128 columns.  The k-steps are issued in order: sat is where the next one's are, sstep bytes on
+    // from the last block's.
+    int64_t sat[C::S_PT], sstep[C::S_PT];
+    uint32_t sbytes[C::S_PT], svoff[C::S_PT], slds[C::S_PT];
+#pragma unroll
+    for (int i = 0; i < C::S_PT; ++i) {
+      const int idx = (wave + i * C::NW) % (C::S_A + C::S_B);
+      const bool is_a = idx < C::S_A;
+      const int e = (is_a ? idx : idx - C::S_A) * 64 + lane, nb = n0 % kBlock;
+      const float* const from = is_a ? g.SA + m0 : BROW ? g.SB + n0 : g.SB + (int64_t)(n0 / kBlock) * g.kb;
+      sstep[i] = 4 * uniform(is_a ? g.M : BROW ? g.N : 1);
+      sat[i] = uniform((int64_t)(uintptr_t)from) + group * sstep[i];
+      sbytes[i] = (uint32_t)uniform(is_a ? rows : BROW ? cols : g.kb * ((nb + cols - 1) / kBlock + 1)) * 4u;
+      svoff[i] = e >= (is_a ? rows : cols) ? kOob : (uint32_t)(is_a || BROW ? e : (nb + e) / kBlock * g.kb) * 4u;
+      slds[i] = C::S_OFF + (uint32_t)idx * 256u;
+    }
 
-    // Load l of k-step d into stage d % STAGES; past the last one every lane is out of range (zeros, no traffic).
-    // (The k-steps are issued in order: sat is the step's scales, advanced with its last load.)
-    int64_t sat = uniform((int64_t)(uintptr_t)sbase) + group * sstep;
+    // Load l of k-step d into stage d % STAGES; past the last block every lane is out of range (zeros, no traffic).
     auto issue_one = [&](int d, auto lc) {
       constexpr int l = decltype(lc)::value;
       const uint32_t stage = ring + (uint32_t)(d % C::STAGES) * C::STAGE;
       const bool live = d * C::WK + group < g.kb;
       const uint32_t kbyte = live ? (uint32_t)(d * C::WK + group) * kBlock : 0u;
-      const uint32_t voff = live && kbyte < lim ? off : kOob;
-      if constexpr (l < C::A_PT) {
-        dma_load16(ra, voff, kbyte + l * gstep, stage + (uint32_t)(wave + l * C::NW) * 1024u);
-      } else if constexpr (l < C::A_PT + C::B_PT) {
-        constexpr int i = l - C::A_PT;
-        dma_load16(rbw, voff, kbyte + i * gstep, stage + C::B_OFF + (uint32_t)(wave + i * C::NW) * 1024u);
+      if constexpr (l < C::A_PT + C::B_PT) {
+        constexpr bool is_a = l < C::A_PT;
+        constexpr int i = is_a ? l : l - C::A_PT;
+        const uint32_t c = chunk ^ (C::NW % 2 && i % 2 ? 64u : 0u);
+        const uint32_t voff = live && kbyte + c < rb ? row_off + c : kOob;
+        dma_load16(is_a ? ra : rbw, voff, kbyte + i * gstep,
+                   stage + (is_a ? 0u : C::B_OFF) + (uint32_t)(wave + i * C::NW) * 1024u);
       } else {
-        dma_load4(rsrc_words((const void*)(uintptr_t)sat, sbytes), live ? svoff : kOob, 0u, stage + C::S_OFF + (uint32_t)sidx * 256u);
-        sat += live ? C::WK * sstep : 0;
+        constexpr int i = l - C::A_PT - C::B_PT;
+        dma_load4(rsrc_words((const void*)(uintptr_t)sat[i], sbytes[i]), live ? svoff[i] : kOob, 0u, stage + slds[i]);
+        sat[i] += live ? C::WK * sstep[i] : 0;
       }
     };
     auto issue = [&](int d) { static_for<C::PER_STAGE>([&](auto lc) { issue_one(d, lc); }); };
+    // Waves of a group meet (one alone only waits for its own LDS reads)
+    auto meet = [&]() {
+      if constexpr (C::NW > 1) lds_barrier();
+      else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
 
     v4f acc[C::FM][C::FN];
 #pragma unroll
@@ -179,7 +189,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
     const uint32_t base = ring;
     uint32_t la = base + (wm * C::WTM + lr) * kBlock + c0, lb = base + C::B_OFF + (wn * C::WTN + lr) * kBlock + c0;
     uint32_t lsa = base + C::S_OFF + (wm * C::WTM + lr) * 4;
-    uint32_t lsb = base + C::S_OFF + (C::BM + wn * C::WTN + (BROW ? 4 * lg : 0)) * 4;
+    uint32_t lsb = base + C::SB_OFF + (wn * C::WTN + (BROW ? 4 * lg : 0)) * 4;
     auto at = [](uint32_t x) { return (const lds_u8*)(uintptr_t)x; };
     auto read_a = [&](auto ic) {
       constexpr int i = decltype(ic)::value;
@@ -212,7 +222,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
 #pragma unroll
     for (int d = 0; d < C::STAGES; ++d) issue(d);
     wait_vmcnt_n<(C::STAGES - 1) * C::PER_STAGE>();
-    lds_barrier();
+    meet();
     read_scales();
     static_for<C::FM>(read_a);
     static_for<2>(read_b);
@@ -232,7 +242,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
         constexpr int n = decltype(nc)::value, r = n % PS, i = r / 2, pair = n / PS, j = pair * 2 + n % 2;
         if constexpr (r == 0 && pair == NP - 1) {
           wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE>();
-          lds_barrier();
+          meet();
           const uint32_t move = (uint32_t)((d + 1) % C::STAGES ? C::STAGE : -(C::STAGES - 1) * C::STAGE);
           la += move;
           lb += move;
@@ -275,7 +285,8 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
       if (group > 0) {
         static_for<C::FM * C::FN>([&](auto nc) {
           constexpr int n = decltype(nc)::value;
-          *(__attribute__((address_space(3))) v4f*)(red + (group - 1) * (C::BM * C::BN * 4) + n * 1024) = acc[n / C::FN][n % C::FN];
+          *(__attribute__((address_space(3))) v4f*)(red + (group - 1) * (C::BM * C::BN * 4) + n * 1024) =
+              acc[n / C::FN][n % C::FN];
         });
       }
       lds_barrier();
@@ -283,68 +294,71 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
         static_for<C::FM * C::FN>([&](auto nc) {
           constexpr int n = decltype(nc)::value;
 #pragma unroll
-          for (int k = 1; k < C::WK; ++k) acc[n / C::FN][n % C::FN] += ld_v4f(red + (k - 1) * (C::BM * C::BN * 4) + n * 1024);
+          for (int k = 1; k < C::WK; ++k)
+            acc[n / C::FN][n % C::FN] += ld_v4f(red + (k - 1) * (C::BM * C::BN * 4) + n * 1024);
         });
       }
     }
     lds_u8* const so = smem + wave * C::OUT_WAVE;
-    if (group == 0) {
-    v2u bias[C::FN];
-    if (bias_staged) {
+    auto finish = [&]() {
+      v2u bias[C::FN];
+      if (bias_staged) {
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-        bias[j] = *(const __attribute__((address_space(3))) v2u*)(smem + C::BIAS_OFF + (wn * C::WTN + j * 16 + 4 * olg) * 2);
-    } else {
-      const __amdgpu_buffer_rsrc_t rbias = make_rsrc(g.bias + n0, bias_bytes);
+        for (int j = 0; j < C::FN; ++j)
+          bias[j] =
+              *(const __attribute__((address_space(3))) v2u*)(smem + C::BIAS_OFF + (wn * C::WTN + j * 16 + 4 * olg) * 2);
+      } else {
+        const __amdgpu_buffer_rsrc_t rbias = make_rsrc(g.bias + n0, bias_bytes);
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        uint32_t w[4];
+        for (int j = 0; j < C::FN; ++j) {
+          uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = __builtin_amdgcn_raw_buffer_load_b16(rbias, (uint32_t)(wn * C::WTN + j * 16 + 4 * olg + k) * 2u, 0, 0);
-        bias[j] = v2u{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-      const float b4[4] = {bf16_lo(bias[j][0]), bf16_hi(bias[j][0]), bf16_lo(bias[j][1]), bf16_hi(bias[j][1])};
-#pragma unroll
-      for (int i = 0; i < C::FM; ++i) {
-        const int row = i * 16 + olr, c = (2 * j + (olg >> 1)) ^ (row & (C::CH - 1));
-        *(__attribute__((address_space(3))) v2u*)(so + row * (C::WTN * 2) + c * 16 + (olg & 1) * 8) = out4(acc[i][j], b4);
-      }
-    }
-    asm volatile("" ::: "memory");   // (one wave's LDS operations execute in order)
-    constexpr int RPI = 64 / C::CH;  // rows per store
-    const int c = ol % C::CH, col = n0 + wn * C::WTN + c * 8, orow = wm * C::WTM + ol / C::CH;
-    if ((g.N & 7) == 0) {
-      const __amdgpu_buffer_rsrc_t rc = make_rsrc(g.C + (int64_t)m0 * g.N, (uint32_t)rows * (uint32_t)g.N * 2u);
-      const uint32_t to = ((uint32_t)orow * (uint32_t)g.N + (uint32_t)col) * 2u;
-#pragma unroll
-      for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
-        const int row = r0 + ol / C::CH;
-        const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
-        __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < g.N ? to + (uint32_t)r0 * (uint32_t)g.N * 2u : kOob, 0, 0);
-      }
-    } else {
-      // rows that start anywhere: the same sixteen bytes to any element's address, the row's last piece by elements
-      uint16_t* const to = g.C + (int64_t)(m0 + orow) * g.N + col;
-#pragma unroll
-      for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
-        const int row = r0 + ol / C::CH;
-        const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
-        if (orow + r0 >= rows) continue;
-        uint16_t* const p = to + (int64_t)r0 * g.N;
-        if (col + 8 <= g.N) {
-          *(u32x4_any*)p = v;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (col + k < g.N) p[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
+          for (int k = 0; k < 4; ++k)
+            w[k] = __builtin_amdgcn_raw_buffer_load_b16(rbias, (uint32_t)(wn * C::WTN + j * 16 + 4 * olg + k) * 2u, 0, 0);
+          bias[j] = v2u{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
         }
       }
-    }
-    }
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        const float b4[4] = {bf16_lo(bias[j][0]), bf16_hi(bias[j][0]), bf16_lo(bias[j][1]), bf16_hi(bias[j][1])};
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+          const int row = i * 16 + olr, c = (2 * j + (olg >> 1)) ^ (row & (C::CH - 1));
+          *(__attribute__((address_space(3))) v2u*)(so + row * (C::WTN * 2) + c * 16 + (olg & 1) * 8) = out4(acc[i][j], b4);
+        }
+      }
+      asm volatile("" ::: "memory");   // (one wave's LDS operations execute in order)
+      constexpr int RPI = 64 / C::CH;  // rows per store
+      const int c = ol % C::CH, col = n0 + wn * C::WTN + c * 8, orow = wm * C::WTM + ol / C::CH;
+      if ((g.N & 7) == 0) {
+        const __amdgpu_buffer_rsrc_t rc = make_rsrc(g.C + (int64_t)m0 * g.N, (uint32_t)rows * (uint32_t)g.N * 2u);
+        const uint32_t to = ((uint32_t)orow * (uint32_t)g.N + (uint32_t)col) * 2u;
+#pragma unroll
+        for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
+          const int row = r0 + ol / C::CH;
+          const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
+          __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < g.N ? to + (uint32_t)r0 * (uint32_t)g.N * 2u : kOob, 0, 0);
+        }
+      } else {
+        // rows that start anywhere: the same sixteen bytes to any element's address, the row's last piece by elements
+        uint16_t* const to = g.C + (int64_t)(m0 + orow) * g.N + col;
+#pragma unroll
+        for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
+          const int row = r0 + ol / C::CH;
+          const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
+          if (orow + r0 >= rows) continue;
+          uint16_t* const p = to + (int64_t)r0 * g.N;
+          if (col + 8 <= g.N) {
+            *(u32x4_any*)p = v;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (col + k < g.N) p[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
+          }
+        }
+      }
+    };
+    if (group == 0) finish();
     if (t + (int)gridDim.x < T) lds_barrier();   // the next tile's loads go where the outputs were read from
   }
 }
@@ -480,17 +494,32 @@ hipError_t launch_rows(BlockGemm g, bool b_tile, hipStream_t s) {
 
 }  // namespace
 
+// The kernel by how many tiles of each shape there are to `cus` compute units (times below: 256 of them).  A tile
+// twice as large reads half as much for each product, so the largest shape that keeps most units busy is
+// taken; below that, the smallest tiles that still run all at once, with waves sharing out K to shorten it.
 hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int cus, hipStream_t s) {
-  if (grid_cap <= 0) {
-    if (g.M <= 16) return launch_rows<1, 1, 8, 4>(g, b_tile, s);
-    if (g.M <= 32) return launch_rows<2, 1, 8, 4>(g, b_tile, s);
-    if (g.M <= 64) return launch_rows<4, 2, 8, 2>(g, b_tile, s);
-  }
+  if (grid_cap > 0 && grid_cap < cus) cus = grid_cap;
   auto tiles = [&](int bm, int bn) { return (int64_t)cdiv(g.M, bm) * cdiv(g.N, bn); };
-  if (tiles(256, 256) * 4 >= (int64_t)cus * 3) return launch_tiled<BlockCfg<256, 256, 4, 2, 2>>(g, b_tile, grid_cap, cus, s);
-  if (tiles(128, 128) * 2 >= cus) return launch_tiled<BlockCfg<128, 128, 4, 2, 4>>(g, b_tile, grid_cap, cus, s);
-  if (tiles(64, 64) <= cus && g.kb >= 16) return launch_tiled<BlockCfg<64, 64, 2, 2, 4, 2>>(g, b_tile, grid_cap, cus, s);
-  return launch_tiled<BlockCfg<64, 64, 2, 2, 4>>(g, b_tile, grid_cap, cus, s);
+  auto go = [&](auto cfg) { return launch_tiled<decltype(cfg)>(g, b_tile, grid_cap, cus, s); };
+  // A's rows come from the caches once for every 16 columns here and once for 32 there, B's straight to registers:
+  // 1x4096x4096 6.2 against 7.2 us, 16x1024x1024 4.3 / 4.8, but 16x8192x8192 18.7 / 14.7
+  if (grid_cap <= 0 && (g.M <= 8 || (g.M <= 16 && (int64_t)g.N * g.row_bytes <= (8 << 20))))
+    return launch_rows<1, 1, 8, 4>(g, b_tile, s);
+  // 512x512x8192 10.7 us against 14.8 with 64x32 tiles and 15.8 with 64x64
+  if (g.M <= 32 || tiles(32, 32) <= cus) return go(BlockCfg<32, 32, 1, 1, 3, 4>{});
+  // 500x700x900 5.7 us against 6.4 with 64x64 tiles, 100x4096x4096 9.8 / 10.3
+  if (g.M <= 64 || tiles(64, 32) <= cus) return go(BlockCfg<64, 32, 2, 1, 3, 2>{});
+  // two groups of waves pay from 16 blocks on: 128x8192x8192 28.3 -> 25.4 us, but 1024x1024x1024 6.0 -> 6.6
+  if (tiles(64, 64) <= cus && g.kb >= 16) return go(BlockCfg<64, 64, 2, 2, 4, 2>{});
+  // 3000x4100x2060 (204 tiles) 40.6 us against 48.0 with 256x128 and 50.8 with 128x128
+  if (tiles(256, 256) * 4 >= (int64_t)cus * 3) return go(BlockCfg<256, 256, 4, 2, 2>{});
+  // 4096x2048x4096 39.7 us against 41.7 with 128x128 tiles and 57.9 with 256x256
+  if (tiles(256, 128) * 4 >= (int64_t)cus * 3) return go(BlockCfg<256, 128, 4, 2, 3>{});
+  // more than one to a unit: two at once, on half the stages (3000x2000x1000 18.8 -> 15.2 us)
+  if (tiles(128, 128) > cus) return go(BlockCfg<128, 128, 4, 2, 2>{});
+  // 777x4096x2048 14.0 us against 20.6 with 64x64 tiles; 1037x1290x2064 (99 tiles) 15.8 / 13.8
+  if (tiles(128, 128) * 2 >= cus) return go(BlockCfg<128, 128, 4, 2, 4>{});
+  return go(BlockCfg<64, 64, 2, 2, 4>{});
 }
 
 }  // namespace sk
