@@ -40,9 +40,9 @@ bool elem_ok(int e) { return e == SK_ELEM_BF16 || e == SK_ELEM_F32; }
 bool block_ok(int b) { return b == SK_BLOCK_ROW || b == SK_BLOCK_TILE; }
 int64_t elem_size(int e) { return e == SK_ELEM_F32 ? 4 : 2; }
 
-// One product on the stream (checked arguments).
-sk_status product(const void* A, const void* B, const float* sa, const float* sb, bool b_tile, const void* bias,
-                  void* C, int64_t M, int64_t N, int64_t K, int grid_cap, int cus, hipStream_t s) {
+// One product (checked arguments).
+sk::BlockGemm product(const void* A, const void* B, const float* sa, const float* sb, const void* bias, void* C,
+                      int64_t M, int64_t N, int64_t K) {
   sk::BlockGemm g;
   std::memset(&g, 0, sizeof(g));
   g.A = (const uint8_t*)A;
@@ -55,8 +55,10 @@ sk_status product(const void* A, const void* B, const float* sa, const float* sb
   g.N = (int)N;
   g.row_bytes = (int)K;
   g.kb = (int)cdiv(K, 128);
-  return sk::launch_gemm_block(g, b_tile, grid_cap, cus, s) == hipSuccess ? SK_OK : SK_ERR_HIP;
+  return g;
 }
+
+sk_status ok(hipError_t e) { return e == hipSuccess ? SK_OK : SK_ERR_HIP; }
 
 }  // namespace
 
@@ -116,7 +118,8 @@ sk_status sk_gemm_fp8_block(const void* A, const void* B, const float* A_scale, 
   int dev = 0, cus = 0;
   sk_status st = sk::host::device_for((hipStream_t)stream, &dev, &cus);
   if (st != SK_OK) return st;
-  return product(A, B, A_scale, B_scale, tile, bias, C, M, N, K, grid_cap, cus, (hipStream_t)stream);
+  return ok(sk::launch_gemm_block(product(A, B, A_scale, B_scale, bias, C, M, N, K), tile, grid_cap, cus,
+                                  (hipStream_t)stream));
 }
 
 sk_status sk_gemm_fp8_block_backward(const void* dC, const void* At, const float* At_scale, const void* Bt,
@@ -168,16 +171,13 @@ sk_status sk_gemm_fp8_block_backward(const void* dC, const void* At, const float
   a.kb = (int)nb;
   a.rb = (int)mb;
   if (sk::launch_quantize_block(a, false, false, s) != hipSuccess) return SK_ERR_HIP;
-  if (dA) {
-    st = product(a.q, Bt, a.scale, Bt_scale, true, nullptr, dA, M, K, np, grid_cap, cus, s);
-    if (st != SK_OK) return st;
-  }
-  if (dB) {
-    st = product(a.qt, At, a.scale_t, At_scale, false, nullptr, dB, N, K, mp, grid_cap, cus, s);
-    if (st != SK_OK) return st;
-  }
-  if (dbias && sk::launch_column_sums_bf16(a.part, (uint16_t*)dbias, (int)mb, (int)N, s) != hipSuccess) return SK_ERR_HIP;
-  return SK_OK;
+  const sk::ColumnSums sums{a.part, (uint16_t*)dbias, (int)mb, (int)N};
+  const sk::BlockGemm ga = product(a.q, Bt, a.scale, Bt_scale, nullptr, dA, M, K, np);
+  const sk::BlockGemm gb = product(a.qt, At, a.scale_t, At_scale, nullptr, dB, N, K, mp);
+  if ((dA || dB) && grid_cap <= 0) return ok(sk::launch_gemm_block_pair(ga, gb, sums, cus, s));
+  if (dA && sk::launch_gemm_block(ga, true, grid_cap, cus, s) != hipSuccess) return SK_ERR_HIP;
+  if (dB && sk::launch_gemm_block(gb, false, grid_cap, cus, s) != hipSuccess) return SK_ERR_HIP;
+  return dbias ? ok(sk::launch_column_sums_bf16(sums, s)) : SK_OK;
 }
 
 sk_status sk_norm_forward(const sk_norm_args* p) {

@@ -238,6 +238,15 @@ struct BlockGemm {
   int kb;                 // ceil(K / 128)
   int tiles_m, tiles_n;
 };
+// out[n] = bf16 of the sum over `count` rows of part [count][N], in a fixed order (out NULL: none).
+struct ColumnSums {
+  const float* part;
+  uint16_t* out;
+  int count, N;
+};
+hipError_t launch_column_sums_bf16(const ColumnSums& c, hipStream_t s);
+// a with B's scales per tile, b with them per row (either without C: not computed), and c, as one launch.
+hipError_t launch_gemm_block_pair(const BlockGemm& a, const BlockGemm& b, const ColumnSums& c, int cus, hipStream_t s);
 hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int cus, hipStream_t s);
 
 // The norms (sk_norm.hip).  Pointers are NULL where a part is absent; T is one of bf16 / fp32.
@@ -288,7 +297,5 @@ struct NormGradArgs {
 int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus);
 hipError_t launch_norm_backward(const NormGradArgs& a, bool f32, hipStream_t s);
 constexpr int kMaxNormWidth = 32768;
-// out[d] = bf16 of the sum over `count` rows of part [count][D], in a fixed order.
-hipError_t launch_column_sums_bf16(const float* part, uint16_t* out, int count, int D, hipStream_t s);
 
 }  // namespace sk

@@ -79,15 +79,36 @@ __device__ __forceinline__ v4f block_mfma(const v4u (&b)[2], const v4u (&a)[2]) 
 __device__ __forceinline__ v4f ld_v4f(const lds_u8* p) { return *(const __attribute__((address_space(3))) v4f*)p; }
 __device__ __forceinline__ v4u ld_v4u(const lds_u8* p) { return *(const __attribute__((address_space(3))) v4u*)p; }
 
+// out[n] = bf16 of the sum of part's rows at column n, in an order that does not depend on NT: slice k of kSumSlices
+// adds its run of rows in turn, then the runs are added in turn.  A workgroup takes NT / kSumSlices columns.
+constexpr int kSumSlices = 16;
+template <int NT>
+__device__ __forceinline__ void column_sums_bf16(const ColumnSums& c, int block, float* run) {
+  constexpr int COLS = NT / kSumSlices;
+  const int col = threadIdx.x % COLS, slice = threadIdx.x / COLS, n = block * COLS + col;
+  const int per = (c.count + kSumSlices - 1) / kSumSlices, c0 = slice * per, c1 = min(c.count, c0 + per);
+  float s = 0.0f;
+  if (n < c.N) {
+#pragma unroll 4
+    for (int r = c0; r < c1; ++r) s += c.part[(int64_t)r * c.N + n];
+  }
+  run[threadIdx.x] = s;
+  __syncthreads();
+  if (slice || n >= c.N) return;
+  float x = run[col];
+#pragma unroll
+  for (int k = 1; k < kSumSlices; ++k) x += run[k * COLS + col];
+  c.out[n] = (uint16_t)pack_bf16(x, x);
+}
+
 // Four outputs of a row: sums plus bias, rounded once to bf16 (the sum with the bias is one more fp32 addition).
 __device__ __forceinline__ v2u out4(const v4f& x, const float (&b)[4]) {
   return v2u{pack_bf16(x[0] + b[0], x[1] + b[1]), pack_bf16(x[2] + b[2], x[3] + b[3])};
 }
 
+// Tiles first, first + stride, ... of one product.
 template <class C, bool BROW>
-__global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem_raw[C::LDS];
-  lds_u8* const smem = (lds_u8*)smem_raw;
+__device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const smem, int first, int stride) {
   const int lane = threadIdx.x & 63, wave = wave_id() % C::NW, group = wave_id() / C::NW;
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int lr = lane & 15, lg = lane >> 4;
@@ -110,7 +131,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
   const int c0 = (lg ^ sw) * 16;
 
   const int T = g.tiles_m * g.tiles_n;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+  for (int t = first; t < T; t += stride) {
     int tm, tn;
     tile_of<C::BM >= 256 ? 4 : 8>(t, g.tiles_m, g.tiles_n, &tm, &tn);
     tm = __builtin_amdgcn_readfirstlane(tm);
@@ -359,8 +380,30 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
       }
     };
     if (group == 0) finish();
-    if (t + (int)gridDim.x < T) lds_barrier();   // the next tile's loads go where the outputs were read from
+    if (t + stride < T) lds_barrier();   // the next tile's loads go where the outputs were read from
   }
+}
+
+template <class C, bool BROW>
+__global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
+  block_tiles<C, BROW>(g, (lds_u8*)smem, blockIdx.x, gridDim.x);
+}
+
+// The two products of a backward and the last pass of its column sums as one launch: the second product's tiles start
+// as the first's end, and a small problem's three parts run side by side.
+template <class C>
+__global__ __launch_bounds__(C::NT) void sk_gemm_block_pair(BlockGemm a, BlockGemm b, ColumnSums c) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
+  const int ta = a.tiles_m * a.tiles_n, tb = b.tiles_m * b.tiles_n, wg = blockIdx.x;
+  if (wg < ta) block_tiles<C, false>(a, (lds_u8*)smem, wg, ta);
+  else if (wg < ta + tb) block_tiles<C, true>(b, (lds_u8*)smem, wg - ta, tb);
+  else column_sums_bf16<C::NT>(c, wg - ta - tb, (float*)smem);
+}
+template <int NT>
+__global__ __launch_bounds__(NT) void sk_column_sums(ColumnSums c) {
+  __shared__ float run[NT];
+  column_sums_bf16<NT>(c, blockIdx.x, run);
 }
 
 // Few rows of A: a workgroup takes 16 NB columns and 16 MB rows, and its NWK waves share out the blocks of K
@@ -471,7 +514,7 @@ __global__ __launch_bounds__(64 * NWK) void sk_gemm_block_rows(BlockGemm g) {
 }
 
 template <class C>
-hipError_t launch_tiled(BlockGemm g, bool b_tile, int grid_cap, int cus, hipStream_t s) {
+hipError_t launch_tiled(BlockGemm g, bool b_tile, int grid_cap, hipStream_t s) {
   g.tiles_m = cdiv(g.M, C::BM);
   g.tiles_n = cdiv(g.N, C::BN);
   const int64_t T = (int64_t)g.tiles_m * g.tiles_n;
@@ -492,25 +535,31 @@ hipError_t launch_rows(BlockGemm g, bool b_tile, hipStream_t s) {
   return hipGetLastError();
 }
 
-}  // namespace
+template <class C>
+hipError_t launch_pair(BlockGemm a, BlockGemm b, const ColumnSums& c, hipStream_t s) {
+  for (BlockGemm* g : {&a, &b}) {
+    g->tiles_m = g->C ? cdiv(g->M, C::BM) : 0;
+    g->tiles_n = g->C ? cdiv(g->N, C::BN) : 0;
+  }
+  const int64_t sums = c.out ? cdiv(c.N, C::NT / kSumSlices) : 0;
+  const int64_t grid = (int64_t)a.tiles_m * a.tiles_n + (int64_t)b.tiles_m * b.tiles_n + sums;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((sk_gemm_block_pair<C>), dim3((unsigned)grid), dim3(C::NT), 0, s, a, b, c);
+  return hipGetLastError();
+}
 
-// The kernel by how many tiles of each shape there are to `cus` compute units (times below: 256 of them).  A tile
+// The tile by how many of each shape there are to `cus` compute units (times below: 256 of them, one product).  A tile
 // twice as large reads half as much for each product, so the largest shape that keeps most units busy is
 // taken; below that, the smallest tiles that still run all at once, with waves sharing out K to shorten it.
-hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int cus, hipStream_t s) {
-  if (grid_cap > 0 && grid_cap < cus) cus = grid_cap;
-  auto tiles = [&](int bm, int bn) { return (int64_t)cdiv(g.M, bm) * cdiv(g.N, bn); };
-  auto go = [&](auto cfg) { return launch_tiled<decltype(cfg)>(g, b_tile, grid_cap, cus, s); };
-  // A's rows come from the caches once for every 16 columns here and once for 32 there, B's straight to registers:
-  // 1x4096x4096 6.2 against 7.2 us, 16x1024x1024 4.3 / 4.8, but 16x8192x8192 18.7 / 14.7
-  if (grid_cap <= 0 && (g.M <= 8 || (g.M <= 16 && (int64_t)g.N * g.row_bytes <= (8 << 20))))
-    return launch_rows<1, 1, 8, 4>(g, b_tile, s);
+// (kb: the product's blocks of K; rows: its rows.)
+template <class Tiles, class Go>
+hipError_t choose_tile(Tiles&& tiles, int rows, int kb, int cus, Go&& go) {
   // 512x512x8192 10.7 us against 14.8 with 64x32 tiles and 15.8 with 64x64
-  if (g.M <= 32 || tiles(32, 32) <= cus) return go(BlockCfg<32, 32, 1, 1, 3, 4>{});
+  if (rows <= 32 || tiles(32, 32) <= cus) return go(BlockCfg<32, 32, 1, 1, 3, 4>{});
   // 500x700x900 5.7 us against 6.4 with 64x64 tiles, 100x4096x4096 9.8 / 10.3
-  if (g.M <= 64 || tiles(64, 32) <= cus) return go(BlockCfg<64, 32, 2, 1, 3, 2>{});
+  if (rows <= 64 || tiles(64, 32) <= cus) return go(BlockCfg<64, 32, 2, 1, 3, 2>{});
   // two groups of waves pay from 16 blocks on: 128x8192x8192 28.3 -> 25.4 us, but 1024x1024x1024 6.0 -> 6.6
-  if (tiles(64, 64) <= cus && g.kb >= 16) return go(BlockCfg<64, 64, 2, 2, 4, 2>{});
+  if (tiles(64, 64) <= cus && kb >= 16) return go(BlockCfg<64, 64, 2, 2, 4, 2>{});
   // 3000x4100x2060 (204 tiles) 40.6 us against 48.0 with 256x128 and 50.8 with 128x128
   if (tiles(256, 256) * 4 >= (int64_t)cus * 3) return go(BlockCfg<256, 256, 4, 2, 2>{});
   // 4096x2048x4096 39.7 us against 41.7 with 128x128 tiles and 57.9 with 256x256
@@ -520,6 +569,33 @@ hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int 
   // 777x4096x2048 14.0 us against 20.6 with 64x64 tiles; 1037x1290x2064 (99 tiles) 15.8 / 13.8
   if (tiles(128, 128) * 2 >= cus) return go(BlockCfg<128, 128, 4, 2, 4>{});
   return go(BlockCfg<64, 64, 2, 2, 4>{});
+}
+
+}  // namespace
+
+hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int cus, hipStream_t s) {
+  if (grid_cap > 0 && grid_cap < cus) cus = grid_cap;
+  // A's rows come from the caches once for every 16 columns here and once for 32 in a tile, B's straight to registers:
+  // 1x4096x4096 6.2 against 7.2 us, 16x1024x1024 4.3 / 4.8, but 16x8192x8192 18.7 / 14.7
+  if (grid_cap <= 0 && (g.M <= 8 || (g.M <= 16 && (int64_t)g.N * g.row_bytes <= (8 << 20))))
+    return launch_rows<1, 1, 8, 4>(g, b_tile, s);
+  auto tiles = [&](int bm, int bn) { return (int64_t)cdiv(g.M, bm) * cdiv(g.N, bn); };
+  return choose_tile(tiles, g.M, g.kb, cus, [&](auto cfg) { return launch_tiled<decltype(cfg)>(g, b_tile, grid_cap, s); });
+}
+
+// (the tile is the two products' together also where only one is wanted, so that its bits are the same)
+hipError_t launch_gemm_block_pair(const BlockGemm& a, const BlockGemm& b, const ColumnSums& c, int cus, hipStream_t s) {
+  auto tiles = [&](int bm, int bn) {
+    return (int64_t)cdiv(a.M, bm) * cdiv(a.N, bn) + (int64_t)cdiv(b.M, bm) * cdiv(b.N, bn);
+  };
+  const int rows = a.M > b.M ? a.M : b.M, kb = a.kb < b.kb ? a.kb : b.kb;
+  return choose_tile(tiles, rows, kb, cus, [&](auto cfg) { return launch_pair<decltype(cfg)>(a, b, c, s); });
+}
+
+hipError_t launch_column_sums_bf16(const ColumnSums& c, hipStream_t s) {
+  constexpr int NT = 512;
+  hipLaunchKernelGGL((sk_column_sums<NT>), dim3((unsigned)cdiv(c.N, NT / kSumSlices)), dim3(NT), 0, s, c);
+  return hipGetLastError();
 }
 
 }  // namespace sk

@@ -432,11 +432,6 @@ __device__ __forceinline__ void column_sum(const float* __restrict__ part, T* __
   else out[d] = x;
 }
 
-template <class T>
-__global__ __launch_bounds__(32 * kSlices) void sk_column_sums(const float* part, T* out, int count, int D) {
-  column_sum<T>(part, out, count, D, blockIdx.x);
-}
-
 // The norms' sums: blockIdx.y 0, 1, 2 the three vectors, then the rows of the gate.
 template <class T>
 __global__ __launch_bounds__(32 * kSlices) void sk_norm_sums(NormGradArgs a, int workers) {
@@ -542,11 +537,6 @@ int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus) {
 hipError_t launch_norm_backward(const NormGradArgs& a, bool f32, hipStream_t s) {
   if (a.D > kMaxNormWidth) return hipErrorInvalidValue;
   return f32 ? backward_form<float>(a, s) : backward_form<uint16_t>(a, s);
-}
-
-hipError_t launch_column_sums_bf16(const float* part, uint16_t* out, int count, int D, hipStream_t s) {
-  hipLaunchKernelGGL((sk_column_sums<uint16_t>), dim3((unsigned)ceil_div(D, 32)), dim3(32 * kSlices), 0, s, part, out, count, D);
-  return hipGetLastError();
 }
 
 }  // namespace sk
