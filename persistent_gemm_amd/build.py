@@ -11,11 +11,10 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libskgemm.so")
 # device-ceiling probes for the roofline (bench.py --ceiling), a library of their own
 PROBE_LIB = os.path.join(HERE, "libskprobe.so")
-PROBE_# the native binding of the block-scaled and norm calls: host code against torch's headers
+PROBE_SOURCES = ["sk_probe.hip"]
+# the native binding of the block-scaled and norm calls: host code against torch's headers
 NATIVE = os.path.join(HERE, "_sknative.so")
 CXX = os.environ.get("CXX", "g++")
-
-SOURCES = ["sk_probe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["sk_kernels.hip", "sk_kernels_mx.hip", "sk_kernels_ksplit.hip", "sk_backward.hip", "sk_quantize.hip",
