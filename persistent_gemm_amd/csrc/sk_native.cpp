@@ -8,8 +8,10 @@
 
 #include <Python.h>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -53,13 +55,22 @@ bool none_or(const Arg& a, c10::Device dev, at::ScalarType type, at::IntArrayRef
   return !a.bad && (!a.t || is(*a.t, dev, type, shape));
 }
 
+// An output, from the allocator that torch's own tensors of the device come from (the first one says which).  at::empty
+// finds it through two dispatches: 0.75 us a tensor against 0.32.  The allocator serves the current device, which
+// stream_of() has made sure of.
 Tensor make(at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  static c10::Allocator* allocator = nullptr;
+  if (allocator) return at::detail::empty_generic(shape, allocator, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
+  const Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  allocator = t.storage().allocator();
+  return t;
 }
 
 // The stream to use: the caller's handle, or torch's current one of the device (by the function bind() was given).
+// False where the handle is none, or the device not the current one, which the library launches on.
 PyObject* current_stream = nullptr;
 bool stream_of(PyObject* o, c10::Device dev, void** s) {
+  if (c10::impl::getDeviceGuardImpl(dev.type())->getDevice() != dev) return false;
   if (o == Py_None) {
     PyObject* index = PyLong_FromLong(dev.index());
     PyObject* handle = index ? PyObject_CallFunctionObjArgs(current_stream, index, nullptr) : nullptr;
