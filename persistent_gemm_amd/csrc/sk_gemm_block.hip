@@ -34,6 +34,9 @@ struct BlockCfg {
   static constexpr int S_A = (BM + 63) / 64, S_B = (BN + 63) / 64;  // 256-byte scale loads of a stage
   static constexpr int S_PT = (S_A + S_B + NW - 1) / NW;            // ... per wave (past the last, one again)
   static constexpr int PER_STAGE = A_PT + B_PT + S_PT;
+  // Two stages: A's part of one, which is in registers by then, is refilled during the k-step that uses it, behind a
+  // barrier of its own (see the k-steps).  Needs three pairs of columns.
+  static constexpr bool EARLY_A = STAGES == 2 && FN > 4;
   static constexpr int B_OFF = BM * kBlock, S_OFF = (BM + BN) * kBlock, SB_OFF = S_OFF + S_A * 256;
   static constexpr int STAGE = SB_OFF + S_B * 256;
   static constexpr int OUT_WAVE = WTM * WTN * 2;                    // a wave's bf16 outputs
@@ -42,7 +45,7 @@ struct BlockCfg {
   static_assert(A_PT * NW * 8 == BM && B_PT * NW * 8 == BN, "whole loads");
   static_assert(WTM % 16 == 0 && WTN % 16 == 0 && WTN <= 128 && 128 % WTN == 0, "a wave's columns share a tile scale");
   static_assert(NW * OUT_WAVE <= BIAS_OFF && LDS <= 160 * 1024, "LDS");
-  static_assert((STAGES - 1) * PER_STAGE <= 63, "vmcnt range");
+  static_assert((STAGES - 1) * PER_STAGE + A_PT <= 63, "vmcnt range");
   static_assert(WK == 1 || NW * OUT_WAVE + (WK - 1) * BM * BN * 4 <= BIAS_OFF, "sums passed between the groups");
 };
 
@@ -197,8 +200,10 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
     // use there over the whole first pair.  B's fragments go round a ring of two pairs, each read
     // during the pair before.  At the last pair every read of the stage has been issued: there the
     // waves wait for the next stage's loads (a whole k-step old) and meet, the loads of the stage after
-    // go out into the one just read, and the reads run on into the next stage.  sched_barrier(0) keeps the
-    // slots, and each MFMA before its slot's fmas, in this order.
+    // go out into the one just read, and the reads run on into the next stage.  (EARLY_A: A's go out during the second
+    // pair already, when every wave has its fragments, so that they have nearly two k-steps to arrive: with
+    // two stages of 64 KiB the loads alone took as long as the k-step, 1.39 us, and 4096^3 65 us; now 61.)
+    // sched_barrier(0) keeps the slots, and each MFMA before its slot's fmas, in this order.
     constexpr int NP = C::FN / 2, PS = 2 * C::FM, NS = C::FM * C::FN, LAG = 2;   // pairs; slots of a pair, of a k-step
     constexpr int RING = NP == 1 ? 2 : 4;
     static_assert(C::FN % 2 == 0 && (NP == 1 || NP % 2 == 0) && C::FM >= 2, "pairs of columns");
@@ -262,7 +267,7 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
       static_for<NS>([&](auto nc) {
         constexpr int n = decltype(nc)::value, r = n % PS, i = r / 2, pair = n / PS, j = pair * 2 + n % 2;
         if constexpr (r == 0 && pair == NP - 1) {
-          wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE>();
+          wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE + (C::EARLY_A ? C::A_PT : 0)>();
           meet();
           const uint32_t move = (uint32_t)((d + 1) % C::STAGES ? C::STAGE : -(C::STAGES - 1) * C::STAGE);
           la += move;
@@ -271,6 +276,7 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
           lsb += move;
           read_scales();   // (first: everything read later may still be on its way when the next k-step starts)
         }
+        if constexpr (C::EARLY_A && r == 0 && pair == 1) meet();
         p[n % (LAG + 1)] = block_mfma(b[j % RING], a[i]);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (n >= LAG) add(std::integral_constant<int, n - LAG>{});
@@ -282,9 +288,16 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
         if constexpr (NP == 1 && i == C::FM - 1) read_b(std::integral_constant<int, j>{});
         if constexpr (pair == NP - 1) {
           if constexpr (n % 2 == 1) read_a(std::integral_constant<int, i>{});
-          static_for<C::PER_STAGE>([&](auto lc) {
+          constexpr int first = C::EARLY_A ? C::A_PT : 0, count = C::PER_STAGE - first;
+          static_for<count>([&](auto lc) {
             constexpr int l = decltype(lc)::value;
-            if constexpr (l * PS / C::PER_STAGE == r) issue_one(d + C::STAGES, lc);
+            if constexpr (l * PS / count == r) issue_one(d + C::STAGES, std::integral_constant<int, first + l>{});
+          });
+        }
+        if constexpr (C::EARLY_A && pair == 1) {
+          static_for<C::A_PT>([&](auto lc) {
+            constexpr int l = decltype(lc)::value;
+            if constexpr (l * PS / C::A_PT == r) issue_one(d + C::STAGES, lc);
           });
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -559,16 +572,17 @@ hipError_t choose_tile(Tiles&& tiles, int rows, int kb, int cus, Go&& go) {
   // 500x700x900 5.7 us against 6.4 with 64x64 tiles, 100x4096x4096 9.8 / 10.3
   if (rows <= 64 || tiles(64, 32) <= cus) return go(BlockCfg<64, 32, 2, 1, 3, 2>{});
   // two groups of waves pay from 16 blocks on: 128x8192x8192 28.3 -> 25.4 us, but 1024x1024x1024 6.0 -> 6.6
-  if (tiles(64, 64) <= cus && kb >= 16) return go(BlockCfg<64, 64, 2, 2, 4, 2>{});
+  if (tiles(64, 64) <= cus) return kb >= 16 ? go(BlockCfg<64, 64, 2, 2, 4, 2>{}) : go(BlockCfg<64, 64, 2, 2, 4>{});
+  // 1037x1290x2064 11.7 us against 13.4 with 64x64 tiles and 14.9 with 128x128
+  if (tiles(128, 64) <= cus) return go(BlockCfg<128, 64, 4, 2, 4>{});
   // 3000x4100x2060 (204 tiles) 40.6 us against 48.0 with 256x128 and 50.8 with 128x128
   if (tiles(256, 256) * 4 >= (int64_t)cus * 3) return go(BlockCfg<256, 256, 4, 2, 2>{});
   // 4096x2048x4096 39.7 us against 41.7 with 128x128 tiles and 57.9 with 256x256
   if (tiles(256, 128) * 4 >= (int64_t)cus * 3) return go(BlockCfg<256, 128, 4, 2, 3>{});
   // more than one to a unit: two at once, on half the stages (3000x2000x1000 18.8 -> 15.2 us)
   if (tiles(128, 128) > cus) return go(BlockCfg<128, 128, 4, 2, 2>{});
-  // 777x4096x2048 14.0 us against 20.6 with 64x64 tiles; 1037x1290x2064 (99 tiles) 15.8 / 13.8
-  if (tiles(128, 128) * 2 >= cus) return go(BlockCfg<128, 128, 4, 2, 4>{});
-  return go(BlockCfg<64, 64, 2, 2, 4>{});
+  // 777x4096x2048 12.5 us against 16.9 with 128x64 tiles and 19.3 with 64x64 (12.9 with the waves as 4 x 2)
+  return go(BlockCfg<128, 128, 2, 4, 4>{});
 }
 
 }  // namespace
