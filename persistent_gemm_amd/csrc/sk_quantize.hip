@@ -3,9 +3,9 @@
 //
 //   s = max(fl(max|x| / 448), 2^-126) over the block,   q = E4M3 nearest to x / s, ties to even.
 //
-// A workgroup takes one 128 x 128 tile: thread (tr, tc) of 16 x 16 holds rows 8 tr .. +7, columns
+// A workgroup takes one 128 x 128 tile: thread (tr, tc) of 128 / RPT x 16 holds rows RPT tr .. and columns
 // 8 tc .. +7 in registers, so a row's block is 16 neighbouring lanes (their maximum is four lane
-// rotations) and a column's block is one thread's eight rows and 16 threads, joined in LDS.  x is read once
+// rotations) and a column's block is one thread's RPT rows and 128 / RPT threads, joined in LDS.  x is read once
 // for both forms.  The transposed codes go through LDS so that each column's 128 codes leave as one line.
 // The pass is bound by HBM: 2 or 4 bytes in and 1 or 2 out per element.
 
@@ -23,47 +23,52 @@ namespace {
 
 constexpr int kPitch = 136;   // LDS bytes between two columns' transposed codes: 34 banks
 
-// Byte of 8-row piece `piece` of column c: pieces are moved by columns / 32, so that the 64 lanes of a
-// store (columns 8 apart, four pieces) meet each bank twice, which is what 512 bytes need.
-__device__ __forceinline__ int t_at(int c, int piece) { return c * kPitch + 8 * (piece ^ (4 * ((c >> 5) & 3))); }
+// Up to this many tiles have twice the threads each (4 rows a thread instead of 8), so that a SIMD has two waves where
+// it would have one: 16x4096 3.4 -> 2.6 us, 1037x2050 both forms 7.3 -> 6.7, 2048x4096 both 11.2 -> 10.5; from
+// 1024 tiles on (4096x4096 both, 16.8 against 16.9 us) there are enough waves without.
+constexpr int64_t kFewTiles = 512;
 
-// 8 rows x 8 columns of codes (row i: w[i][0], w[i][1]) to 8 columns of 8 codes.
-__device__ __forceinline__ void transpose8(const uint32_t (&w)[8][2], uint32_t (&o)[8][2]) {
+// Byte of rows r .. of column c (r a multiple of RPT): 8-row pieces are moved by columns / 32, so that the lanes of a
+// store (columns 8 apart, consecutive rows) meet each bank as often as their bytes need.
+__device__ __forceinline__ int t_at(int c, int r) { return c * kPitch + ((r & ~7) ^ (32 * ((c >> 5) & 3))) + (r & 7); }
+
+// 4 rows x 8 columns of codes (row i: w[i][0], w[i][1]) to 8 columns of 4 codes.
+__device__ __forceinline__ void transpose4(const uint32_t (*w)[2], uint32_t (&o)[8]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)        // columns 4 h .. +3
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {    // rows 4 v .. +3
-      const uint32_t a = w[4 * v][h], b = w[4 * v + 1][h], c = w[4 * v + 2][h], d = w[4 * v + 3][h];
-      // perm(hi, lo): selector bytes 0-3 pick from lo, 4-7 from hi
-      const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602u);
-      const uint32_t cd0 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd1 = __builtin_amdgcn_perm(d, c, 0x07030602u);
-      o[4 * h][v] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100u);
-      o[4 * h + 1][v] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302u);
-      o[4 * h + 2][v] = __builtin_amdgcn_perm(cd1, ab1, 0x05040100u);
-      o[4 * h + 3][v] = __builtin_amdgcn_perm(cd1, ab1, 0x07060302u);
-    }
+  for (int h = 0; h < 2; ++h) {      // columns 4 h .. +3
+    const uint32_t a = w[0][h], b = w[1][h], c = w[2][h], d = w[3][h];
+    // perm(hi, lo): selector bytes 0-3 pick from lo, 4-7 from hi
+    const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+    const uint32_t cd0 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd1 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+    o[4 * h] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100u);
+    o[4 * h + 1] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302u);
+    o[4 * h + 2] = __builtin_amdgcn_perm(cd1, ab1, 0x05040100u);
+    o[4 * h + 3] = __builtin_amdgcn_perm(cd1, ab1, 0x07060302u);
+  }
 }
 
-// TILE: one scale per 128 x 128.  PLAIN / TRANS: which forms are written (with SUMS: perhaps neither).  SUMS: also the column sums of the
-// tile's rows, part[row block][column], in a fixed order (the first pass of a bias gradient).
-template <class T, bool TILE, bool PLAIN, bool TRANS, bool SUMS, bool SHORT>
-__global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
+// TILE: one scale per 128 x 128.  PLAIN / TRANS: which forms are written (with SUMS: perhaps neither).  SUMS: also the
+// column sums of the tile's rows, part[row block][column], in a fixed order (the first pass of a bias gradient).
+template <class T, bool TILE, bool PLAIN, bool TRANS, bool SUMS, bool SHORT, int RPT>
+__global__ __launch_bounds__(2048 / RPT) void sk_quantize_block(QuantArgs a) {
+  static_assert(RPT == 8 || RPT == 4, "rows of a thread");
+  constexpr int TR = 128 / RPT;         // threads of a column
   constexpr bool COLS = TRANS && !TILE;
   __shared__ __attribute__((aligned(16))) uint8_t codes_t[TRANS ? 128 * kPitch : 16];
-  __shared__ __attribute__((aligned(16))) uint32_t tops[COLS ? 16 : 1][128];
+  __shared__ __attribute__((aligned(16))) uint32_t tops[COLS ? TR : 1][128];
   __shared__ __attribute__((aligned(16))) float col_scale[COLS ? 3 : 1][128];
-  __shared__ __attribute__((aligned(16))) float col_sum[SUMS ? 16 : 1][128];
+  __shared__ __attribute__((aligned(16))) float col_sum[SUMS ? TR : 1][128];
   const int rb = blockIdx.x / a.kb, cb = blockIdx.x - rb * a.kb;
   const int t = threadIdx.x, tr = t >> 4, tc = t & 15;
   const int R = a.R, C = a.C;
-  const int row0 = rb * 128 + 8 * tr, col0 = cb * 128 + 8 * tc;
-  float x[8][8];
+  const int row0 = rb * 128 + RPT * tr, col0 = cb * 128 + 8 * tc;
+  float x[RPT][8];
   {
-    Raw8<T> raw[8];
+    Raw8<T> raw[RPT];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = load_raw8<SHORT>((const T*)a.x + (int64_t)min(row0 + i, R - 1) * C, col0, C);
+    for (int i = 0; i < RPT; ++i) raw[i] = load_raw8<SHORT>((const T*)a.x + (int64_t)min(row0 + i, R - 1) * C, col0, C);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RPT; ++i) {
       settle8<SHORT>(raw[i], col0, C);
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[i][k] = row0 + i < R ? raw_at(raw[i], k) : 0.0f;
@@ -75,7 +80,7 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
     for (int k = 0; k < 8; ++k) {
       float s = x[0][k];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) s += x[i][k];
+      for (int i = 1; i < RPT; ++i) s += x[i][k];
       col_sum[tr][8 * tc + k] = s;
     }
   }
@@ -84,7 +89,7 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
     for (int k = 0; k < 8; ++k) {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, f_bits(x[i][k]) & kAbs);
+      for (int i = 0; i < RPT; ++i) m = max(m, f_bits(x[i][k]) & kAbs);
       tops[tr][8 * tc + k] = m;
     }
   }
@@ -92,7 +97,7 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
   if constexpr (TILE) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < RPT; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) m = max(m, f_bits(x[i][k]) & kAbs);
     m = max16(m);
@@ -100,7 +105,9 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
     m = max(m, (uint32_t)__shfl_xor((int)m, 32));
     if ((t & 63) == 0) tops[0][t >> 6] = m;
     __syncthreads();
-    m = max(max(tops[0][0], tops[0][1]), max(tops[0][2], tops[0][3]));
+    m = tops[0][0];
+#pragma unroll
+    for (int w = 1; w < 32 / RPT; ++w) m = max(m, tops[0][w]);
     tile = Coder<T>::scale(m);
     if (t == 0) {
       if (PLAIN) a.scale[(int64_t)rb * a.kb + cb] = tile.s;
@@ -113,7 +120,7 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
       if constexpr (COLS) {
         uint32_t m = tops[0][t];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) m = max(m, tops[i][t]);
+        for (int i = 1; i < TR; ++i) m = max(m, tops[i][t]);
         const BlockScale b = Coder<T>::scale(m);
         col_scale[0][t] = b.s;
         col_scale[1][t] = b.r;
@@ -123,7 +130,7 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
       if constexpr (SUMS) {
         float s = col_sum[0][t];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s += col_sum[i][t];
+        for (int i = 1; i < TR; ++i) s += col_sum[i][t];
         if (c < C) a.part[(int64_t)rb * C + c] = s;
       }
     }
@@ -131,11 +138,11 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
   }
 
   // the rows' codes, eight bytes a lane: 16 lanes write a row's 128
-  [[maybe_unused]] uint32_t w[8][2];
+  [[maybe_unused]] uint32_t w[RPT][2];
   if constexpr (PLAIN || TILE) {
     float own = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RPT; ++i) {
       BlockScale b;
       if constexpr (TILE) {
         b = tile;
@@ -155,31 +162,36 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
       if (PLAIN && row0 + i < R && col0 < a.pitch)
         *(u32x2*)(a.q + (int64_t)(row0 + i) * a.pitch + col0) = u32x2{w[i][0], w[i][1]};
     }
-    if (!TILE && tc < 8 && row0 + tc < R) a.scale[(int64_t)cb * R + row0 + tc] = own;
+    if (!TILE && tc < RPT && row0 + tc < R) a.scale[(int64_t)cb * R + row0 + tc] = own;
   }
 
   if constexpr (TRANS) {
-    uint32_t o[8][2];
+    uint32_t o[RPT / 4][8];    // rows 4 v .. +3 of each column
     if constexpr (TILE) {
-      transpose8(w, o);
+#pragma unroll
+      for (int v = 0; v < RPT / 4; ++v) transpose4(w + 4 * v, o[v]);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const BlockScale b{col_scale[0][8 * tc + k], col_scale[1][8 * tc + k], col_scale[2][8 * tc + k]};
-        float v[8];
+        float v[RPT];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = Coder<T>::nudged(x[i][k], b);
-        o[k][0] = codes4(v[0], v[1], v[2], v[3], b.s);
-        o[k][1] = codes4(v[4], v[5], v[6], v[7], b.s);
+        for (int i = 0; i < RPT; ++i) v[i] = Coder<T>::nudged(x[i][k], b);
+#pragma unroll
+        for (int i = 0; i < RPT; i += 4) o[i / 4][k] = codes4(v[i], v[i + 1], v[i + 2], v[i + 3], b.s);
       }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) *(u32x2*)(codes_t + t_at(8 * tc + k, tr)) = u32x2{o[k][0], o[k][1]};
+    for (int k = 0; k < 8; ++k) {
+      uint8_t* const to = codes_t + t_at(8 * tc + k, RPT * tr);
+      if constexpr (RPT == 8) *(u32x2*)to = u32x2{o[0][k], o[RPT / 4 - 1][k]};
+      else *(uint32_t*)to = o[0][k];
+    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = (t >> 3) + 32 * i, p = t & 7;     // column of the tile, 16 of its rows
-      const uint8_t* from = codes_t + t_at(c, 2 * p);
+    for (int i = 0; i < RPT / 2; ++i) {
+      const int c = (t >> 3) + 256 / RPT * i, p = t & 7;     // column of the tile, 16 of its rows
+      const uint8_t* from = codes_t + t_at(c, 16 * p);
       const u32x2 lo = *(const u32x2*)from, hi = *(const u32x2*)(from + 8);
       if (cb * 128 + c < C && rb * 128 + 16 * p < a.pitch_t)
         *(u32x4*)(a.qt + (int64_t)(cb * 128 + c) * a.pitch_t + rb * 128 + 16 * p) = u32x4{lo[0], lo[1], hi[0], hi[1]};
@@ -187,13 +199,13 @@ __global__ __launch_bounds__(256) void sk_quantize_block(QuantArgs a) {
   }
 }
 
-template <class T, bool TILE, bool SUMS, bool SHORT>
+template <class T, bool TILE, bool SUMS, bool SHORT, int RPT>
 hipError_t launch_form(const QuantArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.kb * (unsigned)a.rb), block(256);
-  if (a.q && a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, true, SUMS, SHORT>), grid, block, 0, s, a);
-  else if (a.q) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, false, SUMS, SHORT>), grid, block, 0, s, a);
-  else if (a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, true, SUMS, SHORT>), grid, block, 0, s, a);
-  else if constexpr (SUMS) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, false, SUMS, SHORT>), grid, block, 0, s, a);
+  const dim3 grid((unsigned)a.kb * (unsigned)a.rb), block(2048 / RPT);
+  if (a.q && a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, true, SUMS, SHORT, RPT>), grid, block, 0, s, a);
+  else if (a.q) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, false, SUMS, SHORT, RPT>), grid, block, 0, s, a);
+  else if (a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, true, SUMS, SHORT, RPT>), grid, block, 0, s, a);
+  else if constexpr (SUMS) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, false, SUMS, SHORT, RPT>), grid, block, 0, s, a);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
@@ -205,7 +217,9 @@ hipError_t launch_quantize_block(const QuantArgs& a, bool f32, bool tile, hipStr
   auto go = [&](auto elem, auto tiled, auto sums) {
     typedef decltype(elem) T;
     constexpr bool TILE = decltype(tiled)::value, SUMS = decltype(sums)::value;
-    return a.C < 8 ? launch_form<T, TILE, SUMS, true>(a, s) : launch_form<T, TILE, SUMS, false>(a, s);
+    if (a.C < 8) return launch_form<T, TILE, SUMS, true, 8>(a, s);
+    if ((int64_t)a.kb * a.rb <= kFewTiles) return launch_form<T, TILE, SUMS, false, 4>(a, s);
+    return launch_form<T, TILE, SUMS, false, 8>(a, s);
   };
   const std::true_type yes;
   const std::false_type no;

@@ -74,7 +74,7 @@ def test_quantize_values(kind, t, block):
     _check_quantize(x, block, f"{kind} {t} {block}")
 
 
-@pytest.mark.parametrize("R,C", [(1, 1), (1, 129), (127, 16), (128, 128), (17, 2060), (1025, 24), (130, 1000)])
+@pytest.mark.parametrize("R,C", [(1, 1), (1, 129), (127, 16), (128, 128), (17, 2060), (1025, 24), (130, 1000), (3000, 3003)])
 @pytest.mark.parametrize("block", ["row", "tile"])
 def test_quantize_sizes(R, C, block):
     g = _gen(R * 7 + C)
@@ -260,7 +260,7 @@ def _pair(x, wq, ws):
 # ---------------------------------------------------------------- gradients
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (16, 64, 64), (130, 70, 50), (129, 257, 300), (300, 1000, 200),
-                                   (1037, 2050, 1290), (2048, 2304, 2176)])
+                                   (1037, 2050, 1290), (2048, 2304, 2176), (3000, 3200, 70)])
 def test_backward(M, N, K):
     g = _gen(M + N + K)
     dC = (torch.randn(M, N, generator=g) * torch.exp(torch.randn(M, 1, generator=g))).to(torch.bfloat16)
