@@ -13,7 +13,7 @@
 // memory into LDS (16-byte and 4-byte direct loads), in a ring of STAGES; the 16-byte chunks of row r are
 // permuted by (r >> 1) & 7 so that 16 lanes reading a chunk of 16 rows meet all banks.  The accumulators are
 // ordinary registers (the ALU cannot reach AGPRs), which bounds a wave's tile to 64 x 128.
-// Skinny kernels (few rows of A): see sk_gemm_block_rows.
+// Few outputs: see sk_gemm_block_rows.
 
 #include "sk_fp8.h"
 #include "sk_kernel.h"
@@ -419,7 +419,7 @@ __global__ __launch_bounds__(NT) void sk_column_sums(ColumnSums c) {
   column_sums_bf16<NT>(c, blockIdx.x, run);
 }
 
-// Few rows of A: a workgroup takes 16 NB columns and 16 MB rows, and its NWK waves share out the blocks of K
+// Few outputs: a workgroup takes 16 NB columns and 16 MB rows, and its NWK waves share out the blocks of K
 // in turn (wave w: blocks w, w + NWK, ...), so that together they read whole stretches of each row of B.  The
 // operands go straight to registers, U blocks at a time, with no barrier before the end, where the waves' sums
 // are added in LDS in wave order.  Bound by reading B once.
@@ -589,11 +589,14 @@ hipError_t choose_tile(Tiles&& tiles, int rows, int kb, int cus, Go&& go) {
 
 hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int cus, hipStream_t s) {
   if (grid_cap > 0 && grid_cap < cus) cus = grid_cap;
-  // A's rows come from the caches once for every 16 columns here and once for 32 in a tile, B's straight to registers:
-  // 1x4096x4096 6.2 against 7.2 us, 16x1024x1024 4.3 / 4.8, but 16x8192x8192 18.7 / 14.7
-  if (grid_cap <= 0 && (g.M <= 8 || (g.M <= 16 && (int64_t)g.N * g.row_bytes <= (8 << 20))))
-    return launch_rows<1, 1, 8, 4>(g, b_tile, s);
   auto tiles = [&](int bm, int bn) { return (int64_t)cdiv(g.M, bm) * cdiv(g.N, bn); };
+  // Straight to registers where 16 x 16 blocks of C fill the device about once (twice, with a short K): no LDS between the
+  // loads and the MFMAs, and the most waves to a block.  256x256x512 3.4 us against 4.1 with 32x32 tiles, 64x1024x1024
+  // 3.4 / 4.5, 64x2048x1024 4.2 / 4.5, but 512x512x1024 (1024 blocks) 6.3 / 4.5 and 8x8192x4096 10.2 / 8.9: A is read
+  // for every 16 columns instead of 32.  With a long K, 16 waves that ask for two blocks at a time:
+  // 1x4096x4096 5.5 us against 6.5 with 8 and one, 256x256x2048 5.0 / 4.4.
+  if (grid_cap <= 0 && tiles(16, 16) <= (g.kb <= 16 ? 2 : 1) * (int64_t)cus)
+    return g.kb < 32 ? launch_rows<1, 1, 8, 1>(g, b_tile, s) : launch_rows<1, 1, 16, 2>(g, b_tile, s);
   return choose_tile(tiles, g.M, g.kb, cus, [&](auto cfg) { return launch_tiled<decltype(cfg)>(g, b_tile, grid_cap, s); });
 }
 
