@@ -221,25 +221,29 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_forward(NormArg
 // ---------------------------------------------------------------- backward
 
 // Workers (a workgroup, or a wave of four) take runs of consecutive rows and keep the column sums of the
-// weights' gradients in registers; each run lies within the tokens that share a row of the gate.  A second
-// kernel adds the workers' sums in worker order, so the results repeat bit for bit.  A row's tensors are
-// asked for one row ahead (AHEAD), and the shared vectors kept (HOLD), where the registers allow it.
+// weights' gradients in registers; each run lies within the tokens that share a row of the gate.  At the end a
+// workgroup's four workers are added in LDS, and a second kernel adds the workgroups' sums, both in order, so the
+// results repeat bit for bit.  A row's tensors are asked for one row ahead (AHEAD), and the shared vectors kept (HOLD),
+// where the registers allow it.  512 threads to a compute unit: with 1024 the sums cost more than the
+// waves gain (4095x2047 fp32 63 -> 71 us), and two rows of 256 threads to a workgroup wait for each other at its
+// barriers (main kernel 36 -> 40 us in bf16).
 //
-// part: [3][workers][D] (weight, next_weight, residual_scale), then [chunks][D] of the gate
-// where a gate row has more than one chunk.
+// part: [3][workgroups][D] (weight, next_weight, residual_scale), then of the gate [workgroups][D] where all tokens
+// share a row, or [chunks][D] where a row has several chunks.
 template <class T, bool POST, bool PRE, int TPR, int CH, bool SHORT>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_backward(NormGradArgs a) {
   __shared__ float red[2][16];
-  int turn = 0;
   constexpr int RPW = rows_per_wg<TPR>();
+  __shared__ float others[RPW > 1 ? RPW - 1 : 1][RPW > 1 ? 8 * CH : 1][RPW > 1 ? TPR : 1];
+  int turn = 0;
   // registers of a lane: a row's tensors as they lie in memory, the column sums, the shared vectors, and the rest
   constexpr int RAW = CH * (int)sizeof(T) * 2, ROW = RAW * (1 + 2 * POST + 2 * PRE), SUM = 8 * CH * (3 * POST + PRE);
   constexpr int VEC = RAW * (2 * POST + PRE), REST = 60 + 28 * CH, MOST = TPR == 1024 ? 128 : 256;
   constexpr bool AHEAD = 2 * ROW + SUM + VEC + REST <= MOST, HOLD = AHEAD || ROW + SUM + VEC + REST <= MOST;
   const int t = threadIdx.x % TPR, D = a.D;
   const float inv = 1.0f / (float)D;
-  const int worker = blockIdx.x * RPW + sub_row<TPR>(), workers = gridDim.x * RPW;
-  const bool gate_sums = POST && a.gate && a.gate_rows > 1;
+  const int sub = sub_row<TPR>(), worker = blockIdx.x * RPW + sub, workers = gridDim.x * RPW;
+  const bool gate_sums = POST && a.gate && a.gate_rows > 1, one_gate = a.groups == 1;
   const int group_rows = a.T / a.groups;
   typedef RawRow<T, CH> Row;
   auto load = [&](const void* p, int row) { return load_row<SHORT, T, TPR, CH>(p, row, t, D); };
@@ -285,14 +289,16 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_backward(NormGr
     const int group = chunk / a.chunks_per_gate, part = chunk - group * a.chunks_per_gate;
     const int row0 = group * group_rows + part * a.rows_per_chunk;
     const int row1 = min(row0 + a.rows_per_chunk, (group + 1) * group_rows);
+    const int rows = row1 - row0, last = row1 - 1;
     Rows ahead;
-    if constexpr (AHEAD) ahead = ask(min(row0, a.T - 1));
-    for (int row = row0; row < row1; ++row) {
+    if constexpr (AHEAD) ahead = ask(row0);
+    for (int i = 0; i < rows; ++i) {
+      const int row = row0 + i;
       const int64_t at = (int64_t)row * D;
       Rows x;
       if constexpr (AHEAD) {
         x = ahead;
-        ahead = ask(min(row + 1, row1 - 1));
+        ahead = ask(min(row + 1, last));
       } else {
         x = ask(row);
       }
@@ -385,27 +391,49 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_backward(NormGr
       }
     }
     if constexpr (POST) {
-      if (gate_sums) {
+      if (gate_sums && !one_gate) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
           if (a.chunks_per_gate == 1) store8((T*)a.dgate + (int64_t)group * D + col, n, dg[c]);
-          else store8(a.part + ((int64_t)3 * workers + chunk) * D + col, n, dg[c]);
+          else store8(a.part + ((int64_t)3 * gridDim.x + chunk) * D + col, n, dg[c]);
 #pragma unroll
           for (int k = 0; k < 8; ++k) dg[c][k] = 0.0f;
         }
       }
     }
   }
+  // the workgroup's workers, added in order by the first
+  auto total = [&](float (*v)[8], int slot) {
+    if constexpr (RPW > 1) {
+      __syncthreads();
+      if (sub > 0) {
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
-    if constexpr (POST) {
-      store8(a.part + (int64_t)worker * D + col, n, dw[c]);
-      if (a.residual_scale) store8(a.part + (int64_t)(2 * workers + worker) * D + col, n, drs[c]);
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) others[sub - 1][8 * c + k][t] = v[c][k];
+      }
+      __syncthreads();
+      if (sub > 0) return;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int o = 0; o < RPW - 1; ++o) v[c][k] += others[o][8 * c + k][t];
     }
-    if constexpr (PRE) store8(a.part + (int64_t)(workers + worker) * D + col, n, dnw[c]);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = 8 * (t + c * TPR);
+      store8(a.part + ((int64_t)slot * gridDim.x + blockIdx.x) * D + col, min(8, max(0, D - col)), v[c]);
+    }
+  };
+  if constexpr (POST) {
+    total(dw, 0);
+    if (a.residual_scale) total(drs, 2);
+    if (gate_sums && one_gate) total(dg, 3);
   }
+  if constexpr (PRE) total(dnw, 1);
 }
 
 // out[d] = the sum of `count` rows of part, in a fixed order: thread (column, slice) of 32 x 32 adds the slice's
@@ -434,15 +462,15 @@ __device__ __forceinline__ void column_sum(const float* __restrict__ part, T* __
 
 // The norms' sums: blockIdx.y 0, 1, 2 the three vectors, then the rows of the gate.
 template <class T>
-__global__ __launch_bounds__(32 * kSlices) void sk_norm_sums(NormGradArgs a, int workers) {
+__global__ __launch_bounds__(32 * kSlices) void sk_norm_sums(NormGradArgs a, int wgs) {
   const int y = blockIdx.y;
   if (y < 3) {
     T* const out = (T*)(y == 0 ? a.dweight : y == 1 ? a.dnext_weight : a.dresidual_scale);
-    if (out) column_sum<T>(a.part + (int64_t)y * workers * a.D, out, workers, a.D, blockIdx.x);
+    if (out) column_sum<T>(a.part + (int64_t)y * wgs * a.D, out, wgs, a.D, blockIdx.x);
   } else {
     const int group = y - 3;
-    column_sum<T>(a.part + ((int64_t)3 * workers + (int64_t)group * a.chunks_per_gate) * a.D,
-                  (T*)a.dgate + (int64_t)group * a.D, a.chunks_per_gate, a.D, blockIdx.x);
+    column_sum<T>(a.part + ((int64_t)3 * wgs + (int64_t)group * a.chunks_per_gate) * a.D,
+                  (T*)a.dgate + (int64_t)group * a.D, a.groups == 1 ? wgs : a.chunks_per_gate, a.D, blockIdx.x);
   }
 }
 
@@ -490,9 +518,8 @@ hipError_t backward(const NormGradArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((sk_norm_backward<T, POST, PRE, TPR, CH, SHORT>), dim3(wgs), dim3(TPR == 64 ? 256 : TPR), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const bool gate = a.dgate && a.gate_rows > 1 && a.chunks_per_gate > 1;
-  hipLaunchKernelGGL((sk_norm_sums<T>), dim3(ceil_div(a.D, 32), 3 + (gate ? a.groups : 0)), dim3(32 * kSlices), 0, s, a,
-                     wgs * grad_rpw(a.D));
+  const bool gate = a.dgate && a.gate_rows > 1 && (a.groups == 1 || a.chunks_per_gate > 1);
+  hipLaunchKernelGGL((sk_norm_sums<T>), dim3(ceil_div(a.D, 32), 3 + (gate ? a.groups : 0)), dim3(32 * kSlices), 0, s, a, wgs);
   return hipGetLastError();
 }
 
@@ -525,13 +552,13 @@ int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus) {
   const bool grouped = a->h && a->gate && a->gate_rows > 1;
   a->groups = grouped ? a->T / a->gate_rows : 1;
   const int group_rows = a->T / a->groups;
-  const int want = 2 * cus * grad_rpw(a->D) * 256 / (grad_threads(a->D) < 256 ? 256 : grad_threads(a->D));
+  const int want = 512 * cus / grad_threads(a->D);   // 512 threads to a compute unit
   a->chunks_per_gate = a->groups >= want ? 1 : ceil_div(want, a->groups);
   a->rows_per_chunk = ceil_div(group_rows, a->chunks_per_gate);
   a->chunks_per_gate = ceil_div(group_rows, a->rows_per_chunk);
   a->chunks = a->groups * a->chunks_per_gate;
-  const int64_t workers = (int64_t)grad_wgs(*a) * grad_rpw(a->D);
-  return (3 * workers + (grouped && a->chunks_per_gate > 1 ? a->chunks : 0)) * (int64_t)a->D * (int64_t)sizeof(float);
+  const int64_t wgs = grad_wgs(*a), gate = !grouped ? 0 : a->groups == 1 ? wgs : a->chunks_per_gate > 1 ? a->chunks : 0;
+  return (3 * wgs + gate) * (int64_t)a->D * (int64_t)sizeof(float);
 }
 
 hipError_t launch_norm_backward(const NormGradArgs& a, bool f32, hipStream_t s) {
