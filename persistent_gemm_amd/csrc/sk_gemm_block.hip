@@ -24,7 +24,7 @@ namespace {
 
 // A tile's 128-byte k-step of BM rows of A and BN of B over WM x WN waves; WK such groups of waves take every WK-th
 // block of K, each with a ring of its own, and their sums are added in group order at the end.
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int WK_ = 1>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int WK_ = 1, bool STREAM_ = false>
 struct BlockCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_, WK = WK_;
   static constexpr int NW = WM * WN, NT = 64 * NW * WK;             // waves of a group, threads of a workgroup
@@ -39,12 +39,20 @@ struct BlockCfg {
   static constexpr bool EARLY_A = STAGES == 2 && FN > 4;
   static constexpr int B_OFF = BM * kBlock, S_OFF = (BM + BN) * kBlock, SB_OFF = S_OFF + S_A * 256;
   static constexpr int STAGE = SB_OFF + S_B * 256;
-  static constexpr int OUT_WAVE = WTM * WTN * 2;                    // a wave's bf16 outputs
+  // Outputs leave through LDS, a wave's OR rows at a time: all of them where the ring is done with.  Where a
+  // workgroup takes several tiles (STREAM) the next tile's first stages are on their way into the ring by then,
+  // and the outputs have a small area of their own.  (Whole rows of a wave all the same: half of them, 128 bytes that
+  // start anywhere, are mostly lines written in part, 5000x6001x700 40.6 -> 48.5 us.)
+  static constexpr bool STREAM = STREAM_;
+  static constexpr int OR = STREAM ? 8 : WTM, OUT_WAVE = OR * WTN * 2;
   static constexpr int CH = WTN / 8;                                // 16-byte chunks of an output row
-  static constexpr int RING = STAGES * STAGE, BIAS_OFF = WK * RING, LDS = BIAS_OFF + (BN < 128 ? 256 : 2 * BN);
+  static constexpr int RING = STAGES * STAGE, BIAS = BN < 128 ? 256 : 2 * BN, BIAS_OFF = WK * RING;
+  static constexpr int OUT_OFF = STREAM ? BIAS_OFF + 2 * BIAS : 0;
+  static constexpr int LDS = STREAM ? OUT_OFF + NW * OUT_WAVE : BIAS_OFF + BIAS;
   static_assert(A_PT * NW * 8 == BM && B_PT * NW * 8 == BN, "whole loads");
   static_assert(WTM % 16 == 0 && WTN % 16 == 0 && WTN <= 128 && 128 % WTN == 0, "a wave's columns share a tile scale");
   static_assert(NW * OUT_WAVE <= BIAS_OFF && LDS <= 160 * 1024, "LDS");
+  static_assert(!STREAM || (WK == 1 && BN <= 256 && BN / 128 <= NW), "a streamed tile");
   static_assert((STAGES - 1) * PER_STAGE + A_PT <= 63, "vmcnt range");
   static_assert(WK == 1 || NW * OUT_WAVE + (WK - 1) * BM * BN * 4 <= BIAS_OFF, "sums passed between the groups");
 };
@@ -134,20 +142,28 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
   const int c0 = (lg ^ sw) * 16;
 
   const int T = g.tiles_m * g.tiles_n;
-  for (int t = first; t < T; t += stride) {
+  // The tile that loads are issued for.  This wave's scale loads of a stage are 64 floats each: rows of A, or columns of B,
+  // whose scale is their own or that of their 128 columns.  The k-steps are issued in order: sat is where the next
+  // one's are, sstep bytes on from the last block's.
+  int m0, n0, rows, cols;
+  v4u ra, rbw;
+  int64_t sat[C::S_PT], sstep[C::S_PT];
+  uint32_t sbytes[C::S_PT], svoff[C::S_PT], slds[C::S_PT];
+  // the tile's bias goes to LDS too, two columns a lane (a lone last column, or a bias not on four bytes, would
+  // not: it is read when the outputs are made)
+  const bool bias_staged = (((uintptr_t)g.bias | (uintptr_t)(2 * g.N)) & 3) == 0;
+  constexpr int BI = (C::BN + 127) / 128;
+  auto aim = [&](int t, int turn) {
     int tm, tn;
     tile_of<C::BM >= 256 ? 4 : 8>(t, g.tiles_m, g.tiles_n, &tm, &tn);
     tm = __builtin_amdgcn_readfirstlane(tm);
     tn = __builtin_amdgcn_readfirstlane(tn);
-    const int m0 = tm * C::BM, n0 = tn * C::BN;
-    const int rows = min(C::BM, g.M - m0), cols = min(C::BN, g.N - n0);
-    const v4u ra = rsrc_words(g.A + (int64_t)m0 * rb, (uint32_t)rows * rb);
-    const v4u rbw = rsrc_words(g.B + (int64_t)n0 * rb, (uint32_t)cols * rb);
-    // This wave's scale loads of a stage, 64 floats each: rows of A, or columns of B, whose scale is their own or
-    // that of their 128 columns.  The k-steps are issued in order: sat is where the next one's are, sstep bytes on
-    // from the last block's.
-    int64_t sat[C::S_PT], sstep[C::S_PT];
-    uint32_t sbytes[C::S_PT], svoff[C::S_PT], slds[C::S_PT];
+    m0 = tm * C::BM;
+    n0 = tn * C::BN;
+    rows = min(C::BM, g.M - m0);
+    cols = min(C::BN, g.N - n0);
+    ra = rsrc_words(g.A + (int64_t)m0 * rb, (uint32_t)rows * rb);
+    rbw = rsrc_words(g.B + (int64_t)n0 * rb, (uint32_t)cols * rb);
 #pragma unroll
     for (int i = 0; i < C::S_PT; ++i) {
       const int idx = (wave + i * C::NW) % (C::S_A + C::S_B);
@@ -160,32 +176,90 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
       svoff[i] = e >= (is_a ? rows : cols) ? kOob : (uint32_t)(is_a || BROW ? e : (nb + e) / kBlock * g.kb) * 4u;
       slds[i] = C::S_OFF + (uint32_t)idx * 256u;
     }
+    if (bias_staged)
+      dma_load4(rsrc_words(g.bias + n0, g.bias ? (uint32_t)cols * 2u : 0u), (uint32_t)((wave % BI) * 64 + lane) * 4u, 0u,
+                (uint32_t)(uintptr_t)smem + C::BIAS_OFF + (uint32_t)turn * C::BIAS + (uint32_t)(wave % BI) * 256u);
+  };
+  // Load l of block k of that tile into a stage; where there is none every lane is out of range (zeros, no traffic).
+  auto issue_one = [&](int k, int slot, bool live, auto lc) {
+    constexpr int l = decltype(lc)::value;
+    const uint32_t stage = ring + (uint32_t)slot * C::STAGE;
+    const uint32_t kbyte = live ? (uint32_t)k * kBlock : 0u;
+    if constexpr (l < C::A_PT + C::B_PT) {
+      constexpr bool is_a = l < C::A_PT;
+      constexpr int i = is_a ? l : l - C::A_PT;
+      const uint32_t c = chunk ^ (C::NW % 2 && i % 2 ? 64u : 0u);
+      const uint32_t voff = live && kbyte + c < rb ? row_off + c : kOob;
+      dma_load16(is_a ? ra : rbw, voff, kbyte + i * gstep,
+                 stage + (is_a ? 0u : C::B_OFF) + (uint32_t)(wave + i * C::NW) * 1024u);
+    } else {
+      constexpr int i = l - C::A_PT - C::B_PT;
+      dma_load4(rsrc_words((const void*)(uintptr_t)sat[i], sbytes[i]), live ? svoff[i] : kOob, 0u, stage + slds[i]);
+      sat[i] += live ? C::WK * sstep[i] : 0;
+    }
+  };
+  // Waves of a group meet (one alone only waits for its own LDS reads)
+  auto meet = [&]() {
+    if constexpr (C::NW > 1) lds_barrier();
+    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
 
-    // Load l of k-step d into stage d % STAGES; past the last block every lane is out of range (zeros, no traffic).
-    auto issue_one = [&](int d, auto lc) {
-      constexpr int l = decltype(lc)::value;
-      const uint32_t stage = ring + (uint32_t)(d % C::STAGES) * C::STAGE;
-      const bool live = d * C::WK + group < g.kb;
-      const uint32_t kbyte = live ? (uint32_t)(d * C::WK + group) * kBlock : 0u;
-      if constexpr (l < C::A_PT + C::B_PT) {
-        constexpr bool is_a = l < C::A_PT;
-        constexpr int i = is_a ? l : l - C::A_PT;
-        const uint32_t c = chunk ^ (C::NW % 2 && i % 2 ? 64u : 0u);
-        const uint32_t voff = live && kbyte + c < rb ? row_off + c : kOob;
-        dma_load16(is_a ? ra : rbw, voff, kbyte + i * gstep,
-                   stage + (is_a ? 0u : C::B_OFF) + (uint32_t)(wave + i * C::NW) * 1024u);
-      } else {
-        constexpr int i = l - C::A_PT - C::B_PT;
-        dma_load4(rsrc_words((const void*)(uintptr_t)sat[i], sbytes[i]), live ? svoff[i] : kOob, 0u, stage + slds[i]);
-        sat[i] += live ? C::WK * sstep[i] : 0;
-      }
-    };
-    auto issue = [&](int d) { static_for<C::PER_STAGE>([&](auto lc) { issue_one(d, lc); }); };
-    // Waves of a group meet (one alone only waits for its own LDS reads)
-    auto meet = [&]() {
-      if constexpr (C::NW > 1) lds_barrier();
-      else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    };
+  // The k-steps as one stream of FM x FN slots, each starting a block's MFMA and adding the result of LAG slots
+  // before, so that the ALU does not wait for the MFMA just started.  Columns of blocks go in pairs,
+  // (i, j), (i, j + 1), (i + 1, j), ...: A's fragment i is used twice in a row, which spreads its refill for
+  // the next stage (in place, after its last use) over the whole last pair of a k-step, and its first
+  // use there over the whole first pair.  B's fragments go round a ring of two pairs, each read
+  // during the pair before.  At the last pair every read of the stage has been issued: there the
+  // waves wait for the next stage's loads (a whole k-step old) and meet, the loads of the stage after
+  // go out into the one just read, and the reads run on into the next stage.  (EARLY_A: A's go out during the second
+  // pair already, when every wave has its fragments, so that they have nearly two k-steps to arrive: with
+  // two stages of 64 KiB the loads alone took as long as the k-step, 1.39 us, and 4096^3 65 us; now 61.)
+  // sched_barrier(0) keeps the slots, and each MFMA before its slot's fmas, in this order.
+  constexpr int NP = C::FN / 2, PS = 2 * C::FM, NS = C::FM * C::FN, LAG = 2;   // pairs; slots of a pair, of a k-step
+  constexpr int RING = NP == 1 ? 2 : 4;
+  static_assert(C::FN % 2 == 0 && (NP == 1 || NP % 2 == 0) && C::FM >= 2, "pairs of columns");
+  v4u a[C::FM][2], b[RING][2];   // column j in b[j % RING]
+  v4f sbv[RING];                 // (BROW) the four columns' scales
+  float sa[C::FM], sbt = 0.0f;
+  // LDS addresses in the stage being read, moved on behind each barrier.  (Chunk 4 + lg is 64 bytes from chunk lg,
+  // with the sign of one of the permutation's bits: an exclusive or, since rows are 128 bytes.)
+  uint32_t la, lb, lsa, lsb;
+  auto aim_reads = [&]() {
+    la = ring + (wm * C::WTM + lr) * kBlock + c0;
+    lb = ring + C::B_OFF + (wn * C::WTN + lr) * kBlock + c0;
+    lsa = ring + C::S_OFF + (wm * C::WTM + lr) * 4;
+    lsb = ring + C::SB_OFF + (wn * C::WTN + (BROW ? 4 * lg : 0)) * 4;
+  };
+  auto at = [](uint32_t x) { return (const lds_u8*)(uintptr_t)x; };
+  auto read_a = [&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    a[i][0] = ld_v4u(at(la) + i * 16 * kBlock);
+    a[i][1] = ld_v4u(at(la ^ 64u) + i * 16 * kBlock);
+  };
+  auto read_b = [&](auto jc) {
+    constexpr int j = decltype(jc)::value;
+    b[j % RING][0] = ld_v4u(at(lb) + j * 16 * kBlock);
+    b[j % RING][1] = ld_v4u(at(lb ^ 64u) + j * 16 * kBlock);
+  };
+  auto read_sb = [&](auto jc) {
+    constexpr int j = decltype(jc)::value;
+    if constexpr (BROW) sbv[j % RING] = ld_v4f(at(lsb) + j * 64);
+  };
+  auto read_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) sa[i] = *(const __attribute__((address_space(3))) float*)(at(lsa) + i * 64);
+    if constexpr (!BROW) sbt = *(const __attribute__((address_space(3))) float*)at(lsb);
+  };
+
+  // STREAM: one tile's loads follow the other's without a gap, so that no tile waits for its first stages or for the
+  // stores of the last.  Takes more than STAGES k-steps a tile: the bias of tile t + 1 goes to the place of
+  // tile t - 1's, which every wave has read once it has met the others in tile t's first k-step.
+  int turn = 0;      // of the bias: tiles alternate
+  int g0 = 0;        // k-steps before the tile's
+  for (int t = first; t < T; t += stride) {
+    const bool more = C::STREAM && t + stride < T;
+    if (!C::STREAM || t == first) aim(t, turn);
+    const int tm0 = m0, tn0 = n0, trows = rows, tcols = cols;     // the tile that is computed
 
     v4f acc[C::FM][C::FN];
 #pragma unroll
@@ -193,67 +267,25 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{};
 
-    // The k-steps as one stream of FM x FN slots, each starting a block's MFMA and adding the result of LAG slots
-    // before, so that the ALU does not wait for the MFMA just started.  Columns of blocks go in pairs,
-    // (i, j), (i, j + 1), (i + 1, j), ...: A's fragment i is used twice in a row, which spreads its refill for
-    // the next stage (in place, after its last use) over the whole last pair of a k-step, and its first
-    // use there over the whole first pair.  B's fragments go round a ring of two pairs, each read
-    // during the pair before.  At the last pair every read of the stage has been issued: there the
-    // waves wait for the next stage's loads (a whole k-step old) and meet, the loads of the stage after
-    // go out into the one just read, and the reads run on into the next stage.  (EARLY_A: A's go out during the second
-    // pair already, when every wave has its fragments, so that they have nearly two k-steps to arrive: with
-    // two stages of 64 KiB the loads alone took as long as the k-step, 1.39 us, and 4096^3 65 us; now 61.)
-    // sched_barrier(0) keeps the slots, and each MFMA before its slot's fmas, in this order.
-    constexpr int NP = C::FN / 2, PS = 2 * C::FM, NS = C::FM * C::FN, LAG = 2;   // pairs; slots of a pair, of a k-step
-    constexpr int RING = NP == 1 ? 2 : 4;
-    static_assert(C::FN % 2 == 0 && (NP == 1 || NP % 2 == 0) && C::FM >= 2, "pairs of columns");
-    v4u a[C::FM][2], b[RING][2];   // column j in b[j % RING]
-    v4f sbv[RING];                 // (BROW) the four columns' scales
-    float sa[C::FM], sbt = 0.0f;
-    // LDS addresses in the stage being read, moved on behind each barrier.  (Chunk 4 + lg is 64 bytes from chunk lg,
-    // with the sign of one of the permutation's bits: an exclusive or, since rows are 128 bytes.)
-    const uint32_t base = ring;
-    uint32_t la = base + (wm * C::WTM + lr) * kBlock + c0, lb = base + C::B_OFF + (wn * C::WTN + lr) * kBlock + c0;
-    uint32_t lsa = base + C::S_OFF + (wm * C::WTM + lr) * 4;
-    uint32_t lsb = base + C::SB_OFF + (wn * C::WTN + (BROW ? 4 * lg : 0)) * 4;
-    auto at = [](uint32_t x) { return (const lds_u8*)(uintptr_t)x; };
-    auto read_a = [&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      a[i][0] = ld_v4u(at(la) + i * 16 * kBlock);
-      a[i][1] = ld_v4u(at(la ^ 64u) + i * 16 * kBlock);
-    };
-    auto read_b = [&](auto jc) {
-      constexpr int j = decltype(jc)::value;
-      b[j % RING][0] = ld_v4u(at(lb) + j * 16 * kBlock);
-      b[j % RING][1] = ld_v4u(at(lb ^ 64u) + j * 16 * kBlock);
-    };
-    auto read_sb = [&](auto jc) {
-      constexpr int j = decltype(jc)::value;
-      if constexpr (BROW) sbv[j % RING] = ld_v4f(at(lsb) + j * 64);
-    };
-    auto read_scales = [&]() {
+    if (!C::STREAM || t == first) {
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i) sa[i] = *(const __attribute__((address_space(3))) float*)(at(lsa) + i * 64);
-      if constexpr (!BROW) sbt = *(const __attribute__((address_space(3))) float*)at(lsb);
-    };
-
-    // the tile's bias goes the same way, two columns a lane (a lone last column, or a bias not on four bytes, would
-    // not: it is read when the outputs are made)
-    const bool bias_staged = (((uintptr_t)g.bias | (uintptr_t)(2 * g.N)) & 3) == 0;
-    const uint32_t bias_bytes = g.bias ? (uint32_t)cols * 2u : 0u;
-    constexpr int BI = (C::BN + 127) / 128;
-    if (bias_staged)
-      dma_load4(rsrc_words(g.bias + n0, bias_bytes), (uint32_t)((wave % BI) * 64 + lane) * 4u, 0u,
-                (uint32_t)(uintptr_t)smem + C::BIAS_OFF + (uint32_t)(wave % BI) * 256u);
-#pragma unroll
-    for (int d = 0; d < C::STAGES; ++d) issue(d);
-    wait_vmcnt_n<(C::STAGES - 1) * C::PER_STAGE>();
-    meet();
-    read_scales();
-    static_for<C::FM>(read_a);
-    static_for<2>(read_b);
-    static_for<2>(read_sb);
+      for (int d = 0; d < C::STAGES; ++d)
+        static_for<C::PER_STAGE>([&](auto lc) { issue_one(d * C::WK + group, d, d * C::WK + group < g.kb, lc); });
+      wait_vmcnt_n<(C::STAGES - 1) * C::PER_STAGE>();
+      meet();
+      aim_reads();
+      read_scales();
+      static_for<C::FM>(read_a);
+      static_for<2>(read_b);
+      static_for<2>(read_sb);
+    }
     for (int d = 0; d < steps; ++d) {
+      const int slot = (C::STREAM ? g0 + d : d) % C::STAGES;
+      const int ahead = d + C::STAGES, ik = C::STREAM && ahead >= steps ? ahead - steps : ahead * C::WK + group;
+      const bool live = C::STREAM ? ahead < steps || more : ik < g.kb;
+      if constexpr (C::STREAM) {
+        if (ahead == steps && more) aim(t + stride, turn ^ 1);     // from here on the loads are the next tile's
+      }
       float s[C::FM];
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) s[i] = BROW ? sa[i] : sa[i] * sbt;
@@ -269,7 +301,7 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
         if constexpr (r == 0 && pair == NP - 1) {
           wait_vmcnt_n<(C::STAGES - 2) * C::PER_STAGE + (C::EARLY_A ? C::A_PT : 0)>();
           meet();
-          const uint32_t move = (uint32_t)((d + 1) % C::STAGES ? C::STAGE : -(C::STAGES - 1) * C::STAGE);
+          const uint32_t move = (uint32_t)(slot + 1 < C::STAGES ? C::STAGE : -(C::STAGES - 1) * C::STAGE);
           la += move;
           lb += move;
           lsa += move;
@@ -288,16 +320,16 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
         if constexpr (NP == 1 && i == C::FM - 1) read_b(std::integral_constant<int, j>{});
         if constexpr (pair == NP - 1) {
           if constexpr (n % 2 == 1) read_a(std::integral_constant<int, i>{});
-          constexpr int first = C::EARLY_A ? C::A_PT : 0, count = C::PER_STAGE - first;
+          constexpr int early = C::EARLY_A ? C::A_PT : 0, count = C::PER_STAGE - early;
           static_for<count>([&](auto lc) {
             constexpr int l = decltype(lc)::value;
-            if constexpr (l * PS / count == r) issue_one(d + C::STAGES, std::integral_constant<int, first + l>{});
+            if constexpr (l * PS / count == r) issue_one(ik, slot, live, std::integral_constant<int, early + l>{});
           });
         }
         if constexpr (C::EARLY_A && pair == 1) {
           static_for<C::A_PT>([&](auto lc) {
             constexpr int l = decltype(lc)::value;
-            if constexpr (l * PS / C::A_PT == r) issue_one(d + C::STAGES, lc);
+            if constexpr (l * PS / C::A_PT == r) issue_one(ik, slot, live, lc);
           });
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -308,8 +340,10 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
 
     // outputs: each wave's through its own part of LDS, so that a store fills whole lines.  (The lane is read
     // afresh: offsets worked out from it would otherwise be kept, in spilled registers, through every k-step.)
-    wait_vmcnt_n<0>();
-    lds_barrier();
+    if constexpr (!C::STREAM) {
+      wait_vmcnt_n<0>();
+      lds_barrier();
+    }
     int ol = lane;
     asm volatile("" : "+v"(ol));
     const int olr = ol & 15, olg = ol >> 4;
@@ -333,16 +367,15 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
         });
       }
     }
-    lds_u8* const so = smem + wave * C::OUT_WAVE;
+    const uint32_t so = (uint32_t)(uintptr_t)smem + C::OUT_OFF + wave * C::OUT_WAVE;
     auto finish = [&]() {
       v2u bias[C::FN];
       if (bias_staged) {
+        const lds_u8* const at_bias = smem + C::BIAS_OFF + turn * C::BIAS + (wn * C::WTN + 4 * olg) * 2;
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-          bias[j] =
-              *(const __attribute__((address_space(3))) v2u*)(smem + C::BIAS_OFF + (wn * C::WTN + j * 16 + 4 * olg) * 2);
+        for (int j = 0; j < C::FN; ++j) bias[j] = *(const __attribute__((address_space(3))) v2u*)(at_bias + j * 32);
       } else {
-        const __amdgpu_buffer_rsrc_t rbias = make_rsrc(g.bias + n0, bias_bytes);
+        const __amdgpu_buffer_rsrc_t rbias = make_rsrc(g.bias + tn0, g.bias ? (uint32_t)tcols * 2u : 0u);
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
           uint32_t w[4];
@@ -352,54 +385,71 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
           bias[j] = v2u{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
         }
       }
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        const float b4[4] = {bf16_lo(bias[j][0]), bf16_hi(bias[j][0]), bf16_lo(bias[j][1]), bf16_hi(bias[j][1])};
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-          const int row = i * 16 + olr, c = (2 * j + (olg >> 1)) ^ (row & (C::CH - 1));
-          *(__attribute__((address_space(3))) v2u*)(so + row * (C::WTN * 2) + c * 16 + (olg & 1) * 8) = out4(acc[i][j], b4);
-        }
-      }
-      asm volatile("" ::: "memory");   // (one wave's LDS operations execute in order)
       constexpr int RPI = 64 / C::CH;  // rows per store
-      const int c = ol % C::CH, col = n0 + wn * C::WTN + c * 8, orow = wm * C::WTM + ol / C::CH;
-      if ((g.N & 7) == 0) {
-        const __amdgpu_buffer_rsrc_t rc = make_rsrc(g.C + (int64_t)m0 * g.N, (uint32_t)rows * (uint32_t)g.N * 2u);
-        const uint32_t to = ((uint32_t)orow * (uint32_t)g.N + (uint32_t)col) * 2u;
+      const int c = ol % C::CH, col = tn0 + wn * C::WTN + c * 8, orow = wm * C::WTM + ol / C::CH;
+      const __amdgpu_buffer_rsrc_t rc = make_rsrc(g.C + (int64_t)tm0 * g.N, (uint32_t)trows * (uint32_t)g.N * 2u);
+      // chunk q of row r is at (q ^ r) % CH.  Block j's chunks are 2 j and 2 j + 1: an exclusive or of 32 j bytes away
+      // from block 0's (a row is a power of two, and starts at a multiple of itself).
+      constexpr uint32_t PITCH = C::WTN * 2;
+      static_assert((PITCH & (PITCH - 1)) == 0 && C::OUT_OFF % PITCH == 0 && C::OUT_WAVE % PITCH == 0 && PITCH <= 256, "rows");
+      const int wrow = olr & (C::OR - 1);
+      const uint32_t put = so + wrow * PITCH + ((((olg >> 1) ^ wrow) & (C::CH - 1)) * 16) + (olg & 1) * 8;
 #pragma unroll
-        for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
-          const int row = r0 + ol / C::CH;
-          const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
-          __builtin_amdgcn_raw_buffer_store_b128(v, rc, col < g.N ? to + (uint32_t)r0 * (uint32_t)g.N * 2u : kOob, 0, 0);
-        }
-      } else {
-        // rows that start anywhere: the same sixteen bytes to any element's address, the row's last piece by elements
-        uint16_t* const to = g.C + (int64_t)(m0 + orow) * g.N + col;
+      for (int part = 0; part < C::WTM; part += C::OR) {
 #pragma unroll
-        for (int r0 = 0; r0 < C::WTM; r0 += RPI) {
-          const int row = r0 + ol / C::CH;
-          const v4u v = ld_v4u(so + row * (C::WTN * 2) + ((c ^ (row & (C::CH - 1))) * 16));
-          if (orow + r0 >= rows) continue;
-          uint16_t* const p = to + (int64_t)r0 * g.N;
-          if (col + 8 <= g.N) {
-            *(u32x4_any*)p = v;
-          } else {
+        for (int j = 0; j < C::FN; ++j) {
+          const float b4[4] = {bf16_lo(bias[j][0]), bf16_hi(bias[j][0]), bf16_lo(bias[j][1]), bf16_hi(bias[j][1])};
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (col + k < g.N) p[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
+          for (int i = part / 16; i < (part + C::OR + 15) / 16; ++i) {
+            const v2u x = out4(acc[i][j], b4);
+            if (C::OR >= 16 || olr / C::OR == part % 16 / C::OR)
+              *(__attribute__((address_space(3))) v2u*)(uintptr_t)((put ^ (32u * j)) + (C::OR >= 16 ? (i * 16 - part) * PITCH : 0)) = x;
           }
         }
+        asm volatile("" ::: "memory");   // (one wave's LDS operations execute in order)
+        auto take = [&](int r0) {
+          const int row = r0 + ol / C::CH;
+          return ld_v4u(at(so + row * PITCH + ((c ^ (row & (C::CH - 1))) * 16)));
+        };
+        if ((g.N & 7) == 0) {
+          const uint32_t to = ((uint32_t)(orow + part) * (uint32_t)g.N + (uint32_t)col) * 2u;
+#pragma unroll
+          for (int r0 = 0; r0 < C::OR; r0 += RPI)
+            __builtin_amdgcn_raw_buffer_store_b128(take(r0), rc, col < g.N ? to + (uint32_t)r0 * (uint32_t)g.N * 2u : kOob, 0, 0);
+        } else {
+          // rows that start anywhere: the same sixteen bytes to any element's address, the row's last piece by elements
+          uint16_t* const to = g.C + (int64_t)(tm0 + orow + part) * g.N + col;
+#pragma unroll
+          for (int r0 = 0; r0 < C::OR; r0 += RPI) {
+            const v4u v = take(r0);
+            if (orow + part + r0 >= trows) continue;
+            uint16_t* const p = to + (int64_t)r0 * g.N;
+            if (col + 8 <= g.N) {
+              *(u32x4_any*)p = v;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (col + k < g.N) p[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
+            }
+          }
+        }
+        asm volatile("" ::: "memory");
       }
     };
     if (group == 0) finish();
-    if (t + stride < T) lds_barrier();   // the next tile's loads go where the outputs were read from
+    if constexpr (C::STREAM) {
+      g0 = (g0 + steps) % C::STAGES;
+      turn ^= 1;
+    } else if (t + stride < T) {
+      lds_barrier();   // the next tile's loads go where the outputs were read from
+    }
   }
+  if constexpr (C::STREAM) wait_vmcnt_n<0>();     // nothing may still be on its way into LDS when the workgroup's is given up
 }
 
 template <class C, bool BROW>
 __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
+  __shared__ __attribute__((aligned(256))) uint8_t smem[C::LDS];
   block_tiles<C, BROW>(g, (lds_u8*)smem, blockIdx.x, gridDim.x);
 }
 
@@ -407,7 +457,7 @@ __global__ __launch_bounds__(C::NT) void sk_gemm_block(BlockGemm g) {
 // as the first's end, and a small problem's three parts run side by side.
 template <class C>
 __global__ __launch_bounds__(C::NT) void sk_gemm_block_pair(BlockGemm a, BlockGemm b, ColumnSums c) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
+  __shared__ __attribute__((aligned(256))) uint8_t smem[C::LDS];
   const int ta = a.tiles_m * a.tiles_n, tb = b.tiles_m * b.tiles_n, wg = blockIdx.x;
   if (wg < ta) block_tiles<C, false>(a, (lds_u8*)smem, wg, ta);
   else if (wg < ta + tb) block_tiles<C, true>(b, (lds_u8*)smem, wg - ta, tb);
@@ -527,7 +577,14 @@ __global__ __launch_bounds__(64 * NWK) void sk_gemm_block_rows(BlockGemm g) {
 }
 
 template <class C>
-hipError_t launch_tiled(BlockGemm g, bool b_tile, int grid_cap, hipStream_t s) {
+hipError_t launch_tiled(BlockGemm g, bool b_tile, int grid_cap, int cus, hipStream_t s) {
+  if constexpr (C::EARLY_A && !C::STREAM) {
+    // Such a tile fills a compute unit, and where there are several to each, one workgroup to a unit takes every cus-th as one
+    // stream: 8192x8192x512 65 -> 52 us, 8192x8192x2048 130 -> 124, 8192x8192x4096 227 -> 225, but 6144 327 / 327 and
+    // 8192 424 / 430, where the units' different speeds tell (they are dealt single tiles as they become free).
+    if (g.kb > C::STAGES && g.kb < 48 && (int64_t)cdiv(g.M, C::BM) * cdiv(g.N, C::BN) > cus)
+      return launch_tiled<BlockCfg<C::BM, C::BN, C::WM, C::WN, C::STAGES, 1, true>>(g, b_tile, cus, cus, s);
+  }
   g.tiles_m = cdiv(g.M, C::BM);
   g.tiles_n = cdiv(g.N, C::BN);
   const int64_t T = (int64_t)g.tiles_m * g.tiles_n;
@@ -597,7 +654,7 @@ hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int 
   // 1x4096x4096 5.5 us against 6.5 with 8 and one, 256x256x2048 5.0 / 4.4.
   if (grid_cap <= 0 && tiles(16, 16) <= (g.kb <= 16 ? 2 : 1) * (int64_t)cus)
     return g.kb < 32 ? launch_rows<1, 1, 8, 1>(g, b_tile, s) : launch_rows<1, 1, 16, 2>(g, b_tile, s);
-  return choose_tile(tiles, g.M, g.kb, cus, [&](auto cfg) { return launch_tiled<decltype(cfg)>(g, b_tile, grid_cap, s); });
+  return choose_tile(tiles, g.M, g.kb, cus, [&](auto cfg) { return launch_tiled<decltype(cfg)>(g, b_tile, grid_cap, cus, s); });
 }
 
 // (the tile is the two products' together also where only one is wanted, so that its bits are the same)

@@ -164,13 +164,13 @@ def _check_gemm(M, N, K, block, exact, seed=0, bias=True, **kw):
 
 
 # every kernel: few outputs (short and long K), tiles of 32x32, 64x32, 64x64 (one and two groups of waves), 128x64, 128x128 (two and four stages), 256x128
-# and 256x256, whole and ragged in each dimension
+# and 256x256 (one and several to a workgroup, k-steps even and odd in number), whole and ragged in each dimension
 SIZES = [(1, 1, 16), (1, 64, 128), (1, 4096, 4096), (7, 100, 48), (16, 512, 1040), (17, 130, 2064), (32, 96, 256),
          (33, 999, 144), (64, 640, 1000), (65, 63, 16), (100, 100, 2060), (256, 256, 512), (200, 1000, 400),
          (1000, 1500, 272), (777, 4099, 300), (1540, 3000, 528), (4096, 4096, 128), (3000, 4100, 2060),
          (500, 700, 400), (40, 8200, 640), (300, 3000, 2064), (290, 2999, 4100), (2304, 2900, 272), (2310, 2897, 1000),
          (1500, 3100, 300), (16, 8192, 2064), (31, 8300, 400), (1037, 1290, 528), (1100, 1920, 300), (2048, 2048, 400), (200, 300, 1520),
-         (130, 250, 4112), (300, 330, 1000)]
+         (130, 250, 4112), (300, 330, 1000), (4200, 4400, 400), (4100, 4501, 300), (8300, 2100, 656), (8200, 8300, 272)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
