@@ -8,7 +8,8 @@
 // and their gradients.  A row is held in registers by TPR threads (a wave, with four rows to a workgroup, or
 // a workgroup), CH pieces of eight elements each, so every tensor is read once and written once: all of it
 // is bound by HBM (by latency for few rows).  Statistics and sums are fp32.  Rows need no alignment beyond
-// their elements' (a row of odd length starts anywhere).
+// their elements' (a row of odd length starts anywhere).  Gated, with the next norm in fp8, 16384x4096 bf16: 103 us,
+// 4.6 TB/s (a copy of 2 GiB: 4.9).  Backward of both, 4095x2047 fp32: 62 us, 3.8 TB/s, 6 us of it the column sums.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
