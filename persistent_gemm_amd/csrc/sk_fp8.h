@@ -12,6 +12,16 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 // The same bytes at any element's address: a row of an odd length starts anywhere.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
+// A launch with its arguments given by address: the triple-chevron form passes them through a call-configuration stack,
+// 0.2 us of the 2.4 that a launch takes the host.
+template <class... P>
+inline hipError_t launch(void (*kernel)(P...), dim3 grid, int threads, hipStream_t s, P... a) {
+  void* args[] = {(void*)&a...};
+  const hipError_t e = hipLaunchKernel((const void*)kernel, grid, dim3((unsigned)threads), args, 0, s);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
+}
+
 constexpr int kBlock = 128;              // elements that share a scale
 constexpr float kScaleMin = 0x1p-126f;   // the smallest scale (an empty or all-zero block has it)
 constexpr uint32_t kAbs = 0x7fffffffu;

@@ -530,11 +530,15 @@ __global__ __launch_bounds__(64 * NWK) void sk_gemm_block_rows(BlockGemm g) {
       for (int j = 0; j < NB; ++j) {
         if constexpr (BROW) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) sb[u][j][q] = g.SB[(int64_t)ks * g.N + min(n0 + j * 16 + 4 * lg + q, g.N - 1)];
+          for (int q = 0; q < 4; ++q) {
+            const float s = g.SB[(int64_t)ks * g.N + min(n0 + j * 16 + 4 * lg + q, g.N - 1)];
+            sb[u][j][q] = k < g.kb ? s : 0.0f;
+          }
         } else {
           // (columns past N may start the next 128: their outputs are not stored)
           const int n = min(n0 + j * 16, g.N - 1);
-          sb[u][j][0] = g.SB[(int64_t)(n / kBlock) * g.kb + ks];
+          const float s = g.SB[(int64_t)(n / kBlock) * g.kb + ks];
+          sb[u][j][0] = k < g.kb ? s : 0.0f;
         }
       }
     }
@@ -592,19 +596,15 @@ hipError_t launch_tiled(BlockGemm g, bool b_tile, int grid_cap, int cus, hipStre
   const int64_t T = (int64_t)g.tiles_m * g.tiles_n;
   if (T > 0x7fffffff) return hipErrorInvalidValue;
   const int grid = grid_cap > 0 && grid_cap < T ? grid_cap : (int)T;
-  if (b_tile) hipLaunchKernelGGL((sk_gemm_block<C, false>), dim3(grid), dim3(C::NT), 0, s, g);
-  else hipLaunchKernelGGL((sk_gemm_block<C, true>), dim3(grid), dim3(C::NT), 0, s, g);
-  return hipGetLastError();
+  return launch(b_tile ? sk_gemm_block<C, false> : sk_gemm_block<C, true>, dim3(grid), C::NT, s, g);
 }
 
 template <int MB, int NB, int NWK, int U>
 hipError_t launch_rows(BlockGemm g, bool b_tile, hipStream_t s) {
   g.tiles_m = cdiv(g.M, 16 * MB);
   g.tiles_n = cdiv(g.N, 16 * NB);
-  const dim3 grid((unsigned)(g.tiles_m * g.tiles_n)), block(64 * NWK);
-  if (b_tile) hipLaunchKernelGGL((sk_gemm_block_rows<MB, NB, NWK, U, false>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((sk_gemm_block_rows<MB, NB, NWK, U, true>), grid, block, 0, s, g);
-  return hipGetLastError();
+  return launch(b_tile ? sk_gemm_block_rows<MB, NB, NWK, U, false> : sk_gemm_block_rows<MB, NB, NWK, U, true>,
+                dim3((unsigned)(g.tiles_m * g.tiles_n)), 64 * NWK, s, g);
 }
 
 template <class C>
@@ -616,8 +616,7 @@ hipError_t launch_pair(BlockGemm a, BlockGemm b, const ColumnSums& c, hipStream_
   const int64_t sums = c.out ? cdiv(c.N, C::NT / kSumSlices) : 0;
   const int64_t grid = (int64_t)a.tiles_m * a.tiles_n + (int64_t)b.tiles_m * b.tiles_n + sums;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((sk_gemm_block_pair<C>), dim3((unsigned)grid), dim3(C::NT), 0, s, a, b, c);
-  return hipGetLastError();
+  return launch(sk_gemm_block_pair<C>, dim3((unsigned)grid), C::NT, s, a, b, c);
 }
 
 // The tile by how many of each shape there are to `cus` compute units (times below: 256 of them, one product).  A tile
@@ -670,8 +669,7 @@ hipError_t launch_gemm_block_pair(const BlockGemm& a, const BlockGemm& b, const 
 
 hipError_t launch_column_sums_bf16(const ColumnSums& c, hipStream_t s) {
   constexpr int NT = 512;
-  hipLaunchKernelGGL((sk_column_sums<NT>), dim3((unsigned)cdiv(c.N, NT / kSumSlices)), dim3(NT), 0, s, c);
-  return hipGetLastError();
+  return launch(sk_column_sums<NT>, dim3((unsigned)cdiv(c.N, NT / kSumSlices)), NT, s, c);
 }
 
 }  // namespace sk

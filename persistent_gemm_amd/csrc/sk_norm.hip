@@ -480,8 +480,7 @@ hipError_t forward(const NormArgs& a, int cus, hipStream_t s) {
   const int rpw = rows_per_wg<TPR>(), threads = TPR == 64 ? 256 : TPR;
   // as many workgroups as run at once (about 1024 threads to a compute unit), each on a run of rows
   const int wgs = ceil_div(a.T, rpw), most = cus * (1024 / threads);
-  hipLaunchKernelGGL((sk_norm_forward<T, POST, PRE, FP8, TPR, CH, SHORT>), dim3(min(wgs, most)), dim3(threads), 0, s, a);
-  return hipGetLastError();
+  return launch(sk_norm_forward<T, POST, PRE, FP8, TPR, CH, SHORT>, dim3(min(wgs, most)), threads, s, a);
 }
 
 template <class T, bool POST, bool PRE, bool FP8>
@@ -516,12 +515,10 @@ int grad_wgs(const NormGradArgs& a) { return ceil_div(a.chunks, grad_rpw(a.D) * 
 template <class T, bool POST, bool PRE, int TPR, int CH, bool SHORT = false>
 hipError_t backward(const NormGradArgs& a, hipStream_t s) {
   const int wgs = grad_wgs(a);
-  hipLaunchKernelGGL((sk_norm_backward<T, POST, PRE, TPR, CH, SHORT>), dim3(wgs), dim3(TPR == 64 ? 256 : TPR), 0, s, a);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = launch(sk_norm_backward<T, POST, PRE, TPR, CH, SHORT>, dim3(wgs), TPR == 64 ? 256 : TPR, s, a);
   if (e != hipSuccess) return e;
   const bool gate = a.dgate && a.gate_rows > 1 && (a.groups == 1 || a.chunks_per_gate > 1);
-  hipLaunchKernelGGL((sk_norm_sums<T>), dim3(ceil_div(a.D, 32), 3 + (gate ? a.groups : 0)), dim3(32 * kSlices), 0, s, a, wgs);
-  return hipGetLastError();
+  return launch(sk_norm_sums<T>, dim3(ceil_div(a.D, 32), 3 + (gate ? a.groups : 0)), 32 * kSlices, s, a, wgs);
 }
 
 template <class T, bool POST, bool PRE>

@@ -202,13 +202,12 @@ __global__ __launch_bounds__(2048 / RPT) void sk_quantize_block(QuantArgs a) {
 
 template <class T, bool TILE, bool SUMS, bool SHORT, int RPT>
 hipError_t launch_form(const QuantArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.kb * (unsigned)a.rb), block(2048 / RPT);
-  if (a.q && a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, true, SUMS, SHORT, RPT>), grid, block, 0, s, a);
-  else if (a.q) hipLaunchKernelGGL((sk_quantize_block<T, TILE, true, false, SUMS, SHORT, RPT>), grid, block, 0, s, a);
-  else if (a.qt) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, true, SUMS, SHORT, RPT>), grid, block, 0, s, a);
-  else if constexpr (SUMS) hipLaunchKernelGGL((sk_quantize_block<T, TILE, false, false, SUMS, SHORT, RPT>), grid, block, 0, s, a);
-  else return hipErrorInvalidValue;
-  return hipGetLastError();
+  auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)a.kb * (unsigned)a.rb), 2048 / RPT, s, a); };
+  if (a.q && a.qt) return go(sk_quantize_block<T, TILE, true, true, SUMS, SHORT, RPT>);
+  if (a.q) return go(sk_quantize_block<T, TILE, true, false, SUMS, SHORT, RPT>);
+  if (a.qt) return go(sk_quantize_block<T, TILE, false, true, SUMS, SHORT, RPT>);
+  if constexpr (SUMS) return go(sk_quantize_block<T, TILE, false, false, SUMS, SHORT, RPT>);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
