@@ -658,8 +658,24 @@ hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int 
   return choose_tile(tiles, g.M, g.kb, cus, [&](auto cfg) { return launch_tiled<decltype(cfg)>(g, b_tile, grid_cap, cus, s); });
 }
 
-// (the tile is the two products' together also where only one is wanted, so that its bits are the same)
+// Everything is chosen by both products' sizes also where only one is wanted, so that its bits are the same.
 hipError_t launch_gemm_block_pair(const BlockGemm& a, const BlockGemm& b, const ColumnSums& c, int cus, hipStream_t s) {
+  // One much longer along K has few outputs, so tiles that suit the other leave most units idle over its k-steps: one
+  // after the other, each with tiles of its own, the sums beside the shorter.  (K of 27 blocks and 2) 3362x224x540
+  // 27.6 -> 18.9 us, (32 and 3) 4096x300x4000 71 -> 39, but (13 and 3) 1652x384x1646 19.1 -> 20.7, (12 and 27)
+  // 3456x1447x69 21.9 -> 24.1.
+  if ((a.kb >= 16 && a.kb >= 4 * b.kb) || (b.kb >= 16 && b.kb >= 4 * a.kb)) {
+    const bool a_short = a.kb < b.kb;
+    const BlockGemm &first = a_short ? a : b, &second = a_short ? b : a;
+    hipError_t e = hipSuccess;
+    if (first.C || c.out) {
+      auto tiles = [&](int bm, int bn) { return (int64_t)cdiv(first.M, bm) * cdiv(first.N, bn); };
+      e = choose_tile(tiles, first.M, first.kb, cus, [&](auto cfg) {
+        return launch_pair<decltype(cfg)>(a_short ? a : BlockGemm{}, a_short ? BlockGemm{} : b, c, s);
+      });
+    }
+    return e != hipSuccess || !second.C ? e : launch_gemm_block(second, !a_short, 0, cus, s);
+  }
   auto tiles = [&](int bm, int bn) {
     return (int64_t)cdiv(a.M, bm) * cdiv(a.N, bn) + (int64_t)cdiv(b.M, bm) * cdiv(b.N, bn);
   };

@@ -261,7 +261,8 @@ def _pair(x, wq, ws):
 # ---------------------------------------------------------------- gradients
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (16, 64, 64), (130, 70, 50), (129, 257, 300), (300, 1000, 200),
-                                   (1037, 2050, 1290), (2048, 2304, 2176), (3000, 3200, 70)])
+                                   (1037, 2050, 1290), (2048, 2304, 2176), (3000, 3200, 70),
+                                   (2050, 130, 200), (100, 2300, 300)])
 def test_backward(M, N, K):
     g = _gen(M + N + K)
     dC = (torch.randn(M, N, generator=g) * torch.exp(torch.randn(M, 1, generator=g))).to(torch.bfloat16)
