@@ -633,11 +633,16 @@ hipError_t choose_tile(Tiles&& tiles, int rows, int kb, int cus, Go&& go) {
   if (tiles(64, 64) <= cus) return kb >= 16 ? go(BlockCfg<64, 64, 2, 2, 4, 2>{}) : go(BlockCfg<64, 64, 2, 2, 4>{});
   // 1037x1290x2064 11.7 us against 13.4 with 64x64 tiles and 14.9 with 128x128
   if (tiles(128, 64) <= cus) return go(BlockCfg<128, 64, 4, 2, 4>{});
-  // 3000x4100x2060 (204 tiles) 40.6 us against 48.0 with 256x128 and 50.8 with 128x128
-  if (tiles(256, 256) * 4 >= (int64_t)cus * 3) return go(BlockCfg<256, 256, 4, 2, 2>{});
-  // 4096x2048x4096 39.7 us against 41.7 with 128x128 tiles and 57.9 with 256x256
-  if (tiles(256, 128) * 4 >= (int64_t)cus * 3) return go(BlockCfg<256, 128, 4, 2, 3>{});
-  // more than one to a unit: two at once, on half the stages (3000x2000x1000 18.8 -> 15.2 us)
+  // Large tiles, from three quarters of the units on (3000x4100x2060, 204 tiles, 35.3 us against 46.7 with 256x128 and 47.5
+  // with 128x128), or where the 128x128 ones would not run all at once and K is not short (3000x3000x8000, 144 tiles,
+  // 100 us against 133 and 123; 2200x4096x2048 26.6 / 34.9 / 29.8; but 4500x2100x700 20.3 / 23.2 / 17.6).
+  if (tiles(256, 256) * 4 >= (int64_t)cus * 3 || (tiles(128, 128) > 2 * (int64_t)cus && kb >= 8))
+    return go(BlockCfg<256, 256, 4, 2, 2>{});
+  // one to most units, with a long K: 4096x2048x4096 39.7 us against 41.7 with 128x128 tiles; 1913x2560x1792 (160 tiles)
+  // 17.4 / 16.8, 2048x3147x512 11.4 / 10.8
+  const int64_t halves = tiles(256, 128);
+  if (halves <= cus && halves * 4 >= (int64_t)cus * 3 && kb >= 16) return go(BlockCfg<256, 128, 4, 2, 3>{});
+  // more than one to a unit: two at once, on half the stages (3000x2000x1000 14.5 us against 18.1 with four stages)
   if (tiles(128, 128) > cus) return go(BlockCfg<128, 128, 4, 2, 2>{});
   // 777x4096x2048 12.5 us against 16.9 with 128x64 tiles and 19.3 with 64x64 (12.9 with the waves as 4 x 2)
   return go(BlockCfg<128, 128, 2, 4, 4>{});

@@ -170,7 +170,8 @@ SIZES = [(1, 1, 16), (1, 64, 128), (1, 4096, 4096), (7, 100, 48), (16, 512, 1040
          (1000, 1500, 272), (777, 4099, 300), (1540, 3000, 528), (4096, 4096, 128), (3000, 4100, 2060),
          (500, 700, 400), (40, 8200, 640), (300, 3000, 2064), (290, 2999, 4100), (2304, 2900, 272), (2310, 2897, 1000),
          (1500, 3100, 300), (16, 8192, 2064), (31, 8300, 400), (1037, 1290, 528), (1100, 1920, 300), (2048, 2048, 400), (200, 300, 1520),
-         (130, 250, 4112), (300, 330, 1000), (4200, 4400, 400), (4100, 4501, 300), (8300, 2100, 656), (8200, 8300, 272)]
+         (130, 250, 4112), (300, 330, 1000), (4200, 4400, 400), (4100, 4501, 300), (8300, 2100, 656), (8200, 8300, 272),
+         (2304, 2900, 2064), (2310, 2897, 2100), (2200, 4096, 1040), (2201, 4099, 1040)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
