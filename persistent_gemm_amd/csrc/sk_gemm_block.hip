@@ -587,8 +587,10 @@ hipError_t launch_tiled(BlockGemm g, bool b_tile, int grid_cap, int cus, hipStre
   if constexpr (C::EARLY_A && !C::STREAM) {
     // Such a tile fills a compute unit, and where there are several to each, one workgroup to a unit takes every cus-th as one
     // stream: 8192x8192x512 65 -> 52 us, 8192x8192x2048 130 -> 124, 8192x8192x4096 227 -> 225, but 6144 327 / 327 and
-    // 8192 424 / 430, where the units' different speeds tell (they are dealt single tiles as they become free).
-    if (g.kb > C::STAGES && g.kb < 48 && (int64_t)cdiv(g.M, C::BM) * cdiv(g.N, C::BN) > cus)
+    // 8192 424 / 430, where the units' different speeds tell (they are dealt single tiles as they become free).  With a scale
+    // per row of B, whose loop has no registers to spare: 8192x8192x512 70.5 -> 59.4 us, 4096x8192x2048 81.1 / 80.8,
+    // 6000x6000x4000 193.4 / 196.6.
+    if (g.kb > C::STAGES && g.kb < (b_tile ? 48 : 16) && (int64_t)cdiv(g.M, C::BM) * cdiv(g.N, C::BN) > cus)
       return launch_tiled<BlockCfg<C::BM, C::BN, C::WM, C::WN, C::STAGES, 1, true>>(g, b_tile, cus, cus, s);
   }
   g.tiles_m = cdiv(g.M, C::BM);
