@@ -57,8 +57,10 @@
  * (fp32 partial tiles, lock flags, an error word, and for the MX types a
  * k-step-major copy of the two scale arrays that a small kernel writes before
  * the GEMM on the same stream), kept per (device, stream), grown on demand and
- * freed by sk_release_workspace().  Device-side failures (a workgroup that
- * waited past its spin limit) are reported by sk_check().
+ * freed by sk_release_workspace().  Host threads may call on one stream at
+ * the same time (sk_gemm_mxfp4_noalloc: see there): a call keeps the scratch
+ * to itself until its last launch, and the others wait.  Device-side failures
+ * (a workgroup that waited past its spin limit) are reported by sk_check().
  *
  * HIP graphs: a stream that is being captured is refused (SK_ERR_UNSUPPORTED,
  * nothing enqueued).  The lock flags of the fixup are compared with a

@@ -51,10 +51,15 @@ struct Workspace {
   size_t t_bytes = 0;
   uint32_t* flags = nullptr;  // kMaxGrid locks, then the error word
   uint32_t epoch = 0;         // last epoch used
+  // Held from where a call takes its buffers to its last launch (a Hold): a call's kernels hand data on in them, so
+  // another host thread's kernels on the stream, or its growing or freeing of them, may not come in between.  (Recursive: the
+  // bf16 backward makes its products by the calls of their own.)  g_mu is only ever taken within it.
+  std::recursive_mutex use;
 };
+using sk::host::Hold;
 
 std::mutex g_mu;
-std::map<std::pair<int, uintptr_t>, Workspace*> g_ws;
+std::map<std::pair<int, uintptr_t>, Workspace*> g_ws;   // (an entry stays until its stream is destroyed)
 std::map<int, DeviceInfo> g_dev;
 // Compute units a stream's kernels may use, read once per (device, stream).
 std::map<std::pair<int, uintptr_t>, int> g_stream_cus;
@@ -369,53 +374,68 @@ sk_status grow(hipStream_t stream, T** buf, size_t* have, size_t want) {
   return SK_OK;
 }
 
+// Gives a workspace's buffers back; the caller holds it, or is the last to know it.
+void free_buffers(Workspace* ws) {
+  if (ws->P) hipFree(ws->P);
+  if (ws->S) hipFree(ws->S);
+  if (ws->T) hipFree(ws->T);
+  if (ws->flags) hipFree(ws->flags);
+  ws->P = nullptr;
+  ws->S = ws->T = nullptr;
+  ws->flags = nullptr;
+  ws->p_bytes = ws->s_bytes = ws->t_bytes = 0;
+}
+
 // Scratch of (device, stream), grown to p_bytes of partial tiles and s_bytes
-// of re-laid scales; called with g_mu unlocked.
-sk_status get_workspace(int dev, hipStream_t stream, size_t p_bytes, size_t s_bytes, Workspace** out) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  const auto key = std::make_pair(dev, (uintptr_t)stream);
-  Workspace*& ws = g_ws[key];
-  if (!ws) {
-    Workspace* w = new Workspace();
-    w->device = dev;
-    w->stream = stream;
-    if (hipMalloc((void**)&w->flags, sk::kFlagWords * sizeof(uint32_t)) != hipSuccess) {
-      delete w;
-      g_ws.erase(key);
+// of re-laid scales, and held for the call by *hold; called with g_mu unlocked.
+sk_status get_workspace(int dev, hipStream_t stream, size_t p_bytes, size_t s_bytes, Hold* hold, Workspace** out) {
+  Workspace* ws;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    Workspace*& at = g_ws[std::make_pair(dev, (uintptr_t)stream)];
+    if (!at) {
+      at = new Workspace();
+      at->device = dev;
+      at->stream = stream;
+    }
+    ws = at;
+  }
+  Hold h(ws->use);
+  if (!ws->flags) {
+    if (hipMalloc((void**)&ws->flags, sk::kFlagWords * sizeof(uint32_t)) != hipSuccess) {
+      ws->flags = nullptr;
       return SK_ERR_NOMEM;
     }
-    if (hipMemset(w->flags, 0, sk::kFlagWords * sizeof(uint32_t)) != hipSuccess) {
-      hipFree(w->flags);
-      delete w;
-      g_ws.erase(key);
+    if (hipMemset(ws->flags, 0, sk::kFlagWords * sizeof(uint32_t)) != hipSuccess) {
+      hipFree(ws->flags);
+      ws->flags = nullptr;
       return SK_ERR_HIP;
     }
-    ws = w;
+    ws->epoch = 0;
   }
   sk_status st = grow(stream, &ws->P, &ws->p_bytes, p_bytes);
   if (st != SK_OK) return st;
   st = grow(stream, &ws->S, &ws->s_bytes, s_bytes);
   if (st != SK_OK) return st;
+  *hold = std::move(h);
   *out = ws;
   return SK_OK;
 }
 
-// The backward pass's buffer of (device, stream), grown to t_bytes; called
-// with g_mu unlocked.
-sk_status get_aux(int dev, hipStream_t stream, size_t t_bytes, uint8_t** out) {
+// The backward passes' buffer of (device, stream), grown to t_bytes and held for the call; called with g_mu
+// unlocked.
+sk_status get_aux(int dev, hipStream_t stream, size_t t_bytes, Hold* hold, uint8_t** out) {
   Workspace* ws = nullptr;
-  sk_status st = get_workspace(dev, stream, 0, 0, &ws);
+  sk_status st = get_workspace(dev, stream, 0, 0, hold, &ws);
   if (st != SK_OK) return st;
-  std::lock_guard<std::mutex> lk(g_mu);
   st = grow(stream, &ws->T, &ws->t_bytes, t_bytes);
   if (st != SK_OK) return st;
   *out = ws->T;
   return SK_OK;
 }
 
-// Next epoch of a workspace; restarts the flags when the counter would wrap.
+// Next epoch of a workspace that the caller holds; restarts the flags when the counter would wrap.
 sk_status next_epoch(Workspace* ws, uint32_t* epoch) {
-  std::lock_guard<std::mutex> lk(g_mu);
   if (ws->epoch == 0xFFFFFFFFu) {
     if (hipMemsetAsync(ws->flags, 0, sk::kMaxGrid * sizeof(uint32_t), ws->stream) != hipSuccess) return SK_ERR_HIP;
     ws->epoch = 0;
@@ -536,6 +556,7 @@ sk_status run(const sk_gemm_args& g, bool fixed = false) {
   const int64_t sb_at = (sa_bytes + 255) / 256 * 256;
   const size_t s_need = is_mx(g.dtype) && !direct ? (size_t)(sb_at + sb_bytes) : 0;
   Scratch sc;
+  Hold hold;   // until the launch
   if (fixed) {
     const size_t p_at = ((size_t)p.scratch_bytes + 255) / 256 * 256;
     if (p_at + s_need > kStaticDataBytes) return SK_ERR_SCRATCH;
@@ -554,7 +575,7 @@ sk_status run(const sk_gemm_args& g, bool fixed = false) {
     sc.epoch = ++ss.epoch;
   } else {
     Workspace* ws = nullptr;
-    st = get_workspace(dev, stream, (size_t)p.scratch_bytes, s_need, &ws);
+    st = get_workspace(dev, stream, (size_t)p.scratch_bytes, s_need, &hold, &ws);
     if (st != SK_OK) return st;
     st = next_epoch(ws, &sc.epoch);
     if (st != SK_OK) return st;
@@ -649,7 +670,9 @@ sk_status device_for(hipStream_t stream, int* dev, int* cus) {
   return SK_OK;
 }
 sk_status refuse_capture(hipStream_t stream) { return ::refuse_capture(stream); }
-sk_status scratch(int dev, hipStream_t stream, size_t bytes, uint8_t** out) { return get_aux(dev, stream, bytes, out); }
+sk_status scratch(int dev, hipStream_t stream, size_t bytes, Hold* hold, uint8_t** out) {
+  return get_aux(dev, stream, bytes, hold, out);
+}
 bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) { return ::overlaps(a, na, b, nb); }
 
 }  // namespace host
@@ -719,7 +742,8 @@ sk_status sk_gemm_bf16_backward(const void* dC, const void* A, const void* B, vo
   const int64_t at_bt = 0, at_dct = up(dA ? bb : 0), at_at = at_dct + up(dB ? bc : 0), at_part = at_at + up(dB ? ba : 0);
   const int64_t total = at_part + (dbias ? sk::colsum_scratch_bytes((int)M, (int)N) : 0);
   uint8_t* T = nullptr;
-  st = get_aux(dev, s, (size_t)total, &T);
+  Hold hold;
+  st = get_aux(dev, s, (size_t)total, &hold, &T);
   if (st != SK_OK) return st;
   if (dA) {
     // dA[m][k] = sum_n dC[m][n] B[n][k]: A' = dC (K' = N contiguous), B' = B^T [K][N]
@@ -817,11 +841,17 @@ sk_status sk_check(void* stream) {
   // the error words this stream's launches may have set: its workspace's,
   // and the fixed scratch's of this device (sk_gemm_mxfp4_noalloc)
   uint32_t* words[2] = {nullptr, nullptr};
+  Workspace* ws = nullptr;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_ws.find(std::make_pair(dev, (uintptr_t)stream));
-    if (it != g_ws.end() && it->second) words[0] = it->second->flags + sk::kErrIndex;
+    if (it != g_ws.end()) ws = it->second;
     if (dev >= 0 && dev < kMaxDevices && g_static[dev].ptr) words[1] = (uint32_t*)g_static[dev].ptr + sk::kErrIndex;
+  }
+  Hold hold;
+  if (ws) {
+    hold = Hold(ws->use);
+    if (ws->flags) words[0] = ws->flags + sk::kErrIndex;
   }
   bool timed_out = false;
   for (uint32_t* wp : words) {
@@ -837,21 +867,20 @@ sk_status sk_check(void* stream) {
 }
 
 void sk_release_workspace(void) {
-  std::lock_guard<std::mutex> lk(g_mu);
   int cur = 0;
   const bool have_cur = hipGetDevice(&cur) == hipSuccess;
-  for (auto& kv : g_ws) {
-    Workspace* ws = kv.second;
-    if (!ws) continue;
+  std::vector<Workspace*> all;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    for (auto& kv : g_ws) all.push_back(kv.second);
+  }
+  for (Workspace* ws : all) {
+    Hold hold(ws->use);   // a call under way on another thread launches first
+    if (!ws->flags) continue;
     hipSetDevice(ws->device);
     hipStreamSynchronize(ws->stream);
-    if (ws->P) hipFree(ws->P);
-    if (ws->S) hipFree(ws->S);
-    if (ws->T) hipFree(ws->T);
-    if (ws->flags) hipFree(ws->flags);
-    delete ws;
+    free_buffers(ws);
   }
-  g_ws.clear();
   if (have_cur) hipSetDevice(cur);
 }
 
@@ -863,7 +892,8 @@ sk_status sk_debug_poison_workspace(void* stream, int64_t scratch_bytes) {
   st = device_info(&dev, &info);
   if (st != SK_OK) return st;
   Workspace* ws = nullptr;
-  st = get_workspace(dev, (hipStream_t)stream, scratch_bytes > 0 ? (size_t)scratch_bytes : 0, 0, &ws);
+  Hold hold;
+  st = get_workspace(dev, (hipStream_t)stream, scratch_bytes > 0 ? (size_t)scratch_bytes : 0, 0, &hold, &ws);
   if (st != SK_OK) return st;
   hipStream_t s = (hipStream_t)stream;
   if (ws->P && hipMemsetAsync(ws->P, 0xFF, ws->p_bytes, s) != hipSuccess) return SK_ERR_HIP;  // all-ones = NaN
@@ -925,14 +955,8 @@ sk_status sk_stream_destroy(void* stream) {
     const auto key = std::make_pair(dev, (uintptr_t)s);
     auto it = g_ws.find(key);
     if (it != g_ws.end()) {
-      Workspace* ws = it->second;
-      if (ws) {
-        if (ws->P) hipFree(ws->P);
-        if (ws->S) hipFree(ws->S);
-        if (ws->T) hipFree(ws->T);
-        if (ws->flags) hipFree(ws->flags);
-        delete ws;
-      }
+      free_buffers(it->second);   // (no call may be using the stream any more)
+      delete it->second;
       g_ws.erase(it);
     }
     g_stream_cus.erase(key);

@@ -150,7 +150,8 @@ sk_status sk_gemm_fp8_block_backward(const void* dC, const void* At, const float
   const int64_t at_s = up(dA ? M * np : 0, 256), at_qt = at_s + up(dA ? 4 * nb * M : 0, 256);
   const int64_t at_st = at_qt + up(dB ? N * mp : 0, 256), at_part = at_st + up(dB ? 4 * mb * N : 0, 256);
   uint8_t* w = nullptr;
-  st = sk::host::scratch(dev, s, (size_t)(at_part + (dbias ? 4 * mb * N : 0)), &w);
+  sk::host::Hold hold;
+  st = sk::host::scratch(dev, s, (size_t)(at_part + (dbias ? 4 * mb * N : 0)), &hold, &w);
   if (st != SK_OK) return st;
   sk::QuantArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -285,7 +286,8 @@ sk_status sk_norm_backward(const sk_norm_grad_args* p) {
   a.D = (int)g.D;
   a.gate_rows = g.gate ? (int)(g.T / g.gates) : 1;
   uint8_t* w = nullptr;
-  st = sk::host::scratch(dev, s, (size_t)sk::norm_grad_scratch_bytes(&a, cus), &w);
+  sk::host::Hold hold;
+  st = sk::host::scratch(dev, s, (size_t)sk::norm_grad_scratch_bytes(&a, cus), &hold, &w);
   if (st != SK_OK) return st;
   a.part = (float*)w;
   return sk::launch_norm_backward(a, g.elem == SK_ELEM_F32, s) == hipSuccess ? SK_OK : SK_ERR_HIP;
