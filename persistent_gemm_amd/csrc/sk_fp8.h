@@ -200,6 +200,9 @@ struct Coder;
 // fp32: t is the quotient to five bits, which holds every code and every border, and the sign of
 // x - t s (one fma, so the sign is exact) says on which side of t the quotient lies.  t is moved that way
 // by far less than the distance to the next border and far more than an ulp, and the conversion rounds it.
+// The difference is at least 2^-29 |t| s where it is not 0, which is less than the smallest fp32 for s below 2^-110: where
+// a wave has a scale below 2^-96, such blocks' values and scales are first multiplied by 2^64.  (As a branch: one more
+// product for every value, 8192x4096 bf16, takes the norm to fp8 from 26.1 to 27.1 us, the branch to 25.8.)
 template <>
 struct Coder<float> {
   static __device__ __forceinline__ BlockScale scale(uint32_t amax_bits) {
@@ -207,18 +210,30 @@ struct Coder<float> {
     float residual;
     b.s = block_scale(amax_bits, &residual);
     b.r = reciprocal(b.s);
-    // x - t s is at least 2^-29 |t| s where it is not 0, so times this at least 2 |t|: clamped to
-    // 2^-10 it is a step of its sign for every t of the codes' range (the cap only matters for
-    // s = 2^-126, where x - t s is a multiple of 2^-149 and the product still 2^-22)
-    b.c = fminf(b.r * 0x1p30f, 0x1p127f);
+    // x - t s times this is at least 2 |t|, so clamped to 2^-10 a step of its sign for every t of the codes' range
+    b.c = b.r * 0x1p30f;
     return b;
   }
-  static __device__ __forceinline__ float nudged(float x, const BlockScale& b) {
-    const float q = x * b.r;
-    const float t = bits_f((f_bits(q) + 0x40000u) & 0xfff80000u);
-    const float e = __builtin_fmaf(-t, b.s, x);
-    const float n = __builtin_amdgcn_fmed3f(e * b.c, -0x1p-10f, 0x1p-10f);
-    return __builtin_fmaf(__builtin_fabsf(t), n, t);
+  // Values of one block, in units of its scale.
+  template <int N>
+  static __device__ __forceinline__ void nudge(float (&v)[N], BlockScale b) {
+    const bool small = b.s < 0x1p-96f;
+    if (__builtin_expect(__any(small), 0)) {
+      const float up = small ? 0x1p64f : 1.0f;
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] *= up;
+      b.s *= up;
+      b.r *= small ? 0x1p-64f : 1.0f;
+      b.c = b.r * 0x1p30f;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float q = v[k] * b.r;
+      const float t = bits_f((f_bits(q) + 0x40000u) & 0xfff80000u);
+      const float e = __builtin_fmaf(-t, b.s, v[k]);
+      const float n = __builtin_amdgcn_fmed3f(e * b.c, -0x1p-10f, 0x1p-10f);
+      v[k] = __builtin_fmaf(__builtin_fabsf(t), n, t);
+    }
   }
 };
 
@@ -239,8 +254,10 @@ struct Coder<uint16_t> {
     b.c += residual > 0.0f ? r * 0x1p-20f : residual < 0.0f ? r * -0x1p-20f : 0.0f;
     return b;
   }
-  static __device__ __forceinline__ float nudged(float x, const BlockScale& b) {
-    return __builtin_fmaf(x, b.c, x * b.r);
+  template <int N>
+  static __device__ __forceinline__ void nudge(float (&v)[N], const BlockScale& b) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __builtin_fmaf(v[k], b.c, v[k] * b.r);
   }
 };
 

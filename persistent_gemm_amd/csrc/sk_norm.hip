@@ -191,8 +191,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_forward(NormArg
 #pragma unroll
           for (int k = 0; k < 8; ++k) m = max(m, f_bits(v[c][k]) & kAbs);
           const BlockScale b = Coder<float>::scale(max16(m));     // 16 lanes hold a block of 128
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[c][k] = Coder<float>::nudged(v[c][k], b);
+          Coder<float>::nudge(v[c], b);
           // rows hold D rounded up to 16 codes: a piece of eight is inside or outside as a whole
           if (col < a.pitch)
             *(u32x2*)at_col(a.q + (int64_t)row * a.pitch, col) = u32x2{codes4(v[c][0], v[c][1], v[c][2], v[c][3], b.s),

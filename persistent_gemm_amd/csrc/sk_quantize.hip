@@ -156,7 +156,8 @@ __global__ __launch_bounds__(2048 / RPT) void sk_quantize_block(QuantArgs a) {
       }
       float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = Coder<T>::nudged(x[i][k], b);
+      for (int k = 0; k < 8; ++k) v[k] = x[i][k];
+      Coder<T>::nudge(v, b);
       w[i][0] = codes4(v[0], v[1], v[2], v[3], b.s);
       w[i][1] = codes4(v[4], v[5], v[6], v[7], b.s);
       // rows hold C rounded up to 16 codes, so a piece of eight is inside or outside as a whole
@@ -177,7 +178,8 @@ __global__ __launch_bounds__(2048 / RPT) void sk_quantize_block(QuantArgs a) {
         const BlockScale b{col_scale[0][8 * tc + k], col_scale[1][8 * tc + k], col_scale[2][8 * tc + k]};
         float v[RPT];
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) v[i] = Coder<T>::nudged(x[i][k], b);
+        for (int i = 0; i < RPT; ++i) v[i] = x[i][k];
+        Coder<T>::nudge(v, b);
 #pragma unroll
         for (int i = 0; i < RPT; i += 4) o[i / 4][k] = codes4(v[i], v[i + 1], v[i + 2], v[i + 3], b.s);
       }
