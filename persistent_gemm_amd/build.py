@@ -27,7 +27,8 @@ FLAGS = [
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source (in parallel) and link the shared libraries; returns the GEMM library's path."""
+    """Compile every source (in parallel) and link the shared libraries; returns the GEMM library's path.  Where the
+    native binding cannot be built, that is said on stderr and only the calls that use it are missing."""
     from concurrent.futures import ThreadPoolExecutor
     objs, cmds = [], []
     for src in SOURCES + PROBE_SOURCES:
@@ -38,17 +39,29 @@ def build(verbose: bool = False) -> str:
             cmd.insert(2, "hip")
         cmds.append(cmd)
         objs.append(obj)
-    cmds.append(_native_command(NATIVE + ".tmp"))
-    with ThreadPoolExecutor(max_workers=min(len(cmds), 5)) as ex:
+    if os.path.exists(NATIVE):
+        os.remove(NATIVE)     # (one of another version must not serve this one's library)
+    with ThreadPoolExecutor(max_workers=5) as ex:
+        native = ex.submit(_build_native, verbose)
         for f in [ex.submit(_run, c, verbose) for c in cmds]:
             f.result()
-    os.replace(NATIVE + ".tmp", NATIVE)
-    n = len(SOURCES)
-    for lib, lib_objs in ((LIB, objs[:n]), (PROBE_LIB, objs[n:])):
-        tmp = lib + ".tmp"
-        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *lib_objs, "-o", tmp], verbose)
-        os.replace(tmp, lib)
+        n = len(SOURCES)
+        for lib, lib_objs in ((LIB, objs[:n]), (PROBE_LIB, objs[n:])):
+            tmp = lib + ".tmp"
+            _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *lib_objs, "-o", tmp], verbose)
+            os.replace(tmp, lib)
+        try:
+            native.result()
+        except (ImportError, OSError, RuntimeError) as e:
+            print(f"the native binding was not built (the block-scaled and norm calls of the Python package need it): {e}",
+                  file=sys.stderr)
     return LIB
+
+
+def _build_native(verbose):
+    """The native binding, which needs torch and a host compiler; the libraries need neither."""
+    _run(_native_command(NATIVE + ".tmp"), verbose)
+    os.replace(NATIVE + ".tmp", NATIVE)
 
 
 def _native_command(out):
