@@ -293,6 +293,7 @@ struct NormGradArgs {
   int gate_rows;
   // set by the launcher
   int rows_per_chunk, chunks_per_gate, chunks, groups;
+  int workers;                // that run at once
 };
 int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus);
 hipError_t launch_norm_backward(const NormGradArgs& a, bool f32, hipStream_t s);
