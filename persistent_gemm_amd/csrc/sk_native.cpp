@@ -109,6 +109,13 @@ PyObject* guarded(F&& f) {
   }
 }
 
+// The interpreter lock given up for a call that uses the library's scratch: it may wait for another thread's call on the
+// stream, or for the stream itself when the scratch has to grow.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 int elem_of(const Tensor& t) {
   return t.scalar_type() == at::kBFloat16 ? SK_ELEM_BF16 : t.scalar_type() == at::kFloat ? SK_ELEM_F32 : -1;
 }
@@ -197,8 +204,11 @@ PyObject* gemm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (at.t) db = make({N, K}, at::kBFloat16, dev);
     if (want_bias) dbias = make({N}, at::kBFloat16, dev);
     auto p = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-    const sk_status r = lib.gemm_backward(d.ptr(), at.ptr(), (const float*)ats.ptr(), bt.ptr(), (const float*)bts.ptr(), p(da),
-                                          p(db), p(dbias), M, N, K, (int)cap, s);
+    const sk_status r = [&] {
+      const Unlocked u;
+      return lib.gemm_backward(d.ptr(), at.ptr(), (const float*)ats.ptr(), bt.ptr(), (const float*)bts.ptr(), p(da), p(db),
+                               p(dbias), M, N, K, (int)cap, s);
+    }();
     return r == SK_OK ? pack({da, db, dbias}) : PyLong_FromLong(r);
   });
 }
@@ -335,7 +345,10 @@ PyObject* norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
       dnw = make({D}, ty, dev);
       a.dnext_weight = dnw.data_ptr();
     }
-    const sk_status r = lib.norm_backward(&a);
+    const sk_status r = [&] {
+      const Unlocked u;
+      return lib.norm_backward(&a);
+    }();
     if (r != SK_OK) return PyLong_FromLong(r);
     return h.t ? pack({dx, dres, dw, dgate, drs, dnw}) : pack({dx, dnw});
   });

@@ -90,3 +90,26 @@ def test_backward_calls_of_several_threads():
         for k, (out, _) in enumerate(mine):
             want = alone[2 * i + k % 2]
             assert all(torch.equal(a, b) for a, b in zip(out, want)), (i, k)
+
+
+def test_backward_calls_give_the_interpreter_lock_up():
+    """The native binding hands the call to whatever entry point it was given: here to the interpreter's own question
+    whether this thread holds its lock, whose answer comes back as the call's status."""
+    held = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    x = torch.zeros(16, 64, dtype=torch.bfloat16, device="cuda")
+    w, r = x[0].clone(), torch.ones(16, device="cuda")
+    qt, st = pg.quantize_fp8_block(x, transpose=True)
+    bt, bst = pg.quantize_fp8_block(x, "tile", transpose=True)
+    native = pg._native()
+    dC = torch.zeros(16, 16, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    native.bind(held, held, held, held, held, torch._C._cuda_getCurrentRawStream)
+    try:
+        with pytest.raises(pg.SkError):      # (a call without scratch keeps it: the question is asked at all)
+            pg.rms_norm(x, w)
+        pg.gemm_fp8_block_backward(dC, qt, st, bt, bst)
+        pg.rms_norm_backward(x, x, w, r)
+    finally:
+        pg._NATIVE = None
+        pg._native()
+    assert torch.equal(pg.rms_norm(x, w)[0], x)
