@@ -471,31 +471,27 @@ __global__ __launch_bounds__(NT) void sk_column_sums(ColumnSums c) {
   column_sums_bf16<NT>(c, blockIdx.x, run);
 }
 
-// Few outputs: a workgroup takes 16 NB columns and 16 MB rows, and its NWK waves share out the blocks of K
-// in turn (wave w: blocks w, w + NWK, ...), so that together they read whole stretches of each row of B.  The
-// operands go straight to registers, U blocks at a time, with no barrier before the end, where the waves' sums
-// are added in LDS in wave order.  Bound by reading B once.
-template <int MB, int NB, int NWK, int U, bool BROW>
+// Few outputs: a workgroup takes 16 x 16 of them, and its NWK waves share out the blocks of K in turn (wave w:
+// blocks w, w + NWK, ...), so that together they read whole stretches of each row of B.  The operands go
+// straight to registers, U blocks at a time, with no barrier before the end, where the waves' sums are added in LDS in
+// wave order.  Bound by reading B once.
+template <int NWK, int U, bool BROW>
 __global__ __launch_bounds__(64 * NWK) void sk_gemm_block_rows(BlockGemm g) {
-  __shared__ __attribute__((aligned(16))) float red[NWK][MB * NB][64][4];
+  __shared__ __attribute__((aligned(16))) float red[NWK][64][4];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
   const int tn = blockIdx.x % g.tiles_n, tm = blockIdx.x / g.tiles_n;
-  const int m0 = tm * 16 * MB, n0 = tn * 16 * NB;
-  const int rows = min(16 * MB, g.M - m0), cols = min(16 * NB, g.N - n0);
+  const int m0 = tm * 16, n0 = tn * 16;
+  const int rows = min(16, g.M - m0), cols = min(16, g.N - n0);
   const uint32_t rb = (uint32_t)g.row_bytes;
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.A + (int64_t)m0 * rb, (uint32_t)rows * rb);
   const __amdgpu_buffer_rsrc_t rbr = make_rsrc(g.B + (int64_t)n0 * rb, (uint32_t)cols * rb);
-  v4f acc[MB][NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = v4f{};
+  v4f acc = v4f{};
 
   for (int k0 = wave; k0 < g.kb; k0 += NWK * U) {
-    v4u a[U][MB][2], b[U][NB][2];
-    float sa[U][MB];
-    v4f sb[U][NB];
+    v4u a[U][2], b[U][2];
+    float sa[U];
+    v4f sb[U];
     // all of B's first: they come from memory, A's from the caches
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -504,9 +500,7 @@ __global__ __launch_bounds__(64 * NWK) void sk_gemm_block_rows(BlockGemm g) {
         const int k = k0 + u * NWK;
         const uint32_t c = (uint32_t)(k * kBlock + 16 * lg + 64 * h);
         const bool in = k < g.kb && c < rb;
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-          b[u][j][h] = __builtin_amdgcn_raw_buffer_load_b128(rbr, in ? (uint32_t)(j * 16 + lr) * rb + c : kOob, 0, 0);
+        b[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rbr, in ? (uint32_t)lr * rb + c : kOob, 0, 0);
       }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -516,69 +510,49 @@ __global__ __launch_bounds__(64 * NWK) void sk_gemm_block_rows(BlockGemm g) {
       for (int h = 0; h < 2; ++h) {
         const uint32_t c = (uint32_t)(k * kBlock + 16 * lg + 64 * h);
         const bool in = k < g.kb && c < rb;
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-          a[u][i][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? (uint32_t)(i * 16 + lr) * rb + c : kOob, 0, 0);
+        a[u][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? (uint32_t)lr * rb + c : kOob, 0, 0);
       }
       const int ks = min(k, g.kb - 1);
+      const float s = g.SA[(int64_t)ks * g.M + min(m0 + lr, g.M - 1)];
+      sa[u] = k < g.kb ? s : 0.0f;
+      if constexpr (BROW) {
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const float s = g.SA[(int64_t)ks * g.M + min(m0 + i * 16 + lr, g.M - 1)];
-        sa[u][i] = k < g.kb ? s : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        if constexpr (BROW) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float s = g.SB[(int64_t)ks * g.N + min(n0 + j * 16 + 4 * lg + q, g.N - 1)];
-            sb[u][j][q] = k < g.kb ? s : 0.0f;
-          }
-        } else {
-          // (columns past N may start the next 128: their outputs are not stored)
-          const int n = min(n0 + j * 16, g.N - 1);
-          const float s = g.SB[(int64_t)(n / kBlock) * g.kb + ks];
-          sb[u][j][0] = k < g.kb ? s : 0.0f;
+        for (int q = 0; q < 4; ++q) {
+          const float sq = g.SB[(int64_t)ks * g.N + min(n0 + 4 * lg + q, g.N - 1)];
+          sb[u][q] = k < g.kb ? sq : 0.0f;
         }
+      } else {
+        const float sq = g.SB[(int64_t)(n0 / kBlock) * g.kb + ks];
+        sb[u][0] = k < g.kb ? sq : 0.0f;
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const v4f p = block_mfma(b[u], a[u]);
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          const v4f p = block_mfma(b[u][j], a[u][i]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            acc[i][j][q] = __builtin_fmaf(sa[u][i] * sb[u][j][BROW ? q : 0], p[q], acc[i][j][q]);
-        }
+      for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(sa[u] * sb[u][BROW ? q : 0], p[q], acc[q]);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) *(v4f*)red[wave][i * NB + j][lane] = acc[i][j];
+  *(v4f*)red[wave][lane] = acc;
   __syncthreads();
-  for (int run = threadIdx.x; run < 64 * MB * NB; run += 64 * NWK) {
-    const int blk = run >> 6, l = run & 63;
-    v4f x = *(const v4f*)red[0][blk][l];
+  if (wave) return;
+  v4f x = *(const v4f*)red[0][lane];
 #pragma unroll
-    for (int w = 1; w < NWK; ++w) x += *(const v4f*)red[w][blk][l];
-    const int row = m0 + (blk / NB) * 16 + (l & 15), col = n0 + (blk % NB) * 16 + 4 * (l >> 4);
-    if (row >= g.M || col >= g.N) continue;
-    float bias[4];
+  for (int w = 1; w < NWK; ++w) x += *(const v4f*)red[w][lane];
+  const int row = m0 + lr, col = n0 + 4 * lg;
+  if (row >= g.M || col >= g.N) return;
+  float bias[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) bias[k] = g.bias && col + k < g.N ? bits_f((uint32_t)g.bias[col + k] << 16) : 0.0f;
-    const v2u h = out4(x, bias);
-    uint16_t* const o = g.C + (int64_t)row * g.N + col;
-    if ((g.N & 3) == 0) {
-      *(v2u*)o = h;
-    } else {
-      const uint32_t v[4] = {h[0] & 0xffffu, h[0] >> 16, h[1] & 0xffffu, h[1] >> 16};
+  for (int k = 0; k < 4; ++k) bias[k] = g.bias && col + k < g.N ? bits_f((uint32_t)g.bias[col + k] << 16) : 0.0f;
+  const v2u h = out4(x, bias);
+  uint16_t* const o = g.C + (int64_t)row * g.N + col;
+  if ((g.N & 3) == 0) {
+    *(v2u*)o = h;
+  } else {
+    const uint32_t v[4] = {h[0] & 0xffffu, h[0] >> 16, h[1] & 0xffffu, h[1] >> 16};
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (col + k < g.N) o[k] = (uint16_t)v[k];
-    }
+    for (int k = 0; k < 4; ++k)
+      if (col + k < g.N) o[k] = (uint16_t)v[k];
   }
 }
 
@@ -601,11 +575,11 @@ hipError_t launch_tiled(BlockGemm g, bool b_tile, int grid_cap, int cus, hipStre
   return launch(b_tile ? sk_gemm_block<C, false> : sk_gemm_block<C, true>, dim3(grid), C::NT, s, g);
 }
 
-template <int MB, int NB, int NWK, int U>
+template <int NWK, int U>
 hipError_t launch_rows(BlockGemm g, bool b_tile, hipStream_t s) {
-  g.tiles_m = cdiv(g.M, 16 * MB);
-  g.tiles_n = cdiv(g.N, 16 * NB);
-  return launch(b_tile ? sk_gemm_block_rows<MB, NB, NWK, U, false> : sk_gemm_block_rows<MB, NB, NWK, U, true>,
+  g.tiles_m = cdiv(g.M, 16);
+  g.tiles_n = cdiv(g.N, 16);
+  return launch(b_tile ? sk_gemm_block_rows<NWK, U, false> : sk_gemm_block_rows<NWK, U, true>,
                 dim3((unsigned)(g.tiles_m * g.tiles_n)), 64 * NWK, s, g);
 }
 
@@ -661,7 +635,7 @@ hipError_t launch_gemm_block(const BlockGemm& g, bool b_tile, int grid_cap, int 
   // for every 16 columns instead of 32.  With a long K, 16 waves that ask for two blocks at a time:
   // 1x4096x4096 5.5 us against 6.5 with 8 and one, 256x256x2048 5.0 / 4.4.
   if (grid_cap <= 0 && tiles(16, 16) <= (g.kb <= 16 ? 2 : 1) * (int64_t)cus)
-    return g.kb < 32 ? launch_rows<1, 1, 8, 1>(g, b_tile, s) : launch_rows<1, 1, 16, 2>(g, b_tile, s);
+    return g.kb < 32 ? launch_rows<8, 1>(g, b_tile, s) : launch_rows<16, 2>(g, b_tile, s);
   return choose_tile(tiles, g.M, g.kb, cus, [&](auto cfg) { return launch_tiled<decltype(cfg)>(g, b_tile, grid_cap, cus, s); });
 }
 
