@@ -551,7 +551,8 @@ int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus) {
   const bool grouped = a->h && a->gate && a->gate_rows > 1;
   a->groups = grouped ? a->T / a->gate_rows : 1;
   const int group_rows = a->T / a->groups;
-  const int want = a->workers = 512 * cus / grad_threads(a->D);   // 512 threads to a compute unit
+  // 512 threads to a compute unit (a stream may be held to one, which has to take a row of 1024)
+  const int want = a->workers = max(1, 512 * cus / grad_threads(a->D));
   a->chunks_per_gate = a->groups >= want ? 1 : ceil_div(want, a->groups);
   a->rows_per_chunk = ceil_div(group_rows, a->chunks_per_gate);
   a->chunks_per_gate = ceil_div(group_rows, a->rows_per_chunk);

@@ -64,7 +64,10 @@ hipError_t hipMemcpy(void* d, const void*, size_t n, hipMemcpyKind) { return std
 hipError_t hipMemcpyAsync(void*, const void*, size_t, hipMemcpyKind, hipStream_t) { return hipSuccess; }
 hipError_t hipStreamSynchronize(hipStream_t) { return hipSuccess; }
 hipError_t hipStreamIsCapturing(hipStream_t, hipStreamCaptureStatus* s) { return *s = hipStreamCaptureStatusNone, hipSuccess; }
-hipError_t hipExtStreamGetCUMask(hipStream_t, uint32_t, uint32_t*) { return hipErrorInvalidValue; }
+hipError_t hipExtStreamGetCUMask(hipStream_t, uint32_t words, uint32_t* mask) {   // every stream but NULL: one unit
+  std::memset(mask, 0, 4 * words);
+  return mask[0] = 1, hipSuccess;
+}
 hipError_t hipGetLastError() { return hipSuccess; }
 // (the two halves of a <<<...>>> launch: the second is the first's own thread's)
 thread_local struct {
@@ -93,7 +96,7 @@ sk_status block_backward(int size, int cap) {
 sk_status bf16_backward(int size) {
   return sk_gemm_bf16_backward(at(0), at(1), at(2), at(3), at(4), at(5), 128 + 256 * size, 384, 512, 0, nullptr);
 }
-sk_status norm_backward(int size) {
+sk_status norm_backward(int size, int64_t D = 1024, void* stream = nullptr) {
   sk_norm_grad_args a;
   std::memset(&a, 0, sizeof(a));
   a.dout = at(0);
@@ -104,7 +107,8 @@ sk_status norm_backward(int size) {
   a.dresidual = at(5);
   a.dweight = at(6);
   a.T = 16 + 32 * size;
-  a.D = 1024;
+  a.D = D;
+  a.stream = stream;
   return sk_norm_backward(&a);
 }
 sk_status relaid_scales(int size) {
@@ -137,11 +141,13 @@ int main(int argc, char** argv) {
   const std::map<std::string, std::vector<Call>> scenes = {
       {"block_backward", {[](int s) { return block_backward(s, 0); }, [](int s) { return block_backward(s + 1, 0); }}},
       {"block_backward_capped", {[](int s) { return block_backward(s, 7); }, [](int s) { return block_backward(s + 1, 7); }}},
-      {"norm_backward", {norm_backward, [](int s) { return norm_backward(s + 1); }}},
+      {"norm_backward", {[](int s) { return norm_backward(s); }, [](int s) { return norm_backward(s + 1); }}},
       {"bf16_backward", {bf16_backward, [](int s) { return bf16_backward(s + 1); }}},
       {"block_and_bf16", {[](int s) { return block_backward(s, 0); }, bf16_backward}},
-      {"block_and_norm", {[](int s) { return block_backward(s, 0); }, norm_backward}},
+      {"block_and_norm", {[](int s) { return block_backward(s, 0); }, [](int s) { return norm_backward(s); }}},
       {"relaid_scales", {relaid_scales, [](int s) { return relaid_scales(s + 1); }}},
+      // rows of 64 to 1024 threads on a stream held to one compute unit
+      {"one_unit", {[](int s) { return norm_backward(s, 300 << s, at(9)); }, [](int s) { return norm_backward(s, 9000, at(9)); }}},
       {"release", {[](int s) { return block_backward(s, 0); }, [](int) { return release(); }}},
   };
   const auto scene = argc == 2 ? scenes.find(argv[1]) : scenes.end();
@@ -154,7 +160,7 @@ int main(int argc, char** argv) {
       while (ready < (int)scene->second.size()) std::this_thread::yield();
       for (int i = 0; i < 40; ++i) {
         this_call = calls++;
-        const sk_status st = call(i % 5 * 2);
+        const sk_status st = call(i % 4 * 2);
         if (st != SK_OK) bad = (int)st;
       }
     });

@@ -26,7 +26,7 @@ def program(tmp_path_factory):
 
 
 @pytest.mark.parametrize("calls", ["block_backward", "block_backward_capped", "norm_backward", "bf16_backward",
-                                   "block_and_bf16", "block_and_norm", "relaid_scales", "release"])
+                                   "block_and_bf16", "block_and_norm", "relaid_scales", "release", "one_unit"])
 def test_calls_on_one_stream_do_not_mix(program, calls):
     r = subprocess.run([program, calls], capture_output=True, text=True, timeout=100)
     assert r.returncode == 0, r.stdout + r.stderr
