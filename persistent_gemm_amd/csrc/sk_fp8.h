@@ -214,18 +214,19 @@ struct Coder<float> {
     b.c = b.r * 0x1p30f;
     return b;
   }
-  // Values of one block, in units of its scale.
+  static __device__ __forceinline__ bool small(const BlockScale& b) { return b.s < 0x1p-96f; }
+  // What to multiply a small block's values by; its scale is.
+  static __device__ __forceinline__ float lift(BlockScale& b) {
+    const bool low = small(b);
+    const float up = low ? 0x1p64f : 1.0f;
+    b.s *= up;
+    b.r *= low ? 0x1p-64f : 1.0f;
+    b.c = b.r * 0x1p30f;
+    return up;
+  }
+  // Values of one block, multiplied where it is small, in units of its scale.
   template <int N>
-  static __device__ __forceinline__ void nudge(float (&v)[N], BlockScale b) {
-    const bool small = b.s < 0x1p-96f;
-    if (__builtin_expect(__any(small), 0)) {
-      const float up = small ? 0x1p64f : 1.0f;
-#pragma unroll
-      for (int k = 0; k < N; ++k) v[k] *= up;
-      b.s *= up;
-      b.r *= small ? 0x1p-64f : 1.0f;
-      b.c = b.r * 0x1p30f;
-    }
+  static __device__ __forceinline__ void nudge_lifted(float (&v)[N], const BlockScale& b) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const float q = v[k] * b.r;
@@ -234,6 +235,15 @@ struct Coder<float> {
       const float n = __builtin_amdgcn_fmed3f(e * b.c, -0x1p-10f, 0x1p-10f);
       v[k] = __builtin_fmaf(__builtin_fabsf(t), n, t);
     }
+  }
+  template <int N>
+  static __device__ __forceinline__ void nudge(float (&v)[N], BlockScale b) {
+    if (__builtin_expect(__any(small(b)), 0)) {
+      const float up = lift(b);
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] *= up;
+    }
+    nudge_lifted(v, b);
   }
 };
 

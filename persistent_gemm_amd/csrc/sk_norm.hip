@@ -89,8 +89,10 @@ __device__ __forceinline__ void repack(RawRow<T, CH>& r) {
 // row ahead and kept as they lie in memory, and the vectors shared by the rows stay in registers where they
 // fit (HOLD), so that the two sums of a row, which wait for all its threads, do not wait for memory.
 // The scales of eight rows leave together: one row's are T apart, 4 bytes in a line each.
+// Four waves to a SIMD, at most 128 registers, since the launch is for 1024 threads to a compute unit (with 129, fp32 rows of
+// 512 threads ran alone on theirs: gated to fp8, 2048x8000, 62.3 -> 68.7 us).
 template <class T, bool POST, bool PRE, bool FP8, int TPR, int CH, bool SHORT>
-__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void sk_norm_forward(NormArgs a) {
+__global__ __launch_bounds__(TPR == 64 ? 256 : TPR, 4) void sk_norm_forward(NormArgs a) {
   constexpr int RPW = rows_per_wg<TPR>();
   constexpr bool HOLD = CH * sizeof(T) <= 4, AHEAD = CH < 4;   // (a wide row's registers hold little else)
   constexpr bool BATCH = FP8 && TPR > 64;

@@ -57,7 +57,9 @@ __global__ __launch_bounds__(2048 / RPT) void sk_quantize_block(QuantArgs a) {
   constexpr bool COLS = TRANS && !TILE;
   __shared__ __attribute__((aligned(16))) uint8_t codes_t[TRANS ? 128 * kPitch : 16];
   __shared__ __attribute__((aligned(16))) uint32_t tops[COLS ? TR : 1][128];
-  __shared__ __attribute__((aligned(16))) float col_scale[COLS ? 3 : 1][128];
+  constexpr bool LIFT = COLS && sizeof(T) == 4;   // columns of small scales are multiplied (see Coder<float>)
+  __shared__ __attribute__((aligned(16))) float col_scale[LIFT ? 4 : COLS ? 3 : 1][128];
+  __shared__ bool any_small;
   __shared__ __attribute__((aligned(16))) float col_sum[SUMS ? TR : 1][128];
   const int rb = blockIdx.x / a.kb, cb = blockIdx.x - rb * a.kb;
   const int t = threadIdx.x, tr = t >> 4, tc = t & 15;
@@ -86,6 +88,7 @@ __global__ __launch_bounds__(2048 / RPT) void sk_quantize_block(QuantArgs a) {
     }
   }
   if constexpr (COLS) {
+    if (LIFT && t == 0) any_small = false;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t m = 0;
@@ -122,11 +125,15 @@ __global__ __launch_bounds__(2048 / RPT) void sk_quantize_block(QuantArgs a) {
         uint32_t m = tops[0][t];
 #pragma unroll
         for (int i = 1; i < TR; ++i) m = max(m, tops[i][t]);
-        const BlockScale b = Coder<T>::scale(m);
+        BlockScale b = Coder<T>::scale(m);
+        if (c < C) a.scale_t[(int64_t)rb * C + c] = b.s;
+        if constexpr (LIFT) {
+          if (Coder<T>::small(b)) any_small = true;
+          col_scale[3][t] = Coder<T>::lift(b);
+        }
         col_scale[0][t] = b.s;
         col_scale[1][t] = b.r;
         col_scale[2][t] = b.c;
-        if (c < C) a.scale_t[(int64_t)rb * C + c] = b.s;
       }
       if constexpr (SUMS) {
         float s = col_sum[0][t];
@@ -173,13 +180,22 @@ __global__ __launch_bounds__(2048 / RPT) void sk_quantize_block(QuantArgs a) {
 #pragma unroll
       for (int v = 0; v < RPT / 4; ++v) transpose4(w + 4 * v, o[v]);
     } else {
+      if constexpr (LIFT) {
+        if (__builtin_expect(any_small, 0)) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) x[i][k] *= col_scale[3][8 * tc + k];
+        }
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const BlockScale b{col_scale[0][8 * tc + k], col_scale[1][8 * tc + k], col_scale[2][8 * tc + k]};
         float v[RPT];
 #pragma unroll
         for (int i = 0; i < RPT; ++i) v[i] = x[i][k];
-        Coder<T>::nudge(v, b);
+        if constexpr (LIFT) Coder<T>::nudge_lifted(v, b);
+        else Coder<T>::nudge(v, b);
 #pragma unroll
         for (int i = 0; i < RPT; i += 4) o[i / 4][k] = codes4(v[i], v[i + 1], v[i + 2], v[i + 3], b.s);
       }

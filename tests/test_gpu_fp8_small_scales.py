@@ -52,6 +52,20 @@ def test_rows_and_columns():
     _equal(qt[:, :128], q, "codes of the transpose")
 
 
+def test_many_tiles():
+    """The same, often enough that a thread takes more rows."""
+    x = _next_to_borders()
+    q, s = ref.quantize(x, "row")
+    n = 45
+    got = pg.quantize_fp8_block(x.repeat(1, n).cuda())
+    _equal(got[1], s.repeat(n, 1), "scales")
+    _equal(got[0], q.repeat(1, n), "codes")
+    for transpose in (True, "both"):
+        qt, st = pg.quantize_fp8_block(x.t().repeat(n, 1).cuda(), transpose=transpose)[-2:]
+        _equal(st, s.repeat(n, 1), "scales of the transpose")
+        _equal(qt, q.repeat(1, n), "codes of the transpose")
+
+
 def test_tiles():
     x = _next_to_borders()
     for first in list(range(4, 60, 4)) + list(range(84, 400, 40)):      # a row and 127 quiet ones
