@@ -121,3 +121,28 @@ def test_norms_past_32_bits():
     assert (dx[:-5] == 0).all()
     # (the zero rows add nothing, exactly)
     _close(dw, want["dnext_weight"], bound["dnext_weight"] * 265 * U + want["dnext_weight"].abs() * 2.0 ** -8, "dweight")
+
+
+# a size for each kernel: few outputs (short and long K), tiles of 32x32, 64x32, 64x64 (one and two groups), 128x64, 128x128 (four and
+# two stages), 256x128, 256x256 (one and several to a unit)
+@pytest.mark.parametrize("M,N,K", [(5, 64, 2000), (16, 256, 8192), (16, 8192, 2064), (40, 8200, 640), (500, 700, 400),
+                                   (300, 3000, 2064), (1037, 1290, 528), (777, 4099, 300), (1540, 3000, 528),
+                                   (3584, 2048, 2064), (2310, 2897, 1000), (4401, 4603, 1664)])
+@pytest.mark.parametrize("block", ["tile", "row"])
+def test_nan_stays_in_its_rows(M, N, K, block):
+    """NaN as a scale of the last block (which ends early, or is followed by blocks that are not there) and as a code."""
+    A, B, SA, SB, _ = _operands(M, N, K, block, 5)
+    r, c, z = M // 2, N // 3, M - 1
+    SA[-1, r] = float("nan")
+    A.view(torch.uint8)[z, 1] = 0x7F
+    bad = torch.zeros(M, N, dtype=torch.bool)
+    bad[r] = True
+    bad[z] = True
+    if block == "tile":
+        SB[c // 128, -1] = float("nan")
+        bad[:, c // 128 * 128:(c // 128 + 1) * 128] = True
+    else:
+        SB[-1, c] = float("nan")
+        bad[:, c] = True
+    got = pg.gemm_fp8_block(A.cuda(), B.cuda(), SA.cuda(), SB.cuda()).cpu()
+    assert torch.equal(got.isnan(), bad)
