@@ -264,7 +264,7 @@ typedef enum sk_block { SK_BLOCK_ROW = 0, SK_BLOCK_TILE = 1 } sk_block;
  *     s = max(fl(max|x| / 448), 2^-126) over each block,   code = E4M3 nearest to x / s
  * (the exact quotient, ties to even; a block that holds an infinity or a NaN has a NaN scale
  * and NaN codes).  Blocks start at multiples of 128 and end at the matrix's edge.
- *   q        uint8 [R][Cp], Cp = C rounded up to 16 (codes past C are 0)
+ *   q        uint8 [R][Cp], Cp = C rounded up to 16 (codes past C are 0, or NaN in a NaN block)
  *   scale    float [ceil(C/128)][R] (SK_BLOCK_ROW) or [ceil(R/128)][ceil(C/128)] (SK_BLOCK_TILE)
  *   qt       uint8 [C][Rp]: the codes of x^T, likewise, with blocks along R
  *   scale_t  float [ceil(R/128)][C] or [ceil(C/128)][ceil(R/128)]

@@ -510,7 +510,8 @@ def quantize_fp8_block(x, block="row", *, transpose=False, stream=None):
     block "row": 128 consecutive elements of a row share a scale; returns (q, scale) with q
     float8_e4m3fn [R, C rounded up to 16] (zeros past C) and scale [ceil(C/128), R].  block "tile":
     128 x 128 elements do; scale [ceil(R/128), ceil(C/128)].  transpose=True gives the same of x^T (blocks
-    along R) instead, transpose="both" gives (q, scale, qt, scale_t) from one pass over x."""
+    along R) instead, transpose="both" gives (q, scale, qt, scale_t) from one pass over x.  A block that holds
+    a NaN or an infinity has a NaN scale and NaN codes, those past C included."""
     if block in _BLOCKS and transpose in (False, True, "both"):
         got = (_NATIVE or _native()).quantize(x, _BLOCKS[block], 3 if transpose == "both" else 2 if transpose else 1,
                                               None if stream is None else _handle(stream))

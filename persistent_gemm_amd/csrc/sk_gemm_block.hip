@@ -183,6 +183,8 @@ __device__ __forceinline__ void block_tiles(const BlockGemm& g, lds_u8* const sm
                 (uint32_t)(uintptr_t)smem + C::BIAS_OFF + (uint32_t)turn * C::BIAS + (uint32_t)(wave % BI) * 256u);
   };
   // Load l of block k of that tile into a stage; where there is none every lane is out of range (zeros, no traffic).
+  // (The range check is on the lane's offset plus the scalar one, measured also where the scalar one alone is past the end: row
+  // groups beyond a ragged tile's rows read zeros.)
   auto issue_one = [&](int k, int slot, bool live, auto lc) {
     constexpr int l = decltype(lc)::value;
     const uint32_t stage = ring + (uint32_t)slot * C::STAGE;
