@@ -74,6 +74,12 @@ __device__ __forceinline__ void settle_row(RawRow<T, CH>& r, int t, int D) {
   for (int c = 0; c < CH; ++c) settle8<SHORT>(r.c[c], 8 * (t + c * TPR), D);
 }
 
+// a + b of products that are rounded before: the formula's operations one by one, as a caller would write them.
+__device__ __forceinline__ float sum(float a, float b) {
+#pragma clang fp contract(off)
+  return a + b;
+}
+
 // Has the row unpacked again where it is next used, instead of kept as floats from before: twice the registers.
 template <class T, int CH>
 __device__ __forceinline__ void repack(RawRow<T, CH>& r) {
@@ -156,10 +162,10 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR, 4) void sk_norm_forward(Norm
         const int col = 8 * (t + c * TPR), n = min(8, max(0, D - col));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          float y = raw_at(h0.c[c], k) * (r * raw_at(w.c[c], k));
+          float y = raw_at(h0.c[c], k) * r * raw_at(w.c[c], k), x = raw_at(x0.c[c], k);
           if (a.gate) y *= raw_at(g.c[c], k);
-          const float x = raw_at(x0.c[c], k);
-          v[c][k] = a.residual_scale ? __builtin_fmaf(x, raw_at(rs.c[c], k), y) : x + y;
+          if (a.residual_scale) x *= raw_at(rs.c[c], k);
+          v[c][k] = sum(x, y);
         }
         store8(at_col((T*)a.out + at, col), n, v[c]);
         // the next norm reads what is stored
