@@ -151,12 +151,20 @@ __device__ __forceinline__ uint32_t max16(uint32_t x) {
   return max(x, row_rotate<1>(x));
 }
 
+template <int N>
+__device__ __forceinline__ float row_rotated(float x) { return bits_f(row_rotate<N>(f_bits(x))); }
+template <int N>
+__device__ __forceinline__ double row_rotated(double x) {
+  return __hiloint2double((int)row_rotate<N>((uint32_t)__double2hiint(x)), (int)row_rotate<N>((uint32_t)__double2loint(x)));
+}
+
 // The sum over a wave, in every lane: rotations within 16 lanes, then across them.  The order is fixed.
-__device__ __forceinline__ float wave_sum(float x) {
-  x += bits_f(row_rotate<8>(f_bits(x)));
-  x += bits_f(row_rotate<4>(f_bits(x)));
-  x += bits_f(row_rotate<2>(f_bits(x)));
-  x += bits_f(row_rotate<1>(f_bits(x)));
+template <class T>
+__device__ __forceinline__ T wave_sum(T x) {
+  x += row_rotated<8>(x);
+  x += row_rotated<4>(x);
+  x += row_rotated<2>(x);
+  x += row_rotated<1>(x);
   x += __shfl_xor(x, 16);
   return x + __shfl_xor(x, 32);
 }

@@ -7,7 +7,7 @@
 //
 // and their gradients.  A row is held in registers by TPR threads (a wave, with four rows to a workgroup, or
 // a workgroup), CH pieces of eight elements each, so every tensor is read once and written once: all of it
-// is bound by HBM (by latency for few rows).  Statistics and sums are fp32.  Rows need no alignment beyond
+// is bound by HBM (by latency for few rows).  Sums are fp32, a row's of squares across threads 64 bits.  Rows need no alignment beyond
 // their elements' (a row of odd length starts anywhere).  Gated, with the next norm in fp8, 16384x4096 bf16: 103 us,
 // 4.6 TB/s (a copy of 2 GiB: 4.9).  Backward of both, 4095x2047 fp32: 62 us, 3.8 TB/s, 6 us of it the column sums.
 
@@ -23,19 +23,30 @@ namespace {
 
 constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// The sum over the TPR threads of a row, in each of them.  `red`: two areas of 16 floats, used in turn, so that
+// The sum over the TPR threads of a row, in each of them.  `red`: two areas of 16 sums, used in turn, so that
 // one barrier a sum is enough (whoever writes an area again has passed the barrier after its last reading).
-template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float (*red)[16], int& turn) {
+template <int TPR, class T>
+__device__ __forceinline__ T row_sum(T x, T (*red)[16], int& turn) {
   x = wave_sum(x);
   if constexpr (TPR > 64) {
-    float* const r = red[turn];
+    T* const r = red[turn];
     turn ^= 1;
     if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = x;
     __syncthreads();
-    x = r[0];
+    if constexpr (sizeof(T) == 8 || TPR == 1024) {
+      // a lane for each wave's sum, the same again in every TPR / 64 lanes.  All of them in each lane take more registers:
+      // doubles then spill 7 with 512 threads (gated to fp8, 2048x8000 fp32, 62.7 -> 66.8 us), floats with 1024 threads
+      // more than they do (backward 2048x12000 fp32 820 -> 990 us, in bf16 685 -> 650; 2048x20000 fp32 2860 -> 3210).
+      x = r[threadIdx.x & (TPR / 64 - 1)];
+      if constexpr (TPR >= 1024) x += row_rotated<8>(x);
+      if constexpr (TPR >= 512) x += row_rotated<4>(x);
+      x += row_rotated<2>(x);
+      x += row_rotated<1>(x);
+    } else {
+      x = r[0];
 #pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) x += r[w];
+      for (int w = 1; w < TPR / 64; ++w) x += r[w];
+    }
   }
   return x;
 }
@@ -104,11 +115,17 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR, 4) void sk_norm_forward(Norm
   constexpr bool BATCH = FP8 && TPR > 64;
   constexpr int ROWS = 8;                       // rows whose scales leave together
   constexpr int BLOCKS = BATCH ? TPR * CH / 16 : 1;
-  __shared__ float red[2][16];
+  __shared__ double red[2][16];
   __shared__ float scales[BLOCKS][ROWS + 1];
   int turn = 0;
   const int t = threadIdx.x % TPR, D = a.D;
-  const float inv = 1.0f / (float)D;
+  // (the same in every lane, said so: two registers of the few that wide rows leave)
+  const double quotient = 1.0 / (double)D;
+  const double inv = __hiloint2double(__builtin_amdgcn_readfirstlane(__double2hiint(quotient)),
+                                      __builtin_amdgcn_readfirstlane(__double2loint(quotient)));
+  // A thread's squares, 32 at most, are summed in fp32 and the threads' sums in 64 bits: roundings do not add up with the
+  // width, and a row overflows where 32 of its squares do, not where all of them would.
+  auto rstd_of = [&](float squares) { return rsqrtf((float)(row_sum<TPR>((double)squares, red, turn) * inv + (double)a.eps)); };
   const int first = (int)((int64_t)a.T * blockIdx.x / gridDim.x), last = (int)((int64_t)a.T * (blockIdx.x + 1) / gridDim.x);
   typedef RawRow<T, CH> Row;
   auto load = [&](const void* p, int row) { return load_row<SHORT, T, TPR, CH>(p, row, t, D); };
@@ -153,7 +170,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR, 4) void sk_norm_forward(Norm
           const float h = raw_at(h0.c[c], k);
           ss = __builtin_fmaf(h, h, ss);
         }
-      const float r = 1.0f / __builtin_sqrtf(row_sum<TPR>(ss, red, turn) * inv + a.eps);
+      const float r = rstd_of(ss);
       if (t == 0) a.rstd[row] = r;
       settle(x0);
       settle(g);
@@ -187,7 +204,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR, 4) void sk_norm_forward(Norm
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(v[c][k], v[c][k], ss);
-      const float r = 1.0f / __builtin_sqrtf(row_sum<TPR>(ss, red, turn) * inv + a.eps);
+      const float r = rstd_of(ss);
       if (t == 0) a.rstd_next[row] = r;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
