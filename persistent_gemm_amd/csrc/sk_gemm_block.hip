@@ -13,7 +13,7 @@
 // memory into LDS (16-byte and 4-byte direct loads), in a ring of STAGES; the 16-byte chunks of row r are
 // permuted by (r >> 1) & 7 so that 16 lanes reading a chunk of 16 rows meet all banks.  The accumulators are
 // ordinary registers (the ALU cannot reach AGPRs), which bounds a wave's tile to 64 x 128.
-// 8192^3: 422-451 us on different devices (2.4-2.6 PFLOP/s), 340 us on operands of zeros: held by power.  4096^3 60 us,
+// 8192^3: 422-460 us on different devices (2.4-2.6 PFLOP/s), 340 us on operands of zeros: held by power.  4096^3 60 us,
 // 70 us with a scale per row of B: the second product per output and block fills the ALU.
 // Few outputs: see sk_gemm_block_rows.
 
