@@ -272,7 +272,7 @@ def _own_combine(s):
     import persistent_gemm_amd as pg
     if not s["case"]["backward"]:
         return pg.moe_combine(s["y"], s["slots"], s["weights"])
-    dy, dweights = pg.moe_combine_backward(s["dout"], s["y"], s["slots"], s["weights"])
+    dy, dweights = pg.moe_combine_backward(s["dout"], s["y"], s["slots"], s["weights"], offsets=s["offsets"])
     return {"dy": dy} | ({"dweights": dweights} if s["case"]["weighted"] else {})
 
 
