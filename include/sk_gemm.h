@@ -256,7 +256,7 @@ sk_status sk_gemm_bf16_backward(const void* dC, const void* A, const void* B, vo
  * refuse a capturing stream (SK_ERR_UNSUPPORTED) like the Stream-K calls. */
 
 /* Element types of the quantiser's input and of the norms. */
-typedef enum sk_elem { SK_ELEM_BF16 = 0, SK_ELEM_F32 = 1 } sk_elem;
+typedef enum sk_elem { SK_ELEM_BF16 = 0, SK_ELEM_F32 = 1, SK_ELEM_F16 = 2 /* the layer of experts only */ } sk_elem;
 /* What shares a scale: 128 consecutive elements of a row, or 128 rows of them. */
 typedef enum sk_block { SK_BLOCK_ROW = 0, SK_BLOCK_TILE = 1 } sk_block;
 
@@ -361,6 +361,91 @@ typedef struct sk_norm_grad_args {
 } sk_norm_grad_args;
 
 sk_status sk_norm_backward(const sk_norm_grad_args* args);
+
+/* ---- A layer of experts: routing, products grouped by expert, and products with 4-bit weights.
+ *
+ * None of these calls uses scratch of the library, so all of them may be captured into a HIP graph, and calls of
+ * several host threads or streams do not meet.  Offsets, slots and row indexes are device data that the host does not
+ * see: kernels hold each to its range, so that wrong ones give wrong rows and no access out of bounds. */
+
+/* The k largest of each token's E logits (elem: bf16, fp16 or fp32; [T][E]), and the order of the pairs (token, choice)
+ * by expert:
+ *   experts  int32 [T][k]   in falling order of the logits, ties to the lower expert.  An expert whose logit is -inf or
+ *                           NaN is never chosen; where none is left: -1
+ *   weights  float [T][k]   softmax over the chosen logits (normalize != 0) or over all E (sums in fp32); 0 where there is no
+ *                           expert; NaN for a token that has a NaN logit (or +inf, as the formula gives)
+ *   offsets  int32 [E+1]    pairs of expert e are the rows offsets[e] .. offsets[e+1]-1, in the order of the pairs
+ *   slots    int32 [T][k]   the row of each pair, -1 without an expert
+ *   rows     int32 [T*k]    the token of each row, -1 behind the last expert's
+ * work: sk_moe_route_work_bytes(T, E) bytes of the caller's device memory, 4-byte aligned, for this call alone.
+ * SK_ERR_ARG: a NULL pointer, T, E or k < 1, E > 1024, k > 32 or k > E, T * k >= 2^31 - 2^20, an output that overlaps the
+ * logits or another output. */
+int64_t sk_moe_route_work_bytes(int64_t T, int64_t E);
+sk_status sk_moe_route(const void* logits, sk_elem elem, int normalize, int32_t* experts, float* weights,
+                       int32_t* offsets, int32_t* slots, int32_t* rows, void* work, int64_t T, int64_t E, int64_t k,
+                       void* stream);
+
+/* The gradient of the logits, given dweights float [T][k] and the choice: normalised, w_j (d_j - sum_i w_i d_i) at
+ * the chosen experts and 0 elsewhere (logits may then be NULL); else p_e (d_e - sum_i w_i d_i) at every expert, p the
+ * softmax of the logits and d_e 0 where e is not chosen. */
+sk_status sk_moe_route_backward(const float* dweights, const void* logits, sk_elem elem, int normalize,
+                                const int32_t* experts, const float* weights, void* dlogits, int64_t T, int64_t E,
+                                int64_t k, void* stream);
+
+/* out[t] = sum_j weights[t][j] y[slots[t][j]]: y [R][D], slots int32 [T][k] (outside of [0, R): no row), weights float
+ * [T][k] or NULL for 1, out [T][D]; bf16, fp16 or fp32, summed in fp32 in the order of j. */
+sk_status sk_moe_combine(const void* y, sk_elem elem, const int32_t* slots, const float* weights, void* out, int64_t T,
+                         int64_t k, int64_t R, int64_t D, void* stream);
+
+/* Its gradients: dy[slots[t][j]] = weights[t][j] dout[t] [R][D], and dweights[t][j] = <dout[t], y[slots[t][j]]> (float
+ * [T][k], or NULL; y is needed with it).  No two pairs may share a slot (sk_moe_route's do not).  Rows of dy without a
+ * pair are zeros: with offsets (int32 [E+1]) they have to be those behind offsets[E]; with NULL any. */
+sk_status sk_moe_combine_backward(const void* dout, const void* y, sk_elem elem, const int32_t* slots,
+                                  const float* weights, const int32_t* offsets, void* dy, float* dweights, int64_t T,
+                                  int64_t k, int64_t R, int64_t D, int64_t E, void* stream);
+
+/* C[r][n] = sum_k A[rows[r]][k] B[e][n][k] + bias[e][n] for the rows r = offsets[e] .. offsets[e+1]-1 of each expert e;
+ * elem bf16 or fp16, fp32 sums, one rounding.
+ *   A [T][K]; rows int32 [R], or NULL (A's row r, T = R);  B [E][N][K];  offsets int32 [E+1], ascending from 0 to at most R;
+ *   bias [E][N] or NULL;  C [R][N].  Rows of C behind offsets[E] become zeros where tail_zero != 0 and keep their values else.
+ * K is a multiple of 8 (rows of whole 16 bytes), A and B are 16-byte aligned (SK_ERR_ALIGN); N is any.  SK_ERR_ARG: a NULL
+ * pointer, a size < 1, E > 1024, R >= 2^31 - 2^20, N > 2^22, K > 2^21, with rows an A of 2 GiB or more, C over an input. */
+sk_status sk_gemm_grouped(const void* A, const void* B, sk_elem elem, const int32_t* offsets, const int32_t* rows,
+                          const void* bias, void* C, int64_t R, int64_t T, int64_t E, int64_t N, int64_t K,
+                          int tail_zero, void* stream);
+
+/* Its gradients, each output may be NULL (at least one is required):
+ *   dA [R][K]:     dA[r] = sum_n dC[r][n] B[e][n]    (by row; with `rows`, sk_moe_combine without weights adds a token's up);
+ *                  rows behind offsets[E] become zeros
+ *   dB [E][N][K]:  sum over the expert's rows of dC[r][n] A[rows[r]][k]  (zeros for an expert without rows)
+ *   dbias [E][N]:  sum of its rows of dC
+ * B is needed for dA, A for dB and for dbias.  N too is a multiple of 8, dC is 16-byte aligned. */
+sk_status sk_gemm_grouped_backward(const void* dC, const void* A, const void* B, sk_elem elem, const int32_t* offsets,
+                                   const int32_t* rows, void* dA, void* dB, void* dbias, int64_t R, int64_t T, int64_t E,
+                                   int64_t N, int64_t K, void* stream);
+
+/* 4-bit codes of a weight w (bf16, fp16 or fp32), E matrices [N][K] one behind the other, with a 16-bit scale for each
+ * `group` (32, 64 or 128; K is a multiple of it) of elements along a row; w = scale (code - zero):
+ *   q      uint8 [E][N][K/2], the even element in the low half of a byte
+ *   scale  [E][K/group][N], scale_elem bf16 or fp16, at least its type's smallest normal number
+ *   zero   uint8 [E][K/group][N], or NULL: 8 everywhere
+ *     without zero points  scale = max|w| / 7,  code = 8 + w / scale
+ *     with them            scale = (max(w, 0) - min(w, 0)) / 15,  zero = -min(w, 0) / scale,  code = zero + w / scale
+ * quotients to nearest, ties to even, codes and zero points held to 0 .. 15.  A group that holds an infinity or a NaN, or
+ * whose scale is beyond its type, has a NaN scale, and codes and a zero point of 0.  q is 16-byte aligned, the others to their elements. */
+sk_status sk_quantize_w4(const void* w, sk_elem elem, void* q, void* scale, sk_elem scale_elem, uint8_t* zero, int64_t E,
+                         int64_t N, int64_t K, int64_t group, void* stream);
+/* out [E][N][K] of the scale's type = scale (code - zero). */
+sk_status sk_dequantize_w4(const void* q, const void* scale, sk_elem scale_elem, const uint8_t* zero, void* out,
+                           int64_t E, int64_t N, int64_t K, int64_t group, void* stream);
+
+/* C[m][n] = sum_k x[m][k] scale[k/group][n] (code[n][k] - zero[k/group][n]) + bias[n] for few rows (tokens being decoded;
+ * beyond 64 the weight is read again for every 64): x [M][K], C [M][N] and scales bf16 or fp16, q and zero as above, fp32
+ * sums, one rounding.  With offsets (and rows) as in sk_gemm_grouped, M rows in E groups, each with a weight (and a bias) of its
+ * own; without, E is 1 and T is M.  A row of x with an infinity or a NaN gives NaN.  x and q are 16-byte aligned. */
+sk_status sk_gemm_w4(const void* x, const void* q, const void* scale, const uint8_t* zero, sk_elem elem,
+                     const int32_t* offsets, const int32_t* rows, const void* bias, void* C, int64_t M, int64_t T,
+                     int64_t E, int64_t N, int64_t K, int64_t group, int tail_zero, void* stream);
 
 /* Full-control entry point: the same kernels with a chosen policy and tile, plus test hooks.
  * Zero-initialise and fill the fields you need.  The policies are the Stream-K

@@ -11,7 +11,9 @@ Entry points mirror ``include/sk_gemm.h``:
 ``gemm_mxfp4``, ``gemm_mxfp8``, ``gemm_bf16``, ``gemm_fp8``, ``addmm`` and ``gemm_ex`` (policy,
 tile and test hooks); ``quantize_fp8_block``, ``gemm_fp8_block`` and ``gemm_fp8_block_backward``
 (E4M3 with an fp32 scale for each block of 128); ``rms_norm`` and ``gated_norm`` with
-``rms_norm_backward`` and ``gated_norm_backward`` (the norms before and after a block); plus ``plan``, ``plan_wg_range``, ``check``,
+``rms_norm_backward`` and ``gated_norm_backward`` (the norms before and after a block); ``moe_route``,
+``moe_combine``, ``gemm_grouped`` (each with its backward), ``gemm_w4``, ``quantize_w4`` and ``dequantize_w4`` (a
+layer of experts, ``experts.py``); plus ``plan``, ``plan_wg_range``, ``check``,
 ``release_workspace``, ``poison_workspace``, ``variants`` and the CU-masked
 streams ``cu_masked_stream`` / ``destroy_stream`` / ``stream_cu_count``.
 """
@@ -30,6 +32,8 @@ __all__ = [
     "cu_masked_stream", "destroy_stream", "stream_cu_count", "phase_summary",
     "quantize_fp8_block", "gemm_fp8_block", "gemm_fp8_block_backward",
     "rms_norm", "gated_norm", "rms_norm_backward", "gated_norm_backward",
+    "moe_route", "moe_route_backward", "moe_combine", "moe_combine_backward",
+    "gemm_grouped", "gemm_grouped_backward", "gemm_w4", "quantize_w4", "dequantize_w4",
 ]
 
 MXFP4, BF16, FP8, MXFP8 = 0, 1, 2, 3
@@ -165,6 +169,16 @@ def load():
     lib.sk_gemm_fp8_block_backward.argtypes = [vp] * 8 + [i64, i64, i64, i32, vp]
     lib.sk_norm_forward.argtypes = [vp]      # a structure by reference, or its bytes
     lib.sk_norm_backward.argtypes = [vp]
+    lib.sk_moe_route_work_bytes.argtypes = [i64, i64]
+    lib.sk_moe_route.argtypes = [vp, i32, i32] + [vp] * 6 + [i64] * 3 + [vp]
+    lib.sk_moe_route_backward.argtypes = [vp, vp, i32, i32, vp, vp, vp] + [i64] * 3 + [vp]
+    lib.sk_moe_combine.argtypes = [vp, i32, vp, vp, vp] + [i64] * 4 + [vp]
+    lib.sk_moe_combine_backward.argtypes = [vp, vp, i32] + [vp] * 5 + [i64] * 5 + [vp]
+    lib.sk_gemm_grouped.argtypes = [vp, vp, i32] + [vp] * 4 + [i64] * 5 + [i32, vp]
+    lib.sk_gemm_grouped_backward.argtypes = [vp, vp, vp, i32] + [vp] * 5 + [i64] * 5 + [vp]
+    lib.sk_quantize_w4.argtypes = [vp, i32, vp, vp, i32, vp] + [i64] * 4 + [vp]
+    lib.sk_dequantize_w4.argtypes = [vp, vp, i32, vp, vp] + [i64] * 4 + [vp]
+    lib.sk_gemm_w4.argtypes = [vp, vp, vp, vp, i32] + [vp] * 4 + [i64] * 6 + [i32, vp]
     lib.sk_gemm_ex.argtypes = [ctypes.POINTER(_Args)]
     lib.sk_plan.argtypes = [ctypes.POINTER(_PlanQuery), ctypes.POINTER(_PlanInfo)]
     lib.sk_plan_wg_range.argtypes = [ctypes.POINTER(_PlanInfo), ctypes.c_int32,
@@ -186,10 +200,12 @@ def load():
     lib.sk_status_string.restype = ctypes.c_char_p
     for name in ("sk_gemm_mxfp4", "sk_gemm_mxfp4_noalloc", "sk_gemm_mxfp8", "sk_gemm_bf16", "sk_gemm_bf16_backward", "sk_gemm_mx", "sk_gemm_fp8", "sk_addmm", "sk_gemm_ex", "sk_plan",
                  "sk_quantize_fp8_block", "sk_gemm_fp8_block", "sk_gemm_fp8_block_backward", "sk_norm_forward", "sk_norm_backward",
-                 "sk_plan_wg_range", "sk_plan_wg_work", "sk_check", "sk_debug_poison_workspace", "sk_variant_info",
+                 "sk_moe_route", "sk_moe_route_backward", "sk_moe_combine", "sk_moe_combine_backward", "sk_gemm_grouped",
+                 "sk_gemm_grouped_backward", "sk_quantize_w4", "sk_dequantize_w4", "sk_gemm_w4", "sk_plan_wg_range", "sk_plan_wg_work", "sk_check", "sk_debug_poison_workspace", "sk_variant_info",
                  "sk_variant_k_split", "sk_stream_create_cu_masked", "sk_stream_destroy", "sk_stream_cu_count"):
         getattr(lib, name).restype = ctypes.c_int
     lib.sk_num_variants.restype = ctypes.c_int32
+    lib.sk_moe_route_work_bytes.restype = i64
     _LIB = lib
     return lib
 
@@ -927,3 +943,9 @@ def stream_cu_count(stream=None) -> int:
     n = ctypes.c_int32()
     _ok(load().sk_stream_cu_count(stream, ctypes.byref(n)), "sk_stream_cu_count")
     return n.value
+
+
+# ---------------------------------------------------------------- a layer of experts
+
+from .experts import (dequantize_w4, gemm_grouped, gemm_grouped_backward, gemm_w4, moe_combine,  # noqa: E402
+                      moe_combine_backward, moe_route, moe_route_backward, quantize_w4)

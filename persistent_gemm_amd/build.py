@@ -18,7 +18,8 @@ CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["sk_kernels.hip", "sk_kernels_mx.hip", "sk_kernels_ksplit.hip", "sk_backward.hip", "sk_quantize.hip",
-           "sk_gemm_block.hip", "sk_norm.hip", "sk_api.cpp", "sk_api_block.cpp"]
+           "sk_gemm_block.hip", "sk_norm.hip", "sk_experts.hip", "sk_grouped.hip", "sk_grouped_f16.hip", "sk_rows.hip",
+           "sk_quantize4.hip", "sk_api.cpp", "sk_api_block.cpp", "sk_api_experts.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
     # keep hipcc from emitting packed-fp32 arithmetic on its own

@@ -299,4 +299,108 @@ int64_t norm_grad_scratch_bytes(NormGradArgs* a, int cus);
 hipError_t launch_norm_backward(const NormGradArgs& a, bool f32, hipStream_t s);
 constexpr int kMaxNormWidth = 32768;
 
+// ---------------------------------------------------------------- a layer of experts
+
+// One product over rows sorted by expert (sk_grouped.h); sizes in elements, pitches in bytes.
+struct GroupedGemm {
+  const uint8_t* P;         // forward: A; dA, dB: dC
+  const uint8_t* Q;         // forward, dA: B [E][N][K]; dB: A
+  const int* offsets;       // [E + 1]
+  const int* rows;          // [R] rows of A, or NULL: A's rows are those of the groups
+  const uint16_t* bias;     // [E][N] or NULL (forward)
+  uint16_t* C;              // (dB: NULL where dbias alone is wanted)
+  uint16_t* dbias;          // [E][N] or NULL (dB)
+  int E, R;
+  int S;                    // the dimension summed over: K forward, N in dA
+  int Mout, Nout;           // dB: N and K; else Nout is the outputs' row length
+  int p_pitch, q_pitch;
+  int p_rows, q_rows;       // A's rows, where `rows` chooses among them
+  int tiles_m, tiles_n;     // set by the launcher
+  int tail;                 // whether the rows behind the last expert's are written (zeros)
+};
+hipError_t launch_grouped_bf16(const GroupedGemm& g, int kind, int cus, hipStream_t s);
+hipError_t launch_grouped_f16(const GroupedGemm& g, int kind, int cus, hipStream_t s);
+
+// Routing (sk_experts.hip).  Elements (sk_elem) of logits, y, out and their gradients.
+constexpr int kMaxExperts = 1024, kMaxChoices = 32;
+struct RouteArgs {
+  const void* logits;       // [T][E]
+  int* experts;             // [T][k], -1: no choice left
+  float* weights;           // [T][k]
+  int* offsets;             // [E + 1]
+  int* slots;               // [T][k], -1 likewise
+  int* rows;                // [T k]: the token of each row, -1 behind the last expert's
+  int* part;                // [route_blocks(T)][E]
+  int64_t T;
+  int E, k;
+  int normalize;
+  int per_block, blocks;    // set by the launcher
+};
+int64_t route_blocks(int64_t T);
+hipError_t launch_route(RouteArgs a, int elem, hipStream_t s);
+
+struct RouteGradArgs {
+  const float* dweights;    // [T][k]
+  const void* logits;       // [T][E]
+  const int* experts;
+  const float* weights;
+  void* dlogits;
+  int64_t T;
+  int E, k;
+  int normalize;
+};
+hipError_t launch_route_gradient(const RouteGradArgs& a, int elem, hipStream_t s);
+
+struct CombineArgs {
+  const void* y;            // [R][D]
+  const int* slots;         // [T][k]
+  const float* weights;     // [T][k] or NULL: 1
+  void* out;                // [T][D]
+  int64_t T;
+  int R, D, k;
+};
+hipError_t launch_combine(const CombineArgs& a, int elem, hipStream_t s);
+
+struct CombineGradArgs {
+  const void* dout;         // [T][D]
+  const void* y;            // [R][D], with dweights
+  const int* slots;
+  const float* weights;     // [T][k] or NULL: 1
+  const int* offsets;       // [E + 1] or NULL: dy is cleared first
+  void* dy;                 // [R][D]
+  float* dweights;          // [T][k] or NULL
+  int64_t T;
+  int R, D, k, E;
+};
+hipError_t launch_combine_gradient(const CombineGradArgs& a, int elem, hipStream_t s);
+
+// Products of few rows with 4-bit or 16-bit weights (sk_rows.hip), one weight or one for each expert.
+struct RowsGemm {
+  const uint8_t* x;         // rows of K
+  const uint8_t* W;         // [E][N][K / 2] codes, or [E][N][K] 16-bit
+  const uint8_t* scale;     // [E][K / group][N] 16-bit, with codes
+  const uint8_t* zero;      // [E][K / group][N] or NULL
+  const uint16_t* bias;     // [E][N] or NULL
+  const int* offsets;       // [E + 1], or NULL: one weight for all R rows
+  const int* rows;          // [R] rows of x, or NULL
+  uint16_t* C;              // [R][N]
+  int E, R, N, K;
+  int x_rows;
+  int tail;                 // whether the rows behind the last expert's are written (zeros)
+};
+hipError_t launch_rows_w4(const RowsGemm& g, int group, bool f16, int cus, hipStream_t s);
+hipError_t launch_rows_16(const RowsGemm& g, bool f16, int cus, hipStream_t s);
+
+// 4-bit weights (sk_quantize4.hip).
+struct Quant4Args {
+  const void* w;            // [rows][K]
+  uint8_t* q;               // [rows][K / 2]
+  void* scale;              // [E][K / group][N], 16-bit
+  uint8_t* zero;            // likewise, or NULL
+  void* out;                // dequantised: [rows][K]
+  int E, N, K, group;
+};
+hipError_t launch_quantize_w4(const Quant4Args& a, int elem, bool scale_f16, hipStream_t s);
+hipError_t launch_dequantize_w4(const Quant4Args& a, bool scale_f16, hipStream_t s);
+
 }  // namespace sk
