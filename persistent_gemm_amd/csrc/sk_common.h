@@ -315,8 +315,11 @@ struct GroupedGemm {
   int Mout, Nout;           // dB: N and K; else Nout is the outputs' row length
   int p_pitch, q_pitch;
   int p_rows, q_rows;       // A's rows, where `rows` chooses among them
-  int tiles_m, tiles_n;     // set by the launcher
   int tail;                 // whether the rows behind the last expert's are written (zeros)
+  // set by the launcher
+  int tiles_m, tiles_n;
+  int most;                 // tiles there can be
+  int cus;                  // units that share the last tiles' pieces, 0: tiles are not cut
 };
 hipError_t launch_grouped_bf16(const GroupedGemm& g, int kind, int cus, hipStream_t s);
 hipError_t launch_grouped_f16(const GroupedGemm& g, int kind, int cus, hipStream_t s);
