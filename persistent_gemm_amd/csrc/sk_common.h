@@ -337,7 +337,7 @@ struct RouteArgs {
   int64_t T;
   int E, k;
   int normalize;
-  int per_block, blocks;    // set by the launcher
+  int per_block, blocks;    // tokens of a workgroup, and workgroups: set by the launcher
 };
 int64_t route_blocks(int64_t T);
 hipError_t launch_route(RouteArgs a, int elem, hipStream_t s);

@@ -9,6 +9,8 @@ namespace {
 
 // ---------------------------------------------------------------- the choice
 
+constexpr int kFewTokens = 64, kPlaceBlocks = 4;
+
 // A logit as an integer that orders like it, 0 where it cannot be chosen (-inf, NaN).  (-0 is 0.)
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t u = f_bits(x + 0.0f);
@@ -17,88 +19,65 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return bits_f(k ^ ((int32_t)k < 0 ? 0x80000000u : 0xffffffffu)); }
 
-// The largest of L lanes' values, and their sum, in each of the L (a power of two).
+// f over L lanes' values (a power of two) in each of the L, always in the same order: lanes one and two apart, mirrored halves and
+// whole rows of 16, then rows exchanged.
+template <int L, class F>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t x, F&& f) {
+  auto dpp = [](uint32_t v, auto c) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(c)::value, 0xf, 0xf, true); };
+  using std::integral_constant;
+  if constexpr (L >= 2) x = f(x, dpp(x, integral_constant<int, 0xb1>{}));
+  if constexpr (L >= 4) x = f(x, dpp(x, integral_constant<int, 0x4e>{}));
+  if constexpr (L >= 8) x = f(x, dpp(x, integral_constant<int, 0x141>{}));
+  if constexpr (L >= 16) x = f(x, dpp(x, integral_constant<int, 0x140>{}));
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = f(r[0], r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = f(r[0], r[1]);
+  }
+  return x;
+}
 template <int L>
 __device__ __forceinline__ uint32_t max_of(uint32_t x) {
-#pragma unroll
-  for (int d = 1; d < L; d *= 2) x = max(x, (uint32_t)__shfl_xor((int)x, d));
-  return x;
+  return over_lanes<L>(x, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 template <int L>
 __device__ __forceinline__ float sum_of(float x) {
-#pragma unroll
-  for (int d = 1; d < L; d *= 2) x += __shfl_xor(x, d);
-  return x;
+  return bits_f(over_lanes<L>(f_bits(x), [](uint32_t a, uint32_t b) { return f_bits(bits_f(a) + bits_f(b)); }));
+}
+template <int L>
+__device__ __forceinline__ float largest_of(float x) {
+  return bits_f(over_lanes<L>(f_bits(x), [](uint32_t a, uint32_t b) { return f_bits(fmaxf(bits_f(a), bits_f(b))); }));
 }
 
-// L lanes to a token, V logits to a lane (lane l: l V .. l V + V - 1, so that the first lane that holds the largest key
-// holds the lowest expert).  A choice is one maximum over keys; the softmax's maximum is the first choice.
-// Counts of a workgroup's pairs by expert go to part [workgroup][E].
-template <class T, int L, int V>
-__global__ __launch_bounds__(256) void sk_route_choose(RouteArgs a) {
-  constexpr int PER = 256 / L;       // tokens at a time
-  __shared__ float val[PER][kMaxChoices];
-  __shared__ int idx[PER][kMaxChoices];
-  __shared__ int count[kMaxExperts];
-  const int l = threadIdx.x % L, slot = threadIdx.x / L;
-  for (int e = threadIdx.x; e < a.E; e += 256) count[e] = 0;
-  __syncthreads();
-  const int64_t first = (int64_t)blockIdx.x * a.per_block;
-  const int n = (int)min((int64_t)a.per_block, a.T - first);
-  for (int at = slot; at < n; at += PER) {
-    const int64_t t = first + at;
-    const T* const row = (const T*)a.logits + t * a.E;
-    uint32_t key[V];
-    float x[V];
-    bool nan = false;
+// V consecutive logits of a row from column `col` on, -inf behind its end.  `wide`: E is a multiple of V and rows are aligned to V
+// elements, so that a lane's are all there or none.
+template <class T, int V>
+__device__ __forceinline__ void load_logits(const T* row, int col, int E, bool wide, float (&x)[V]) {
+  if (wide) {
+    constexpr int W = V * sizeof(T) / 4 < 4 ? V * sizeof(T) / 4 : 4;      // words of a load
+    typedef uint32_t words __attribute__((ext_vector_type(W)));
+    constexpr int N = V * sizeof(T) / (4 * W);
+    if (col < E) {
+      words w[N];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = l * V + v;
-      x[v] = e < a.E ? load_elem(row + e) : -__builtin_inff();
-      nan |= x[v] != x[v];
-      key[v] = key_of(x[v]);
+      for (int i = 0; i < N; ++i) w[i] = ((const words*)(row + col))[i];
+      const T* const t = (const T*)w;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = load_elem(t + v);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = -__builtin_inff();
     }
-    float top = 0.0f, total = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t best = key[0];
+  } else {
 #pragma unroll
-      for (int v = 1; v < V; ++v) best = max(best, key[v]);
-      const uint32_t most = max_of<L>(best);
-      const uint64_t who = __ballot(best == most) >> ((threadIdx.x & 63) / L * L);
-      const int winner = __builtin_ctzll(who);            // the first lane of the token's
-      int mine = 0;
-#pragma unroll
-      for (int v = V - 1; v >= 0; --v) mine = key[v] == most ? v : mine;
-      if (l == winner) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = v == mine ? 0u : key[v];
-        idx[slot][j] = most ? l * V + mine : -1;
-      }
-      const float f = value_of(most);
-      if (j == 0) top = f;
-      const float p = most ? expf(f - top) : 0.0f;
-      if (a.normalize) total += p;
-      if (l == 0) val[slot][j] = p;
-    }
-    if (!a.normalize) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) total += x[v] > -__builtin_inff() ? expf(x[v] - top) : 0.0f;
-      total = sum_of<L>(total);
-    }
-    nan = (__ballot(nan) >> ((threadIdx.x & 63) / L * L) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) != 0;
-    __builtin_amdgcn_wave_barrier();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (a token's lanes are of one wave)
-    for (int j = l; j < a.k; j += L) {
-      const int e = idx[slot][j];
-      a.experts[t * a.k + j] = e;
-      a.weights[t * a.k + j] = e < 0 ? 0.0f : nan ? __builtin_nanf("") : val[slot][j] / total;
-      if (e >= 0) atomicAdd(&count[e], 1);
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    for (int v = 0; v < V; ++v) x[v] = col + v < E ? load_elem(row + col + v) : -__builtin_inff();
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += 256) a.part[(int64_t)blockIdx.x * a.E + e] = count[e];
 }
+
+// ---------------------------------------------------------------- the order by expert
 
 // Lanes of the wave whose key is this lane's, `bits` bits long.
 __device__ __forceinline__ uint64_t same_key(int key, int bits) {
@@ -111,65 +90,65 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits) {
   return m;
 }
 
-// The place of each pair of the workgroup's tokens among all pairs sorted by expert: a stable counting sort.  A
-// workgroup adds up the counts of the workgroups before it; a wave takes a run of its pairs, 64 at a time, whose places
-// follow from the lanes before it with the same expert.
 template <int NT>
-__global__ __launch_bounds__(NT) void sk_route_place(RouteArgs a) {
-  constexpr int NW = NT / 64;
-  extern __shared__ int place_smem[];
-  int* const next = place_smem;                 // [NW][E]: a wave's next place in each expert
-  int* const scan = place_smem + NW * a.E;      // [NT]
+struct PlaceShared {
+  int next[NT / 64 * kMaxExperts];   // [wave][expert]: the wave's next place
+  int all[kMaxExperts], before[kMaxExperts];
+  int sums[NT / 64];
+};
+
+// The place of each of a workgroup's n pairs (from pair `first` on, their choices in ids) among all pairs sorted by expert: a stable
+// counting sort.  sh.all has all pairs' counts, sh.before those of the workgroups before this one.  A wave takes a run of
+// the pairs, 64 at a time, whose places follow from the lanes before it with the same expert.  Returns the number of all pairs.
+template <int NT>
+__device__ __forceinline__ int place_pairs(const RouteArgs& a, PlaceShared<NT>& sh, const int* ids, int64_t first, int n, bool write_offsets) {
+  constexpr int WAVES = NT / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-  const int64_t first = (int64_t)blockIdx.x * a.per_block;
-  const int n = (int)(min((int64_t)a.per_block, a.T - first) * a.k);
-  const int* const ids = a.experts + first * a.k;
-  const int run = ((n + NW - 1) / NW + 63) / 64 * 64;      // pairs of a wave
+  const int run = ((n + WAVES - 1) / WAVES + 63) / 64 * 64;      // pairs of a wave
   const int p0 = min(wave * run, n), p1 = min(p0 + run, n);
-  for (int i = threadIdx.x; i < NW * a.E; i += NT) next[i] = 0;
+  for (int i = threadIdx.x; i < WAVES * a.E; i += NT) sh.next[i] = 0;
   __syncthreads();
   for (int p = p0 + lane; p < p1; p += 64) {
     const int e = ids[p];
-    if (e >= 0) atomicAdd(&next[wave * a.E + e], 1);
+    if (e >= 0) atomicAdd(&sh.next[wave * a.E + e], 1);
   }
-  // experts in turn, NT at a time: all workgroups' counts, those before this one, and the sum over experts
   int base = 0;
   for (int e0 = 0; e0 < a.E; e0 += NT) {
     const int e = e0 + (int)threadIdx.x;
-    int all = 0, before = 0;
-    if (e < a.E) {
-      for (int b = 0; b < a.blocks; ++b) {
-        const int c = a.part[(int64_t)b * a.E + e];
-        all += c;
-        before += b < (int)blockIdx.x ? c : 0;
-      }
+    const int mine = e < a.E ? sh.all[e] : 0;
+    int x = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int y = __shfl_up(x, d);
+      x += lane >= d ? y : 0;
     }
-    scan[threadIdx.x] = all;
-    __syncthreads();
-    for (int d = 1; d < NT; d *= 2) {
-      const int y = (int)threadIdx.x >= d ? scan[threadIdx.x - d] : 0;
-      __syncthreads();
-      scan[threadIdx.x] += y;
-      __syncthreads();
+    if (lane == 63) sh.sums[wave] = x;
+    __syncthreads();          // (also: the waves' counts are there)
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const int s = sh.sums[w];
+      x += w < wave ? s : 0;
+      total += s;
     }
-    const int upto = base + scan[threadIdx.x];
     if (e < a.E) {
-      if (blockIdx.x == 0) {
+      if (write_offsets) {
         if (e == 0) a.offsets[0] = 0;
-        a.offsets[e + 1] = upto;
+        a.offsets[e + 1] = base + x;
       }
-      int at = upto - all + before;
-      for (int w = 0; w < NW; ++w) {
-        const int c = next[w * a.E + e];
-        next[w * a.E + e] = at;
+      int at = base + x - mine + sh.before[e];
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const int c = sh.next[w * a.E + e];
+        sh.next[w * a.E + e] = at;
         at += c;
       }
     }
-    base += scan[NT - 1];
+    base += total;
     __syncthreads();
   }
   const int bits = 32 - __builtin_clz(a.E);       // of keys 0 .. E
-  volatile int* const mine = next + wave * a.E;
+  volatile int* const mine = sh.next + wave * a.E;
   for (int p = p0; p < p1; p += 64) {
     const int at = p + lane;
     const int e = at < p1 ? ids[at] : -1;
@@ -183,54 +162,195 @@ __global__ __launch_bounds__(NT) void sk_route_place(RouteArgs a) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_wave_barrier();
     if (at < p1) {
-      a.slots[first * a.k + at] = slot;
-      if (slot >= 0) a.rows[slot] = (int)(first + at / a.k);
+      a.slots[first + at] = slot;
+      if (slot >= 0) a.rows[slot] = (int)((uint32_t)(first + at) / (uint32_t)a.k);
     }
   }
-  // rows behind the last expert's belong to no token
+  return base;
+}
+
+// ---------------------------------------------------------------- the choice
+
+// Choices of the workgroup's tokens, and what is counted of them.  L lanes to a token, V logits to a lane (lane l: l V .. l V + V - 1, so
+// that the first lane that holds the largest key holds the lowest expert).  A lane's keys are sorted once (falling, equal ones
+// in their order); a choice is then one maximum over the lanes' first keys, and the lane that had it moves its others up.
+// The softmax's maximum is the first choice.  Lane l keeps choices l, l + L, ...
+template <class T, int L, int V, int NT>
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t first, int n, int* count, int* ids) {
+  constexpr int PER = NT / L, KEPT = (kMaxChoices + L - 1) / L;
+  const int lane = threadIdx.x & 63, l = threadIdx.x % L, group = lane / L * L;
+  const bool wide = a.E % V == 0 && ((uintptr_t)a.logits & (V * sizeof(T) - 1)) == 0;
+  for (int at = threadIdx.x / L; at < n; at += PER) {
+    const int64_t t = first + at;
+    uint32_t key[V];
+    int expert[V];
+    float x[V];
+    load_logits<T, V>((const T*)a.logits + t * a.E, l * V, a.E, wide, x);
+    bool nan = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      nan |= x[v] != x[v];
+      key[v] = key_of(x[v]);
+      expert[v] = l * V + v;
+    }
+#pragma unroll
+    for (int round = 0; round < V - 1; ++round)
+#pragma unroll
+      for (int v = 0; v < V - 1 - round; ++v) {
+        const bool swap = key[v + 1] > key[v];
+        const uint32_t hi = max(key[v], key[v + 1]), lo = min(key[v], key[v + 1]);
+        const int e0 = swap ? expert[v + 1] : expert[v], e1 = swap ? expert[v] : expert[v + 1];
+        key[v] = hi;
+        key[v + 1] = lo;
+        expert[v] = e0;
+        expert[v + 1] = e1;
+      }
+    uint32_t top_key = 0, kept[KEPT];
+    int which[KEPT];
+#pragma unroll
+    for (int q = 0; q < KEPT; ++q) {
+      kept[q] = 0u;
+      which[q] = -1;
+    }
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t most = max_of<L>(key[0]);
+      if (j == 0) top_key = most;
+      const int winner = __builtin_ctzll(__ballot(key[0] == most) >> group);            // the first lane of the token's
+      const int e = L == 64 ? __builtin_amdgcn_readlane(expert[0], winner) : __shfl(expert[0], group + winner);
+      const bool mine = l == winner;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        key[v] = mine ? (v + 1 < V ? key[v + 1 < V ? v + 1 : 0] : 0u) : key[v];
+        expert[v] = mine && v + 1 < V ? expert[v + 1 < V ? v + 1 : 0] : expert[v];
+      }
+#pragma unroll
+      for (int q = 0; q < KEPT; ++q) {
+        const bool here = j == q * L + l;
+        kept[q] = here ? most : kept[q];
+        which[q] = here && most ? e : which[q];
+      }
+    }
+    const float top = value_of(top_key);
+    float p[KEPT], total = 0.0f;
+#pragma unroll
+    for (int q = 0; q < KEPT; ++q) {
+      p[q] = kept[q] ? expf(value_of(kept[q]) - top) : 0.0f;
+      total += p[q];
+    }
+    if (!a.normalize) {
+      total = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) total += x[v] > -__builtin_inff() ? expf(x[v] - top) : 0.0f;
+    }
+    total = sum_of<L>(total);
+    nan = (__ballot(nan) >> group & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) != 0;
+#pragma unroll
+    for (int q = 0; q < KEPT; ++q) {
+      const int j = q * L + l, e = which[q];
+      if (j < a.k) {
+        a.experts[t * a.k + j] = e;
+        a.weights[t * a.k + j] = e < 0 ? 0.0f : nan ? __builtin_nanf("") : p[q] / total;
+        if (ids) ids[at * a.k + j] = e;
+        if (e >= 0) atomicAdd(&count[e], 1);
+      }
+    }
+  }
+}
+
+// Many tokens: their choices, and counts by expert of each workgroup's, part [workgroup][E].  (One pass over 16384 x 256 logits; what
+// bounds it is the k maxima of each token.)
+constexpr int kChooseThreads = 1024, kPlaceThreads = 1024, kFewThreads = 512;
+template <class T, int L, int V>
+__global__ __launch_bounds__(kChooseThreads) void sk_route_choose(RouteArgs a) {
+  __shared__ int count[kMaxExperts];
+  for (int e = threadIdx.x; e < a.E; e += kChooseThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t first = (int64_t)blockIdx.x * a.per_block;
+  choose<T, L, V, kChooseThreads>(a, first, (int)min((int64_t)a.per_block, a.T - first), count, nullptr);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kChooseThreads) a.part[(int64_t)blockIdx.x * a.E + e] = count[e];
+}
+
+// The places of the pairs of kPlaceBlocks workgroups of the first kernel; rows behind the last expert's belong to no token.
+__global__ __launch_bounds__(kPlaceThreads) void sk_route_place(RouteArgs a) {
+  __shared__ PlaceShared<kPlaceThreads> sh;
+  for (int e = threadIdx.x; e < a.E; e += kPlaceThreads) sh.all[e] = sh.before[e] = 0;
+  __syncthreads();
+  // the counts of all workgroups: `wide` threads side by side, the rest shares out the workgroups
+  const int wide = a.E >= kPlaceThreads ? kPlaceThreads : 1 << (32 - __builtin_clz(max(a.E - 1, 1)));
+  const int lanes = min(wide, kPlaceThreads), share = kPlaceThreads / lanes, b0 = threadIdx.x / lanes;
+  const int own = (int)blockIdx.x * kPlaceBlocks;
+  for (int e = threadIdx.x % lanes; e < a.E; e += lanes) {
+    int all = 0, before = 0;
+#pragma unroll 16
+    for (int b = b0; b < a.blocks; b += share) {
+      const int c = a.part[(int64_t)b * a.E + e];
+      all += c;
+      before += b < own ? c : 0;
+    }
+    atomicAdd(&sh.all[e], all);
+    atomicAdd(&sh.before[e], before);
+  }
+  __syncthreads();
+  const int64_t first = (int64_t)own * a.per_block;
+  const int n = (int)(min((int64_t)a.per_block * kPlaceBlocks, a.T - first) * a.k);
+  const int base = place_pairs(a, sh, a.experts + first * a.k, first * a.k, n, blockIdx.x == 0);
   const int64_t all = a.T * a.k;
-  for (int64_t r = base + (int64_t)blockIdx.x * NT + threadIdx.x; r < all; r += (int64_t)gridDim.x * NT) a.rows[r] = -1;
+  for (int64_t r = base + (int64_t)blockIdx.x * kPlaceThreads + threadIdx.x; r < all; r += (int64_t)gridDim.x * kPlaceThreads) a.rows[r] = -1;
+}
+
+// Few tokens: both in one workgroup.
+template <class T, int L, int V>
+__global__ __launch_bounds__(kFewThreads) void sk_route_few(RouteArgs a) {
+  __shared__ PlaceShared<kFewThreads> sh;
+  __shared__ int ids[kFewTokens * kMaxChoices];
+  for (int e = threadIdx.x; e < a.E; e += kFewThreads) sh.all[e] = sh.before[e] = 0;
+  __syncthreads();
+  choose<T, L, V, kFewThreads>(a, 0, (int)a.T, sh.all, ids);
+  __syncthreads();
+  const int n = (int)a.T * a.k, base = place_pairs(a, sh, ids, 0, n, true);
+  for (int r = base + threadIdx.x; r < n; r += kFewThreads) a.rows[r] = -1;
 }
 
 // dlogits = w (d - sum w d) at the chosen experts, or p (d - sum w d) at all of them (d 0 where not chosen).
+// (The choices are read by one lane each and handed round.)
 template <class T, int L, int V>
 __global__ __launch_bounds__(256) void sk_route_gradient(RouteGradArgs a) {
-  constexpr int PER = 256 / L;
-  const int l = threadIdx.x % L;
+  constexpr int PER = 256 / L, KEPT = (kMaxChoices + L - 1) / L;
+  const int l = threadIdx.x % L, group = (threadIdx.x & 63) / L * L;
+  const bool wide = a.E % V == 0 && (((uintptr_t)a.logits | (uintptr_t)a.dlogits) & (V * sizeof(T) - 1)) == 0;
   for (int64_t t = (int64_t)blockIdx.x * PER + threadIdx.x / L; t < a.T; t += (int64_t)gridDim.x * PER) {
-    const int* const ids = a.experts + t * a.k;
-    const float* const w = a.weights + t * a.k;
-    const float* const d = a.dweights + t * a.k;
-    float x[V], g[V], top = -__builtin_inff(), total = 0.0f, mean = 0.0f;
+    float x[V], g[V], d[KEPT], mean = 0.0f;
+    int e[KEPT];
+    if (!a.normalize) load_logits<T, V>((const T*)a.logits + t * a.E, l * V, a.E, wide, x);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      g[v] = 0.0f;
-      x[v] = 0.0f;
-      if (!a.normalize) {
-        const int e = l * V + v;
-        x[v] = e < a.E ? load_elem((const T*)a.logits + t * a.E + e) : -__builtin_inff();
-        top = fmaxf(top, x[v]);
-      }
+    for (int q = 0; q < KEPT; ++q) {
+      const int j = q * L + l;
+      const bool in = j < a.k;
+      e[q] = in ? a.experts[t * a.k + j] : -1;
+      const float w = e[q] >= 0 ? a.weights[t * a.k + j] : 0.0f;
+      d[q] = e[q] >= 0 ? a.dweights[t * a.k + j] : 0.0f;
+      mean = __builtin_fmaf(w, d[q], mean);
     }
-    for (int j = 0; j < a.k; ++j) {
-      const int e = ids[j];
-      if (e < 0) continue;
-      mean = __builtin_fmaf(w[j], d[j], mean);
-      if (!a.normalize) {
+    mean = sum_of<L>(mean);
 #pragma unroll
-        for (int v = 0; v < V; ++v) g[v] = e == l * V + v ? d[j] : g[v];
+    for (int q = 0; q < KEPT; ++q)
+      if (a.normalize) d[q] = e[q] >= 0 ? a.weights[t * a.k + q * L + l] * (d[q] - mean) : 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < KEPT; ++q)
+      for (int j = 0; j < min(L, a.k - q * L); ++j) {
+        const int at = __shfl(e[q], group + j);
+        const float y = __shfl(d[q], group + j);
+#pragma unroll
+        for (int v = 0; v < V; ++v) g[v] = at == l * V + v ? y : g[v];
       }
-    }
-    if (a.normalize) {
-      for (int j = 0; j < a.k; ++j) {
-        const int e = ids[j];
-        const float y = w[j] * (d[j] - mean);
+    if (!a.normalize) {
+      float top = x[0], total = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) g[v] = e == l * V + v ? y : g[v];
-      }
-    } else {
-#pragma unroll
-      for (int d2 = 1; d2 < L; d2 *= 2) top = fmaxf(top, __shfl_xor(top, d2));
+      for (int v = 1; v < V; ++v) top = fmaxf(top, x[v]);
+      top = largest_of<L>(top);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         // (a NaN compares false and stays one; a token without a choice has probabilities of 0)
@@ -238,12 +358,26 @@ __global__ __launch_bounds__(256) void sk_route_gradient(RouteGradArgs a) {
         total += x[v];
       }
       total = sum_of<L>(total);
+      const float r = total != 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) g[v] = (total != 0.0f ? x[v] / total : 0.0f) * (g[v] - mean);
+      for (int v = 0; v < V; ++v) g[v] = x[v] * r * (g[v] - mean);
     }
+    T* const to = (T*)a.dlogits + t * a.E + l * V;
+    if (wide) {
+      constexpr int W = V * sizeof(T) / 4 < 4 ? V * sizeof(T) / 4 : 4, N = V * sizeof(T) / (4 * W);
+      typedef uint32_t words __attribute__((ext_vector_type(W)));
+      words w[N];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (l * V + v < a.E) store_elem((T*)a.dlogits + t * a.E + l * V + v, g[v]);
+      for (int v = 0; v < V; ++v) store_elem((T*)w + v, g[v]);
+      if (l * V < a.E) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) ((words*)to)[i] = w[i];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (l * V + v < a.E) store_elem(to + v, g[v]);
+    }
   }
 }
 
@@ -337,25 +471,27 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Tokens of a workgroup: 256, and more where there would be over 128 workgroups (each of which reads the counts of all).
-int route_per_block(int64_t T) { return (int)(cdiv64(cdiv64(T, 128), 256) * 256); }
+// Tokens of a workgroup: 64, and more where there would be over 256 workgroups, whose counts are all read by a quarter as many.
+int route_per_block(int64_t T) { return (int)(cdiv64(cdiv64(T, 256), 64) * 64); }
 int64_t route_blocks(int64_t T) { return cdiv64(T, route_per_block(T)); }
 
 hipError_t launch_route(RouteArgs a, int elem, hipStream_t s) {
+  // one workgroup for few tokens: 1 of 64 experts X.X us on the device against Y.Y as two kernels
+  if (a.T <= kFewTokens)
+    return by_elem(elem, [&](auto t) {
+      return by_experts(a.E, [&](auto l, auto v) {
+        return launch(sk_route_few<decltype(t), decltype(l)::value, decltype(v)::value>, dim3(1), kFewThreads, s, a);
+      });
+    });
   a.per_block = route_per_block(a.T);
   a.blocks = (int)route_blocks(a.T);
   const hipError_t e = by_elem(elem, [&](auto t) {
     return by_experts(a.E, [&](auto l, auto v) {
-      return launch(sk_route_choose<decltype(t), decltype(l)::value, decltype(v)::value>, dim3((unsigned)a.blocks), 256, s, a);
+      return launch(sk_route_choose<decltype(t), decltype(l)::value, decltype(v)::value>, dim3((unsigned)a.blocks), kChooseThreads, s, a);
     });
   });
   if (e != hipSuccess) return e;
-  constexpr int NT = 512;
-  void* args[] = {&a};
-  const hipError_t r = hipLaunchKernel((const void*)sk_route_place<NT>, dim3((unsigned)a.blocks), dim3(NT), args,
-                                       (NT / 64 * a.E + NT) * sizeof(int), s);
-  if (r != hipSuccess) (void)hipGetLastError();
-  return r;
+  return launch(sk_route_place, dim3((unsigned)cdiv64(a.blocks, kPlaceBlocks)), kPlaceThreads, s, a);
 }
 
 hipError_t launch_route_gradient(const RouteGradArgs& a, int elem, hipStream_t s) {

@@ -40,15 +40,15 @@ def _check_route(x, k, normalize):
 @pytest.mark.parametrize("T,E,k,dtype", [
     (1, 1, 1, FP), (1, 64, 6, FP), (3, 5, 5, HF), (7, 16, 16, FP), (64, 8, 2, BF), (255, 60, 6, FP), (256, 17, 4, HF),
     (257, 64, 8, FP), (300, 33, 2, BF), (513, 128, 8, FP), (700, 256, 8, FP), (65, 257, 3, HF), (40, 512, 32, FP),
-    (33, 1024, 9, BF), (2000, 4, 1, FP),
+    (33, 1024, 9, BF), (2000, 4, 1, FP), (64, 40, 8, HF), (65, 40, 8, BF), (127, 36, 4, FP),
 ])
 def test_route(T, E, k, dtype, normalize):
     _check_route(_rand(T * 1000 + E, T, E, dtype=dtype, scale=2.0), k, normalize)
 
 
 def test_route_many_tokens():
-    # more tokens than 128 workgroups of 256 take
-    T, E, k = 128 * 256 + 300, 8, 2
+    # more tokens than 256 workgroups of 64 take
+    T, E, k = 2 * 256 * 64 + 300, 8, 2
     x = _rand(5, T, E)
     got = pg.moe_route(x.cuda(), k)
     top, ids = torch.sort(x, dim=1, descending=True, stable=True)
