@@ -377,7 +377,8 @@ sk_status sk_norm_backward(const sk_norm_grad_args* args);
  *   offsets  int32 [E+1]    pairs of expert e are the rows offsets[e] .. offsets[e+1]-1, in the order of the pairs
  *   slots    int32 [T][k]   the row of each pair, -1 without an expert
  *   rows     int32 [T*k]    the token of each row, -1 behind the last expert's
- * work: sk_moe_route_work_bytes(T, E) bytes of the caller's device memory, 4-byte aligned, for this call alone.
+ * work: sk_moe_route_work_bytes(T, E) bytes of the caller's device memory, 4-byte aligned, for this call alone (0 for few
+ * tokens: then it may be NULL).
  * SK_ERR_ARG: a NULL pointer, T, E or k < 1, E > 1024, k > 32 or k > E, T * k >= 2^31 - 2^20, an output that overlaps the
  * logits or another output. */
 int64_t sk_moe_route_work_bytes(int64_t T, int64_t E);

@@ -484,6 +484,9 @@ def _native():
         native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
             "sk_quantize_fp8_block", "sk_gemm_fp8_block", "sk_gemm_fp8_block_backward", "sk_norm_forward",
             "sk_norm_backward")), torch._C._cuda_getCurrentRawStream)
+        native.bind_experts(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "sk_moe_route_work_bytes", "sk_moe_route", "sk_moe_route_backward", "sk_moe_combine", "sk_moe_combine_backward",
+            "sk_gemm_grouped", "sk_gemm_grouped_backward", "sk_quantize_w4", "sk_dequantize_w4", "sk_gemm_w4")))
         _NATIVE = native
     return _NATIVE
 

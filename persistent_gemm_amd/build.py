@@ -12,8 +12,9 @@ LIB = os.path.join(HERE, "libskgemm.so")
 # device-ceiling probes for the roofline (bench.py --ceiling), a library of their own
 PROBE_LIB = os.path.join(HERE, "libskprobe.so")
 PROBE_SOURCES = ["sk_probe.hip"]
-# the native binding of the block-scaled and norm calls: host code against torch's headers
+# the native binding of the block-scaled, norm and expert calls: host code against torch's headers
 NATIVE = os.path.join(HERE, "_sknative.so")
+NATIVE_SOURCES = ["sk_native.cpp", "sk_native_experts.cpp"]
 CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -54,7 +55,7 @@ def build(verbose: bool = False) -> str:
         try:
             native.result()
         except (ImportError, OSError, RuntimeError) as e:
-            print(f"the native binding was not built (the block-scaled and norm calls of the Python package need it): {e}",
+            print(f"the native binding was not built (the block-scaled, norm and expert calls of the Python package need it): {e}",
                   file=sys.stderr)
     return LIB
 
@@ -74,7 +75,7 @@ def _native_command(out):
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + sysconfig.get_paths()["include"]]
     for p in include_paths():
         cmd += ["-isystem", p]
-    return cmd + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "sk_native.cpp"),
+    return cmd + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(os.path.join(CSRC, n) for n in NATIVE_SOURCES),
                   "-o", out, "-L" + root, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 

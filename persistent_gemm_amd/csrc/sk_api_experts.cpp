@@ -55,8 +55,8 @@ int64_t sk_moe_route_work_bytes(int64_t T, int64_t E) {
 sk_status sk_moe_route(const void* logits, sk_elem elem, int normalize, int32_t* experts, float* weights,
                        int32_t* offsets, int32_t* slots, int32_t* rows, void* work, int64_t T, int64_t E, int64_t k,
                        void* stream) {
-  if (!elem_ok(elem) || !logits || !experts || !weights || !offsets || !slots || !rows || !work) return SK_ERR_ARG;
-  if (!route_sizes_ok(T, E, k)) return SK_ERR_ARG;
+  if (!elem_ok(elem) || !logits || !experts || !weights || !offsets || !slots || !rows) return SK_ERR_ARG;
+  if (!route_sizes_ok(T, E, k) || (!work && sk_moe_route_work_bytes(T, E))) return SK_ERR_ARG;
   if (misaligned(logits, (uintptr_t)size_of(elem))) return SK_ERR_ALIGN;
   for (const void* p : {(const void*)experts, (const void*)weights, (const void*)offsets, (const void*)slots,
                         (const void*)rows, (const void*)work})

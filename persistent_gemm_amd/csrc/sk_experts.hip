@@ -473,7 +473,8 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tokens of a workgroup: 64, and more where there would be over 256 workgroups, whose counts are all read by a quarter as many.
 int route_per_block(int64_t T) { return (int)(cdiv64(cdiv64(T, 256), 64) * 64); }
-int64_t route_blocks(int64_t T) { return cdiv64(T, route_per_block(T)); }
+// (none where one workgroup does it all)
+int64_t route_blocks(int64_t T) { return T <= kFewTokens ? 0 : cdiv64(T, route_per_block(T)); }
 
 hipError_t launch_route(RouteArgs a, int elem, hipStream_t s) {
   // one workgroup for few tokens: 1 of 64 experts X.X us on the device against Y.Y as two kernels

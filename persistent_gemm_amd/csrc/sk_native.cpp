@@ -6,21 +6,19 @@
 // nothing: the binding's own checks then say what is wrong.  A status of the C ABI other than SK_OK
 // comes back as an int.  The library's entry points are handed in by bind(), so that both ways run the same one.
 
-#include <Python.h>
+#include "sk_native.h"
 
-#include <ATen/EmptyTensor.h>
-#include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
-#include <c10/core/impl/DeviceGuardImplInterface.h>
-#include <torch/csrc/autograd/python_variable.h>
 
-#include <cstring>
+#include <vector>
 
-#include "../../include/sk_gemm.h"
+namespace sk_native {
+PyObject* current_stream = nullptr;
+}
 
 namespace {
 
-using at::Tensor;
+using namespace sk_native;
 
 struct Library {
   decltype(&sk_quantize_fp8_block) quantize = nullptr;
@@ -33,89 +31,9 @@ struct Library {
 constexpr int64_t up16(int64_t n) { return (n + 15) & ~(int64_t)15; }
 constexpr int64_t blocks(int64_t n) { return (n + 127) >> 7; }
 
-// An argument: a tensor, None, or neither.
-struct Arg {
-  const Tensor* t = nullptr;
-  bool bad = false;
-  explicit Arg(PyObject* o) {
-    if (THPVariable_Check(o)) t = &THPVariable_Unpack(o);
-    else bad = o != Py_None;
-  }
-  void* ptr() const { return t ? t->data_ptr() : nullptr; }
-};
-
-bool is(const Tensor& t, c10::Device dev, at::ScalarType type, at::IntArrayRef shape) {
-  return t.layout() == at::kStrided && t.device() == dev && t.scalar_type() == type && t.sizes() == shape && t.is_contiguous();
-}
 bool is_codes(const Tensor& t, c10::Device dev, at::IntArrayRef shape) {
   return is(t, dev, t.scalar_type() == at::kByte ? at::kByte : at::kFloat8_e4m3fn, shape);
 }
-// NULL, or as described.
-bool none_or(const Arg& a, c10::Device dev, at::ScalarType type, at::IntArrayRef shape) {
-  return !a.bad && (!a.t || is(*a.t, dev, type, shape));
-}
-
-// An output, from the allocator that torch's own tensors of the device come from (the first one says which).  at::empty
-// finds it through two dispatches: 0.75 us a tensor against 0.32.  The allocator serves the current device, which
-// stream_of() has made sure of.
-Tensor make(at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
-  static c10::Allocator* allocator = nullptr;
-  if (allocator) return at::detail::empty_generic(shape, allocator, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
-  const Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(dev));
-  allocator = t.storage().allocator();
-  return t;
-}
-
-// The stream to use: the caller's handle, or torch's current one of the device (by the function bind() was given).
-// False where the handle is none, or the device not the current one, which the library launches on.
-PyObject* current_stream = nullptr;
-bool stream_of(PyObject* o, c10::Device dev, void** s) {
-  if (c10::impl::getDeviceGuardImpl(dev.type())->getDevice() != dev) return false;
-  if (o == Py_None) {
-    PyObject* index = PyLong_FromLong(dev.index());
-    PyObject* handle = index ? PyObject_CallFunctionObjArgs(current_stream, index, nullptr) : nullptr;
-    *s = handle ? PyLong_AsVoidPtr(handle) : nullptr;
-    Py_XDECREF(index);
-    Py_XDECREF(handle);
-  } else {
-    *s = PyLong_AsVoidPtr(o);
-  }
-  if (!PyErr_Occurred()) return true;
-  PyErr_Clear();
-  return false;
-}
-
-PyObject* put(const Tensor& t) {
-  if (!t.defined()) Py_RETURN_NONE;
-  return THPVariable_Wrap(t);
-}
-PyObject* pack(std::initializer_list<Tensor> ts) {
-  PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
-  Py_ssize_t i = 0;
-  if (r)
-    for (const Tensor& t : ts) PyTuple_SET_ITEM(r, i++, put(t));
-  return r;
-}
-PyObject* refuse() { Py_RETURN_NONE; }
-
-// Whatever torch throws (out of memory, say) leaves as a Python error.
-template <class F>
-PyObject* guarded(F&& f) {
-  try {
-    return f();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
-}
-
-// The interpreter lock given up for a call that uses the library's scratch: it may wait for another thread's call on the
-// stream, or for the stream itself when the scratch has to grow.
-struct Unlocked {
-  PyThreadState* const state = PyEval_SaveThread();
-  ~Unlocked() { PyEval_RestoreThread(state); }
-};
-
 int elem_of(const Tensor& t) {
   return t.scalar_type() == at::kBFloat16 ? SK_ELEM_BF16 : t.scalar_type() == at::kFloat ? SK_ELEM_F32 : -1;
 }
@@ -375,16 +293,18 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
-PyMethodDef method(const char* name) {
-  return {name, (PyCFunction)(void*)F, METH_FASTCALL, nullptr};
-}
 PyMethodDef methods[] = {method<quantize>("quantize"),         method<gemm>("gemm"),
                          method<gemm_backward>("gemm_backward"), method<norm_forward>("norm_forward"),
-                         method<norm_backward>("norm_backward"), method<bind>("bind"),
-                         {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sknative", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+                         method<norm_backward>("norm_backward"), method<bind>("bind")};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__sknative() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__sknative() {
+  static std::vector<PyMethodDef> all(methods, methods + sizeof(methods) / sizeof(methods[0]));
+  for (const PyMethodDef* m = experts_methods;; ++m) {
+    all.push_back(*m);
+    if (!m->ml_name) break;
+  }
+  static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sknative", nullptr, -1, all.data(), nullptr, nullptr, nullptr, nullptr};
+  return PyModule_Create(&module);
+}

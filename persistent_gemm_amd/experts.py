@@ -75,6 +75,12 @@ def moe_route(logits, k, *, normalize=True, stream=None):
     slots int32 [T, k], rows int32 [T * k]: pair (t, j) is row slots[t, j] (-1 without an expert) of the rows sorted by expert,
     expert e has rows offsets[e] to offsets[e + 1], in the order of the pairs, and rows gives each one's token (-1 behind the
     last expert's).  They are what gemm_grouped, gemm_w4 and moe_combine take."""
+    if stream is None:
+        got = (_pg._NATIVE or _pg._native()).moe_route(logits, k, normalize)
+        if got.__class__ is not int and got is not None:
+            return got
+        if got is not None:
+            raise _pg.SkError(got, "sk_moe_route")
     T, E = _dims(logits, "logits", 2)
     with _on(logits, "logits", stream):
         torch = _pg._torch()
@@ -87,15 +93,22 @@ def moe_route(logits, k, *, normalize=True, stream=None):
         new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)      # noqa: E731
         experts, offsets, slots, rows = new(T, k), new(E + 1), new(T, k), new(T * k)
         weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-        work = new(max(1, lib.sk_moe_route_work_bytes(T, E) // 4))
+        bytes_ = lib.sk_moe_route_work_bytes(T, E)
+        work = new(bytes_ // 4) if bytes_ else None
         _run("sk_moe_route", logits.data_ptr(), e, int(bool(normalize)), experts.data_ptr(), weights.data_ptr(),
-             offsets.data_ptr(), slots.data_ptr(), rows.data_ptr(), work.data_ptr(), T, E, k, _pg._stream(logits, None))
+             offsets.data_ptr(), slots.data_ptr(), rows.data_ptr(), _pg._ptr(work), T, E, k, _pg._stream(logits, None))
     return experts, weights, offsets, slots, rows
 
 
 def moe_route_backward(dweights, logits, experts, weights, *, normalize=True, stream=None):
     """The logits' gradient [T, E] (of the logits' type), given the gradient dweights (fp32 [T, k]) of moe_route's
     weights and its experts and weights."""
+    if stream is None:
+        got = (_pg._NATIVE or _pg._native()).moe_route_backward(dweights, logits, experts, weights, normalize)
+        if got.__class__ is not int and got is not None:
+            return got
+        if got is not None:
+            raise _pg.SkError(got, "sk_moe_route_backward")
     T, E = _dims(logits, "logits", 2)
     k = _dims(dweights, "dweights", 2)[1]
     with _on(logits, "logits", stream):
@@ -114,6 +127,12 @@ def moe_route_backward(dweights, logits, experts, weights, *, normalize=True, st
 def moe_combine(y, slots, weights=None, *, stream=None):
     """out[t] = sum over j of weights[t, j] * y[slots[t, j]]: y [R, D] (bf16, fp16 or fp32), slots int32 [T, k] (a slot
     outside of 0 to R - 1 is none), weights fp32 [T, k] or None for 1; returns out [T, D] of y's type."""
+    if stream is None:
+        got = (_pg._NATIVE or _pg._native()).moe_combine(y, slots, weights)
+        if got.__class__ is not int and got is not None:
+            return got
+        if got is not None:
+            raise _pg.SkError(got, "sk_moe_combine")
     R, D = _dims(y, "y", 2)
     T, k = _dims(slots, "slots", 2)
     with _on(y, "y", stream):
@@ -132,6 +151,12 @@ def moe_combine_backward(dout, y, slots, weights=None, *, offsets=None, stream=N
     """Gradients of moe_combine: (dy, dweights), dweights None without weights.  No two pairs may share a slot
     (moe_route's do not).  Rows of dy that no slot names are zeros; with moe_route's offsets, which say where those lie, only
     they are cleared and not all of dy first."""
+    if stream is None:
+        got = (_pg._NATIVE or _pg._native()).moe_combine_backward(dout, y, slots, weights, offsets)
+        if got.__class__ is not int and got is not None:
+            return got
+        if got is not None:
+            raise _pg.SkError(got, "sk_moe_combine_backward")
     R, D = _dims(y, "y", 2)
     T, k = _dims(slots, "slots", 2)
     with _on(y, "y", stream):
@@ -178,6 +203,12 @@ def gemm_grouped(A, B, offsets, bias=None, *, rows=None, out=None, stream=None):
 
     The group sizes are read on the device: the call neither waits for them nor depends on them otherwise.  Rows of C behind the
     last expert's are zeros, or in an `out` given by the caller are left as they were."""
+    if stream is None:
+        got = (_pg._NATIVE or _pg._native()).gemm_grouped(A, B, offsets, bias, rows, out)
+        if got.__class__ is not int and got is not None:
+            return got
+        if got is not None:
+            raise _pg.SkError(got, "sk_gemm_grouped")
     T, K = _dims(A, "A", 2)
     E, N, _ = _dims(B, "B", 3)
     with _on(A, "A", stream):
@@ -197,6 +228,12 @@ def gemm_grouped_backward(dC, A, B, offsets, *, rows=None, need_dA=True, need_dB
     """Gradients of gemm_grouped: (dA, dB, dbias), None where not asked for.  dC is [R, N] of A's type (N, too, a
     multiple of 8).  dA [R, K] has a row for each row of the product (zeros behind the last expert's): with rows,
     moe_combine(dA, slots) adds a token's up.  dB [E, N, K] and dbias [E, N] are zeros for an expert without rows."""
+    if stream is None:
+        got = (_pg._NATIVE or _pg._native()).gemm_grouped_backward(dC, A, B, offsets, rows, need_dA, need_dB, need_dbias)
+        if got.__class__ is not int and got is not None:
+            return got
+        if got is not None:
+            raise _pg.SkError(got, "sk_gemm_grouped_backward")
     T, K = _dims(A, "A", 2)
     E, N, _ = _dims(B, "B", 3)
     with _on(A, "A", stream):
@@ -227,6 +264,15 @@ def quantize_w4(w, group=128, *, zero=False, dtype=None, stream=None):
     fp16; None: w's own, bf16 for an fp32 w).  zero=False: scale = max|w| / 7 and codes around 8, None is returned
     for zero; zero=True: uint8 zero points [..., K / group, N], scale = (max(w, 0) - min(w, 0)) / 15.  A group that holds an
     infinity or a NaN has a NaN scale."""
+    if stream is None:
+        torch = _pg._torch()
+        half = dtype is torch.float16 or (dtype is None and getattr(w, "dtype", None) is torch.float16)
+        if half or dtype is None or dtype is torch.bfloat16:
+            got = (_pg._NATIVE or _pg._native()).quantize_w4(w, group, zero, half)
+            if got.__class__ is tuple:
+                return got
+            if got is not None:
+                raise _pg.SkError(got, "sk_quantize_w4")
     shape = _dims(w, "w", (2, 3))
     with _on(w, "w", stream):
         torch = _pg._torch()
@@ -263,6 +309,12 @@ def _codes(q, scale, zero, dev):
 
 def dequantize_w4(q, scale, zero=None, *, stream=None):
     """The values scale * (code - zero) of quantize_w4's outputs, of the scale's type: [N, K] or [E, N, K]."""
+    if stream is None:
+        got = (_pg._NATIVE or _pg._native()).dequantize_w4(q, scale, zero)
+        if got.__class__ is not int and got is not None:
+            return got
+        if got is not None:
+            raise _pg.SkError(got, "sk_dequantize_w4")
     with _on(q, "q", stream):
         torch = _pg._torch()
         lead, N, K, group = _codes(q, scale, zero, q.device)
@@ -281,6 +333,12 @@ def gemm_w4(x, q, scale, zero=None, bias=None, *, offsets=None, rows=None, out=N
     With offsets int32 [E + 1], as in gemm_grouped: q [E, N, K / 2], scale and zero [E, K / group, N], bias [E, N], and the rows of
     C by expert; rows int32 [R] chooses x's rows.  Rows of C behind the last expert's are zeros, or in an `out` given by the
     caller left as they were."""
+    if stream is None:
+        got = (_pg._NATIVE or _pg._native()).gemm_w4(x, q, scale, zero, bias, offsets, rows, out)
+        if got.__class__ is not int and got is not None:
+            return got
+        if got is not None:
+            raise _pg.SkError(got, "sk_gemm_w4")
     T, K = _dims(x, "x", 2)
     with _on(x, "x", stream):
         dev, e = x.device, _types(x, "x", full=False)

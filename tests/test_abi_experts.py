@@ -20,7 +20,7 @@ def _status(name, base, kw):
 
 
 ROUTE = dict(logits=P[0], elem=1, normalize=1, experts=P[1], weights=P[2], offsets=P[3], slots=P[4], rows=P[5], work=P[6],
-             T=8, E=16, k=2)
+             T=100, E=16, k=2)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -36,8 +36,8 @@ def test_route_checks(kw, status):
 
 def test_route_work_bytes():
     f = pg.load().sk_moe_route_work_bytes
-    assert f(1, 64) > 0 and f(0, 8) == 0 and f(8, 0) == 0 and f(8, 1025) == 0
-    for T in (1, 1000, 32768, 32769, 1 << 20, 123456789):
+    assert f(1, 64) == 0 and f(64, 64) == 0 and f(65, 64) > 0 and f(0, 8) == 0 and f(100, 0) == 0 and f(100, 1025) == 0
+    for T in (65, 1000, 32768, 32769, 1 << 20, 123456789):
         assert 0 < f(T, 16) <= 256 * 64          # at most 256 workgroups
 
 
