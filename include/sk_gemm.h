@@ -441,7 +441,7 @@ sk_status sk_dequantize_w4(const void* q, const void* scale, sk_elem scale_elem,
                            int64_t E, int64_t N, int64_t K, int64_t group, void* stream);
 
 /* C[m][n] = sum_k x[m][k] scale[k/group][n] (code[n][k] - zero[k/group][n]) + bias[n] for few rows (tokens being decoded;
- * beyond 64 the weight is read again for every 64): x [M][K], C [M][N] and scales bf16 or fp16, q and zero as above, fp32
+ * beyond 16 the weight is read again for every 16 or 32): x [M][K], C [M][N] and scales bf16 or fp16, q and zero as above, fp32
  * sums, one rounding.  With offsets (and rows) as in sk_gemm_grouped, M rows in E groups, each with a weight (and a bias) of its
  * own; without, E is 1 and T is M.  A row of x with an infinity or a NaN gives NaN.  x and q are 16-byte aligned. */
 sk_status sk_gemm_w4(const void* x, const void* q, const void* scale, const uint8_t* zero, sk_elem elem,

@@ -276,7 +276,7 @@ sk_status sk_quantize_w4(const void* w, sk_elem elem, void* q, void* scale, sk_e
   a.N = (int)N;
   a.K = (int)K;
   a.group = (int)group;
-  return ok(sk::launch_quantize_w4(a, elem, scale_elem == SK_ELEM_F16, (hipStream_t)stream));
+  return ok(sk::launch_quantize_w4(a, elem, scale_elem == SK_ELEM_F16, cus, (hipStream_t)stream));
 }
 
 sk_status sk_dequantize_w4(const void* q, const void* scale, sk_elem scale_elem, const uint8_t* zero, void* out,

@@ -377,11 +377,11 @@ struct CombineGradArgs {
 };
 hipError_t launch_combine_gradient(const CombineGradArgs& a, int elem, hipStream_t s);
 
-// Products of few rows with 4-bit or 16-bit weights (sk_rows.hip), one weight or one for each expert.
+// Products of few rows with 4-bit weights (sk_rows.hip), one weight or one for each expert.
 struct RowsGemm {
   const uint8_t* x;         // rows of K
-  const uint8_t* W;         // [E][N][K / 2] codes, or [E][N][K] 16-bit
-  const uint8_t* scale;     // [E][K / group][N] 16-bit, with codes
+  const uint8_t* W;         // [E][N][K / 2] codes
+  const uint8_t* scale;     // [E][K / group][N], 16-bit
   const uint8_t* zero;      // [E][K / group][N] or NULL
   const uint16_t* bias;     // [E][N] or NULL
   const int* offsets;       // [E + 1], or NULL: one weight for all R rows
@@ -390,9 +390,9 @@ struct RowsGemm {
   int E, R, N, K;
   int x_rows;
   int tail;                 // whether the rows behind the last expert's are written (zeros)
+  int lds;                  // bytes of LDS for x: set by the launcher
 };
 hipError_t launch_rows_w4(const RowsGemm& g, int group, bool f16, int cus, hipStream_t s);
-hipError_t launch_rows_16(const RowsGemm& g, bool f16, int cus, hipStream_t s);
 
 // 4-bit weights (sk_quantize4.hip).
 struct Quant4Args {
@@ -403,7 +403,7 @@ struct Quant4Args {
   void* out;                // dequantised: [rows][K]
   int E, N, K, group;
 };
-hipError_t launch_quantize_w4(const Quant4Args& a, int elem, bool scale_f16, hipStream_t s);
+hipError_t launch_quantize_w4(const Quant4Args& a, int elem, bool scale_f16, int cus, hipStream_t s);
 hipError_t launch_dequantize_w4(const Quant4Args& a, bool scale_f16, hipStream_t s);
 
 }  // namespace sk

@@ -27,11 +27,8 @@ template <class T>
 struct Vec8 {
   float v[8];
 };
-template <bool SHORT, class T>
-__device__ __forceinline__ Vec8<T> load8(const T* row, int col, int D) {
-  using R = std::conditional_t<sizeof(T) == 4, float, uint16_t>;
-  Raw8<R> r = load_raw8<SHORT>((const R*)row, col, D);
-  settle8<SHORT>(r, col, D);
+template <class T, class R>
+__device__ __forceinline__ Vec8<T> unpack8(const Raw8<R>& r) {
   Vec8<T> x;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -43,6 +40,13 @@ __device__ __forceinline__ Vec8<T> load8(const T* row, int col, int D) {
     }
   }
   return x;
+}
+template <bool SHORT, class T>
+__device__ __forceinline__ Vec8<T> load8(const T* row, int col, int D) {
+  using R = std::conditional_t<sizeof(T) == 4, float, uint16_t>;
+  Raw8<R> r = load_raw8<SHORT>((const R*)row, col, D);
+  settle8<SHORT>(r, col, D);
+  return unpack8<T>(r);
 }
 // Stores the first n of eight values, rounded to the element type.
 __device__ __forceinline__ void put8(BfElem* p, int n, const float (&x)[8]) { store8((uint16_t*)p, n, x); }

@@ -37,7 +37,7 @@ struct Bf16 {
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16(a, b); }
   static __device__ __forceinline__ float lo(uint32_t w) { return bf16_lo(w); }
   static __device__ __forceinline__ float hi(uint32_t w) { return bf16_hi(w); }
-  static constexpr uint32_t kOnes = 0x3f803f80u;
+  static constexpr uint32_t kOnes = 0x3f803f80u, kMinus16 = 0xc180c180u, kMinus24 = 0xc1c0c1c0u;
   // c plus both halves of w
   static __device__ __forceinline__ float add2(uint32_t w, float c) {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
@@ -57,7 +57,7 @@ struct Fp16 {
   }
   static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)w); }
   static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)); }
-  static constexpr uint32_t kOnes = 0x3c003c00u;
+  static constexpr uint32_t kOnes = 0x3c003c00u, kMinus16 = 0xcc00cc00u, kMinus24 = 0xce00ce00u;
   static __device__ __forceinline__ float add2(uint32_t w, float c) {
     typedef _Float16 h2 __attribute__((ext_vector_type(2)));
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, w), __builtin_bit_cast(h2, kOnes), c, false);

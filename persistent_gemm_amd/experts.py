@@ -327,8 +327,8 @@ def dequantize_w4(q, scale, zero=None, *, stream=None):
 
 def gemm_w4(x, q, scale, zero=None, bias=None, *, offsets=None, rows=None, out=None, stream=None):
     """C = x . W^T (+ bias) for few rows of x with the 4-bit weight W = scale * (code - zero) of quantize_w4: x [M, K],
-    scale, bias [N] and C [M, N] all bf16 or all fp16.  Sums are fp32; beyond 64 rows the weight is read again for
-    every 64 (then dequantize_w4 and an ordinary product are faster).
+    scale, bias [N] and C [M, N] all bf16 or all fp16.  Sums are fp32; beyond 16 rows the weight is read again for
+    every 16 or 32 (with hundreds, dequantize_w4 and an ordinary product are faster).
 
     With offsets int32 [E + 1], as in gemm_grouped: q [E, N, K / 2], scale and zero [E, K / group, N], bias [E, N], and the rows of
     C by expert; rows int32 [R] chooses x's rows.  Rows of C behind the last expert's are zeros, or in an `out` given by the
