@@ -410,7 +410,7 @@ sk_status sk_moe_combine_backward(const void* dout, const void* y, sk_elem elem,
  *   A [T][K]; rows int32 [R], or NULL (A's row r, T = R);  B [E][N][K];  offsets int32 [E+1], ascending from 0 to at most R;
  *   bias [E][N] or NULL;  C [R][N].  Rows of C behind offsets[E] become zeros where tail_zero != 0 and keep their values else.
  * K is a multiple of 8 (rows of whole 16 bytes), A and B are 16-byte aligned (SK_ERR_ALIGN); N is any.  SK_ERR_ARG: a NULL
- * pointer, a size < 1, E > 1024, R >= 2^31 - 2^20, N > 2^22, K > 2^21, with rows an A of 2 GiB or more, C over an input. */
+ * pointer, a size < 1, E > 1024, R >= 2^31 - 2^20, N > 2^22, K > 2^21, with rows an A of 2 GiB (less 4 KiB) or more, C over an input. */
 sk_status sk_gemm_grouped(const void* A, const void* B, sk_elem elem, const int32_t* offsets, const int32_t* rows,
                           const void* bias, void* C, int64_t R, int64_t T, int64_t E, int64_t N, int64_t K,
                           int tail_zero, void* stream);
@@ -443,7 +443,7 @@ sk_status sk_dequantize_w4(const void* q, const void* scale, sk_elem scale_elem,
 /* C[m][n] = sum_k x[m][k] scale[k/group][n] (code[n][k] - zero[k/group][n]) + bias[n] for few rows (tokens being decoded;
  * beyond 16 the weight is read again for every 16 or 32): x [M][K], C [M][N] and scales bf16 or fp16, q and zero as above, fp32
  * sums, one rounding.  With offsets (and rows) as in sk_gemm_grouped, M rows in E groups, each with a weight (and a bias) of its
- * own; without, E is 1 and T is M.  A row of x with an infinity or a NaN gives NaN.  x and q are 16-byte aligned. */
+ * own; without, E is 1, T is M and M at most 2^20.  A row of x with an infinity or a NaN gives NaN.  x and q are 16-byte aligned. */
 sk_status sk_gemm_w4(const void* x, const void* q, const void* scale, const uint8_t* zero, sk_elem elem,
                      const int32_t* offsets, const int32_t* rows, const void* bias, void* C, int64_t M, int64_t T,
                      int64_t E, int64_t N, int64_t K, int64_t group, int tail_zero, void* stream);

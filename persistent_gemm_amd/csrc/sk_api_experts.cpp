@@ -17,6 +17,10 @@ using sk::host::overlaps;
 
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - (1 << 20);   // (row indices step past the end in 32 bits)
 
+// Bytes of an A whose rows are chosen: lanes address it by 32-bit offsets, and those out of its range lie 2 GiB and up to a few
+// k-steps above the others.
+constexpr int64_t kMaxGathered = ((int64_t)1 << 31) - 4096;
+
 bool misaligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
 bool elem_ok(int e) { return e == SK_ELEM_BF16 || e == SK_ELEM_F16 || e == SK_ELEM_F32; }
 bool half_ok(int e) { return e == SK_ELEM_BF16 || e == SK_ELEM_F16; }
@@ -177,7 +181,7 @@ sk_status sk_gemm_grouped(const void* A, const void* B, sk_elem elem, const int3
   if (!within(R, kMaxRows - 1) || !within(T, kMaxRows - 1) || !within(E, sk::kMaxExperts) || !within(N, sk::kMaxN) ||
       !within(K, sk::kMaxK))
     return SK_ERR_ARG;
-  if (rows ? T * K * 2 >= (int64_t)1 << 31 : T != R) return SK_ERR_ARG;
+  if (rows ? T * K * 2 >= kMaxGathered : T != R) return SK_ERR_ARG;
   if (K % 8 || misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 2) || misaligned(bias, 2) ||
       misaligned(offsets, 4) || misaligned(rows, 4))
     return SK_ERR_ALIGN;
@@ -213,7 +217,7 @@ sk_status sk_gemm_grouped_backward(const void* dC, const void* A, const void* B,
   if (!within(R, kMaxRows - 1) || !within(T, kMaxRows - 1) || !within(E, sk::kMaxExperts) || !within(N, sk::kMaxK) ||
       !within(K, sk::kMaxK))
     return SK_ERR_ARG;
-  if (rows ? T * K * 2 >= (int64_t)1 << 31 : T != R) return SK_ERR_ARG;
+  if (rows ? T * K * 2 >= kMaxGathered : T != R) return SK_ERR_ARG;
   if (K % 8 || N % 8 || misaligned(dC, 16) || misaligned(A, 16) || misaligned(B, 16) || misaligned(dA, 2) ||
       misaligned(dB, 2) || misaligned(dbias, 2) || misaligned(offsets, 4) || misaligned(rows, 4))
     return SK_ERR_ALIGN;
@@ -311,7 +315,7 @@ sk_status sk_gemm_w4(const void* x, const void* q, const void* scale, const uint
   if (!within(M, kMaxRows - 1) || !within(T, kMaxRows - 1) || !within(E, sk::kMaxExperts) || !within(N, sk::kMaxN) ||
       !within(K, sk::kMaxK) || K % group)
     return SK_ERR_ARG;
-  if (offsets ? !rows && T != M : rows || E != 1 || T != M) return SK_ERR_ARG;
+  if (offsets ? !rows && T != M : rows || E != 1 || T != M || M > (1 << 20)) return SK_ERR_ARG;
   if (misaligned(x, 16) || misaligned(q, 16) || misaligned(scale, 2) || misaligned(C, 2) || misaligned(bias, 2) ||
       misaligned(offsets, 4) || misaligned(rows, 4))
     return SK_ERR_ALIGN;

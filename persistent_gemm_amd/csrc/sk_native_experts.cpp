@@ -35,6 +35,13 @@ int half_of(const Tensor& t) {
   return e == SK_ELEM_F32 ? -1 : e;
 }
 bool on_gpu(const Arg& a, int64_t dims) { return a.t && a.t->is_cuda() && a.t->dim() == dims; }
+// A truth value; false where it has none (a tensor of several elements, say), which the binding's own call then reports.
+bool truth(PyObject* o, bool* b) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) PyErr_Clear();
+  *b = t > 0;
+  return t >= 0;
+}
 // The current stream, or false.
 bool here(c10::Device dev, void** s) { return stream_of(Py_None, dev, s); }
 void* p(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -46,7 +53,9 @@ PyObject* route(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (n != 3 || !lib.route) return refuse();
     const Arg x(v[0]);
     if (!on_gpu(x, 2) || !PyLong_CheckExact(v[1])) return refuse();
-    const int e = elem_of(*x.t), normalize = PyObject_IsTrue(v[2]);
+    bool normalize;
+    if (!truth(v[2], &normalize)) return refuse();
+    const int e = elem_of(*x.t);
     const int64_t T = x.t->size(0), E = x.t->size(1), k = PyLong_AsLong(v[1]);
     const c10::Device dev = x.t->device();
     void* s;
@@ -70,7 +79,9 @@ PyObject* route_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (n != 5 || !lib.route_backward) return refuse();
     const Arg d(v[0]), x(v[1]), ids(v[2]), w(v[3]);
     if (!on_gpu(x, 2) || !on_gpu(d, 2) || !ids.t || !w.t) return refuse();
-    const int e = elem_of(*x.t), normalize = PyObject_IsTrue(v[4]);
+    bool normalize;
+    if (!truth(v[4], &normalize)) return refuse();
+    const int e = elem_of(*x.t);
     const int64_t T = x.t->size(0), E = x.t->size(1), k = d.t->size(1);
     const c10::Device dev = x.t->device();
     void* s;
@@ -164,9 +175,9 @@ PyObject* grouped_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t T = a.t->size(0), K = a.t->size(1), E = b.t->size(0), N = b.t->size(1);
     const c10::Device dev = a.t->device();
     const int64_t R = rows_of(o, rows, T, E, dev);
-    const bool wa = PyObject_IsTrue(v[5]), wb = PyObject_IsTrue(v[6]), ws = PyObject_IsTrue(v[7]);
+    bool wa, wb, ws;
     void* s;
-    if (e < 0 || R < 0 || !(wa || wb || ws) || !a.t->is_contiguous() || !is(*b.t, dev, ty, {E, N, K}) ||
+    if (!truth(v[5], &wa) || !truth(v[6], &wb) || !truth(v[7], &ws) || e < 0 || R < 0 || !(wa || wb || ws) || !a.t->is_contiguous() || !is(*b.t, dev, ty, {E, N, K}) ||
         !is(*d.t, dev, ty, {R, N}) || !here(dev, &s))
       return refuse();
     const Tensor da = wa ? make({R, K}, ty, dev) : Tensor(), db = wb ? make({E, N, K}, ty, dev) : Tensor(),
@@ -230,7 +241,9 @@ PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const Arg w(v[0]);
     if (!w.t || !w.t->is_cuda() || (w.t->dim() != 2 && w.t->dim() != 3) || !PyLong_CheckExact(v[1])) return refuse();
     const int e = elem_of(*w.t);
-    const bool lead = w.t->dim() == 3, half = PyObject_IsTrue(v[3]);
+    bool half, zeros;
+    if (!truth(v[2], &zeros) || !truth(v[3], &half)) return refuse();
+    const bool lead = w.t->dim() == 3;
     const int64_t E = lead ? w.t->size(0) : 1, N = w.t->size(-2), K = w.t->size(-1), group = PyLong_AsLong(v[1]);
     const c10::Device dev = w.t->device();
     void* s;
@@ -243,7 +256,7 @@ PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const Tensor q = lead ? make({E, N, K / 2}, kByte, dev) : make({N, K / 2}, kByte, dev);
     const Tensor scale = lead ? make({E, groups, N}, ty, dev) : make({groups, N}, ty, dev);
     Tensor zero;
-    if (PyObject_IsTrue(v[2])) zero = lead ? make({E, groups, N}, kByte, dev) : make({groups, N}, kByte, dev);
+    if (zeros) zero = lead ? make({E, groups, N}, kByte, dev) : make({groups, N}, kByte, dev);
     const sk_status r = lib.quantize(w.ptr(), (sk_elem)e, p(q), p(scale), half ? SK_ELEM_F16 : SK_ELEM_BF16, (uint8_t*)p(zero), E, N, K,
                                      group, s);
     return r == SK_OK ? pack({q, scale, zero}) : status(r);

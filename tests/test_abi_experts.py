@@ -85,7 +85,7 @@ GROUPED = dict(A=P[0], B=P[1], elem=0, offsets=P[2], rows=P[3], bias=P[4], C=P[5
     *[({n: None}, ARG) for n in ("A", "B", "offsets", "C")],
     (dict(elem=1), ARG), (dict(rows=None), ARG), (dict(R=0), ARG), (dict(T=0), ARG), (dict(E=0), ARG), (dict(E=1025), ARG), (dict(N=0), ARG),
     (dict(N=(1 << 22) + 1), ARG), (dict(K=(1 << 21) + 8), ARG), (dict(R=1 << 31), ARG),
-    (dict(T=1 << 20, K=1024), ARG),           # rows of an A of 2 GiB
+    (dict(T=1 << 20, K=1024), ARG), (dict(T=(1 << 20) - 2, K=1024), ARG),           # rows of an A of 2 GiB, and of 4 KiB less
     (dict(K=68), ALIGN), (dict(A=P[0] + 8), ALIGN), (dict(B=P[1] + 2), ALIGN), (dict(C=P[5] + 1), ALIGN), (dict(rows=P[3] + 2), ALIGN),
     (dict(C=P[0] + 16), ARG), (dict(C=P[3]), ARG), (dict(bias=P[5] + 8), ARG),
 ])
@@ -135,7 +135,8 @@ W4 = dict(x=P[0], q=P[1], scale=P[2], zero=P[3], elem=0, offsets=P[4], rows=P[5]
 @pytest.mark.parametrize("kw,status", [
     *[({n: None}, ARG) for n in ("x", "q", "scale", "C", "rows", "offsets")], (dict(elem=1), ARG), (dict(group=256), ARG), (dict(K=96), ARG),
     (dict(M=0), ARG), (dict(E=1025), ARG), (dict(offsets=None, rows=None, T=16), ARG),      # several experts without offsets
-    (dict(offsets=None, rows=None, E=1), ARG), (dict(x=P[0] + 8), ALIGN), (dict(q=P[1] + 8), ALIGN), (dict(C=P[7] + 1), ALIGN),
+    (dict(offsets=None, rows=None, E=1), ARG), (dict(offsets=None, rows=None, E=1, M=(1 << 20) + 1, T=(1 << 20) + 1), ARG),
+    (dict(x=P[0] + 8), ALIGN), (dict(q=P[1] + 8), ALIGN), (dict(C=P[7] + 1), ALIGN),
     (dict(C=P[0]), ARG), (dict(C=P[2] + 16), ARG), (dict(bias=P[7]), ARG),
 ])
 def test_w4_checks(kw, status):
