@@ -43,6 +43,14 @@ template <int L>
 __device__ __forceinline__ uint32_t max_of(uint32_t x) {
   return over_lanes<L>(x, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
+// Over the whole wave, in a scalar register: rows' maxima handed on from row to row, up to the last lane's.
+template <>
+__device__ __forceinline__ uint32_t max_of<64>(uint32_t x) {
+  x = max_of<16>(x);
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xa, 0xf, false));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xc, 0xf, false));
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
 template <int L>
 __device__ __forceinline__ float sum_of(float x) {
   return bits_f(over_lanes<L>(f_bits(x), [](uint32_t a, uint32_t b) { return f_bits(bits_f(a) + bits_f(b)); }));
@@ -212,22 +220,43 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t first, int n,
       kept[q] = 0u;
       which[q] = -1;
     }
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t most = max_of<L>(key[0]);
-      if (j == 0) top_key = most;
-      const int winner = __builtin_ctzll(__ballot(key[0] == most) >> group);            // the first lane of the token's
-      const int e = L == 64 ? __builtin_amdgcn_readlane(expert[0], winner) : __shfl(expert[0], group + winner);
-      const bool mine = l == winner;
+    if constexpr (L == 64) {
+      // A token to a wave: what is chosen is the same in all lanes, and a scalar.  The lane's experts
+      // are four bits each of `order`.
+      std::conditional_t<(V > 8), uint64_t, uint32_t> order = 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        key[v] = mine ? (v + 1 < V ? key[v + 1 < V ? v + 1 : 0] : 0u) : key[v];
-        expert[v] = mine && v + 1 < V ? expert[v + 1 < V ? v + 1 : 0] : expert[v];
+      for (int v = 0; v < V; ++v) order |= (decltype(order))(expert[v] & 15) << (4 * v);
+      static_assert(V <= 16 && KEPT == 1);
+      for (int j = 0; j < a.k; ++j) {
+        const uint32_t most = max_of<L>(key[0]);
+        if (j == 0) top_key = most;
+        const int winner = __builtin_ctzll(__ballot(key[0] == most));
+        const int e = winner * V + (__builtin_amdgcn_readlane((int)order, winner) & 15) % V;
+        const bool mine = l == winner;
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = mine ? (v + 1 < V ? key[v + 1 < V ? v + 1 : 0] : 0u) : key[v];
+        order = mine ? order >> 4 : order;
+        kept[0] = l == j ? most : kept[0];
+        which[0] = l == j ? (most ? e : -1) : which[0];
       }
+    } else {
+      for (int j = 0; j < a.k; ++j) {
+        const uint32_t most = max_of<L>(key[0]);
+        if (j == 0) top_key = most;
+        const int winner = __builtin_ctzll(__ballot(key[0] == most) >> group);            // the first lane of the token's
+        const int e = __shfl(expert[0], group + winner);
+        const bool mine = l == winner;
 #pragma unroll
-      for (int q = 0; q < KEPT; ++q) {
-        const bool here = j == q * L + l;
-        kept[q] = here ? most : kept[q];
-        which[q] = here && most ? e : which[q];
+        for (int v = 0; v < V; ++v) {
+          key[v] = mine ? (v + 1 < V ? key[v + 1 < V ? v + 1 : 0] : 0u) : key[v];
+          expert[v] = mine && v + 1 < V ? expert[v + 1 < V ? v + 1 : 0] : expert[v];
+        }
+#pragma unroll
+        for (int q = 0; q < KEPT; ++q) {
+          const bool here = j == q * L + l;
+          kept[q] = here ? most : kept[q];
+          which[q] = here && most ? e : which[q];
+        }
       }
     }
     const float top = value_of(top_key);
@@ -313,39 +342,40 @@ __global__ __launch_bounds__(kFewThreads) void sk_route_few(RouteArgs a) {
 }
 
 // dlogits = w (d - sum w d) at the chosen experts, or p (d - sum w d) at all of them (d 0 where not chosen).
-// (The choices are read by one lane each and handed round.)
+// (Choice j is read by lane j.)
 template <class T, int L, int V>
 __global__ __launch_bounds__(256) void sk_route_gradient(RouteGradArgs a) {
   constexpr int PER = 256 / L, KEPT = (kMaxChoices + L - 1) / L;
-  const int l = threadIdx.x % L, group = (threadIdx.x & 63) / L * L;
+  __shared__ __attribute__((aligned(16))) float rows[256 * V];
+  const int l = threadIdx.x % L;
+  float* const row = rows + threadIdx.x / L * (L * V);       // the token's experts
   const bool wide = a.E % V == 0 && (((uintptr_t)a.logits | (uintptr_t)a.dlogits) & (V * sizeof(T) - 1)) == 0;
   for (int64_t t = (int64_t)blockIdx.x * PER + threadIdx.x / L; t < a.T; t += (int64_t)gridDim.x * PER) {
-    float x[V], g[V], d[KEPT], mean = 0.0f;
+    float x[V], g[V], w[KEPT], d[KEPT], mean = 0.0f;
     int e[KEPT];
     if (!a.normalize) load_logits<T, V>((const T*)a.logits + t * a.E, l * V, a.E, wide, x);
 #pragma unroll
     for (int q = 0; q < KEPT; ++q) {
       const int j = q * L + l;
-      const bool in = j < a.k;
-      e[q] = in ? a.experts[t * a.k + j] : -1;
-      const float w = e[q] >= 0 ? a.weights[t * a.k + j] : 0.0f;
-      d[q] = e[q] >= 0 ? a.dweights[t * a.k + j] : 0.0f;
-      mean = __builtin_fmaf(w, d[q], mean);
+      const int64_t at = t * a.k + min(j, a.k - 1);      // (three loads that do not wait for one another)
+      const int id = a.experts[at];
+      w[q] = a.weights[at];
+      d[q] = a.dweights[at];
+      e[q] = j < a.k ? id : -1;
+      if (e[q] >= 0) mean = __builtin_fmaf(w[q], d[q], mean);
     }
     mean = sum_of<L>(mean);
+    // (zeros, and then the chosen experts', by way of LDS.  A wave's LDS accesses are done in their order.)
+#pragma unroll
+    for (int v = 0; v < V; ++v) row[l * V + v] = 0.0f;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
     for (int q = 0; q < KEPT; ++q)
-      if (a.normalize) d[q] = e[q] >= 0 ? a.weights[t * a.k + q * L + l] * (d[q] - mean) : 0.0f;
+      if ((uint32_t)e[q] < (uint32_t)a.E) row[e[q]] = a.normalize ? w[q] * (d[q] - mean) : d[q];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int v = 0; v < V; ++v) g[v] = 0.0f;
-#pragma unroll
-    for (int q = 0; q < KEPT; ++q)
-      for (int j = 0; j < min(L, a.k - q * L); ++j) {
-        const int at = __shfl(e[q], group + j);
-        const float y = __shfl(d[q], group + j);
-#pragma unroll
-        for (int v = 0; v < V; ++v) g[v] = at == l * V + v ? y : g[v];
-      }
+    for (int v = 0; v < V; ++v) g[v] = row[l * V + v];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (!a.normalize) {
       float top = x[0], total = 0.0f;
 #pragma unroll
