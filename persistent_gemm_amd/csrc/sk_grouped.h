@@ -24,15 +24,11 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef unsigned v2u_any __attribute__((ext_vector_type(2), aligned(2)));
 
-// The two element types: the matrix instruction, and rounding.  mfma_in_place: the sum in the accumulation registers that it
-// had.  Where 64 of them fill all 256, the compiler, which may give the result other registers, copies some in every k-step.  Its users
-// wait themselves before anything but such a product reads the sums (settle_sums).
+// The two element types: the matrix instruction, and rounding.  (16 x 16 x 32 products, whose rate under the power limit is 10 %
+// above that of 32 x 32 x 16 ones: 2094 against 1899 TFLOP/s on random operands.)
 struct Bf16 {
   static __device__ __forceinline__ v4f mfma(v4u b, v4u a, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, b), __builtin_bit_cast(v8bf, a), c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ void mfma_in_place(v4u b, v4u a, v4f& c) {
-    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
   }
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16(a, b); }
   static __device__ __forceinline__ float lo(uint32_t w) { return bf16_lo(w); }
@@ -48,9 +44,6 @@ struct Fp16 {
   static __device__ __forceinline__ v4f mfma(v4u b, v4u a, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, b), __builtin_bit_cast(v8h, a), c, 0, 0, 0);
   }
-  static __device__ __forceinline__ void mfma_in_place(v4u b, v4u a, v4f& c) {
-    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
-  }
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     typedef _Float16 h2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, (h2{(_Float16)a, (_Float16)b}));
@@ -63,9 +56,6 @@ struct Fp16 {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, w), __builtin_bit_cast(h2, kOnes), c, false);
   }
 };
-
-// The last products' results are in their registers (a 16 x 16 x 32 product needs 11 cycles' wait after its issue).
-__device__ __forceinline__ void settle_sums() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 enum GroupedKind { kForward = 0, kGradA = 1, kGradB = 2 };
 
@@ -268,7 +258,7 @@ struct GroupedPart {
 };
 
 // P is the operand of the output's rows, Q that of its columns.
-// SUMS: dB's tile also adds up its rows of dC (a branch in the k-steps would cost copies of the accumulators).
+// SUMS: dB's tile also adds up its rows of dC.
 template <class C, bool SUMS>
 __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const GroupedPart& part, lds_u8* const smem) {
   using T = typename C::T;
@@ -310,21 +300,18 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
   } else if constexpr (C::GATHER) {
     qr = rsrc_words(g.Q + n0 * 2, (uint32_t)g.q_rows * qp - (uint32_t)n0 * 2);
   }
-  // (gather, dB) the tokens of the wave's rows of a k-step, asked for one k-step ahead; -1 where there is no row.  (In scalar
-  // registers: a wait for a vector load would be one for the direct loads before it too.)
-  constexpr int TOK = C::KIND == kGradB && C::GATHER ? C::Q_PT * OpQ::RPU : 1;
-  int token[TOK], token_next[TOK];
-  auto tokens = [&](int s) {
-    const int b = s * 64 + wave * TOK;
-    const int* const from = g.rows + row0;
-    if (b + TOK <= rows) {
-#pragma unroll
-      for (int i = 0; i < TOK; ++i) token_next[i] = max(from[b + i], 0);
-    } else {
-#pragma unroll
-      for (int i = 0; i < TOK; ++i) token_next[i] = b + i < rows ? max(from[b + i], 0) : -1;
-    }
+  // (gather, dB) where the wave's TOK rows of each of AHEAD k-steps begin, one in each lane, out of range where there is no row.  The
+  // rows' indexes are asked for AHEAD k-steps before, since the wait for them is also one for all direct loads before it.  (Asked for in
+  // every k-step, as scalars, they made all waits for LDS reads wait for them: 8002 rows of 8 experts, 2048 x 4096, 170 us and not 145.)
+  constexpr int TOK = C::KIND == kGradB && C::GATHER ? C::Q_PT * OpQ::RPU : 1, AHEAD = 64 / TOK;
+  uint32_t held = 0;
+  int asked = 0;
+  auto row_at = [&](int s) { return (s + lane / TOK) * 64 + wave * TOK + lane % TOK; };
+  auto ask = [&](int s) {
+    const int b = row_at(s);
+    if (b < rows) asked = g.rows[row0 + b];
   };
+  auto take = [&](int s) { held = row_at(s) < rows ? (uint32_t)min(max(asked, 0), g.q_rows - 1) * qp : kOob; };
   // Rows of the k-step at s of a turned operand: `have` rows from `base` on.
   auto turned = [&](const uint8_t* base, uint32_t pitch, int col0, int have, int s) {
     // (said to be uniform: a value held to a range goes to vector registers otherwise)
@@ -354,9 +341,11 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
       qr = turned(g.Q + e_off * g.S * qp, qp, n0, g.S, s);
       kq = 0;
     } else if constexpr (C::KIND == kGradB && C::GATHER) {
-#pragma unroll
-      for (int i = 0; i < TOK; ++i) token[i] = token_next[i];
-      tokens(s + 1);
+      if (s > 0 && s % AHEAD == 0) {
+        take(s);
+        ask(s + AHEAD);
+      }
+      kq = (uint32_t)(s % AHEAD) * TOK;     // (here: the lane that holds the k-step's first row)
     } else if constexpr (C::KIND == kGradB) {
       qr = turned(g.Q + (uint64_t)row0 * qp, qp, n0, rows, s);
       kq = 0;
@@ -383,12 +372,11 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
     if constexpr (C::KIND == kGradB && C::GATHER) {
       // the wave's rows one behind the other: its load i has rows i RPU .. of them
       const int part = lane / (64 / OpQ::RPU), row = wave * TOK + i * OpQ::RPU + part;
-      int t = token[i * OpQ::RPU];
+      uint32_t from = (uint32_t)__builtin_amdgcn_readlane((int)held, (int)kq + i * OpQ::RPU);
 #pragma unroll
-      for (int j = 1; j < OpQ::RPU; ++j) t = part == j ? token[i * OpQ::RPU + j] : t;
+      for (int j = 1; j < OpQ::RPU; ++j) from = part == j ? (uint32_t)__builtin_amdgcn_readlane((int)held, (int)kq + i * OpQ::RPU + j) : from;
       const int chunk = (lane % (OpQ::ROW / 16)) ^ OpQ::swizzle(row);
-      dma16<(uint32_t)i * 1024u>(qr, t < 0 ? kOob : (uint32_t)min(t, g.q_rows - 1) * qp + (uint32_t)chunk * 16, 0u,
-                                 place + (uint32_t)wave * (C::Q_PT - 1) * 1024u);
+      dma16<(uint32_t)i * 1024u>(qr, from + (uint32_t)chunk * 16, 0u, place + (uint32_t)wave * (C::Q_PT - 1) * 1024u);
     } else if constexpr (i >= QV && v == 0) {
       dma16_next<at>(qr, qvoff[v], kq, qstep, place);
     } else {
@@ -411,9 +399,11 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{};
-  float sums[SUMS ? C::FM : 1];      // of row lr of each block, over the lane's part of the dimension summed over
+  // of row lr of every WN-th block (the waves of a row share them out), over the lane's part of the dimension summed over
+  constexpr int NSUM = SUMS ? (C::FM + C::WN - 1) / C::WN : 1;
+  float sums[NSUM];
 #pragma unroll
-  for (int i = 0; i < (SUMS ? C::FM : 1); ++i) sums[i] = 0.0f;
+  for (int i = 0; i < NSUM; ++i) sums[i] = 0.0f;
 
   v4u p[2][C::FM], q[2][C::FN];
   uint32_t lp, lq;
@@ -429,20 +419,18 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
     else q[h][n - C::FM] = OpQ::template read<h>(lq, n - C::FM);
   };
   // The reads beside a half's products are begun in its first three quarters, so that they are there at its end.  The direct
-  // loads are spread over the whole k-step: in a burst they hold up the wave that issues them (8192^3 of zeros 840 us with all of them
-  // in a quarter of the second half, 755 in three quarters of it).
+  // loads go behind the products of its first half with 8 waves (spread over all of it, 4148 rows of 16 experts, 2051 x
+  // 1288, took 48.5 us and not 46, in the second half 51), and are spread over all of it with 4.
   constexpr int NS = C::FM * C::FN, NR = C::FM + C::FN, NB = NS >= 8 ? NS * 3 / 4 : NS;
-  // behind which product load l of n goes: not the one behind which a read does, where there is room
-  constexpr auto place_of = [](int l, int n) { return NS >= 32 ? l * NS / n / 3 * 3 + 1 : l * NS / n; };
+  constexpr auto place_of = [](int l, int n) { return C::NW == 8 ? 1 + l * NS / n / 2 : l * NS / n; };      // behind which product load l of n goes
   using std::integral_constant;
-  constexpr bool FULL = C::FM * C::FN == 64;
-  auto product = [](v4f& c, const v4u& b, const v4u& a) {
-    if constexpr (FULL) T::mfma_in_place(b, a, c);
-    else c = T::mfma(b, a, c);
-  };
 
   if (steps > 0) {
-    if constexpr (C::KIND == kGradB && C::GATHER) tokens(0);
+    if constexpr (C::KIND == kGradB && C::GATHER) {
+      ask(0);
+      take(0);
+      ask(AHEAD);
+    }
     static_for<C::SLOTS - 1>([&](auto ic) {
       constexpr int i = decltype(ic)::value;
       aim(ic, i / 2);
@@ -464,7 +452,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
       aim(part1, s + (C::SLOTS - 1) / 2);
       static_for<NS>([&](auto nc) {
         constexpr int n = decltype(nc)::value, i = n % C::FM, j = n / C::FM;
-        product(acc[i][j], q[0][j], p[0][i]);
+        acc[i][j] = T::mfma(q[0][j], p[0][i], acc[i][j]);
         constexpr int R0 = n < NB ? n * NR / NB : NR, R1 = n < NB ? (n + 1) * NR / NB : NR;
         static_for<R1 - R0>([&](auto k) { read(integral_constant<int, 1>{}, integral_constant<int, R0 + decltype(k)::value>{}); });
         static_for<L1N>([&](auto l) {
@@ -472,13 +460,15 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
         });
         __builtin_amdgcn_sched_barrier(0);
       });
-      if constexpr (SUMS) {      // (on the ALU: the accumulators fill the registers that the MFMAs could add to)
+      if constexpr (SUMS) {      // (on the ALU: MFMAs of ones would cost an eighth more of them)
+        static_for<C::FM>([&](auto ic) {
+          constexpr int i = decltype(ic)::value;
+          if (wn == i % C::WN)
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) sums[i] = T::add2(p[h][i][c], sums[i]);
+              for (int c = 0; c < 4; ++c) sums[i / C::WN] = T::add2(p[h][i][c], sums[i / C::WN]);
+        });
       }
       // the next k-step has arrived and this one has been read: its two places are free
       wait_vmcnt_n<C::loads(4, C::SLOTS - 4)>();
@@ -491,7 +481,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
       aim(part0, s + C::SLOTS / 2);
       static_for<NS>([&](auto nc) {
         constexpr int n = decltype(nc)::value, i = n % C::FM, j = n / C::FM;
-        product(acc[i][j], q[1][j], p[1][i]);
+        acc[i][j] = T::mfma(q[1][j], p[1][i], acc[i][j]);
         constexpr int R0 = n < NB ? n * NR / NB : NR, R1 = n < NB ? (n + 1) * NR / NB : NR;
         static_for<R1 - R0>([&](auto k) { read(integral_constant<int, 0>{}, integral_constant<int, R0 + decltype(k)::value>{}); });
         static_for<L0N>([&](auto l) {
@@ -501,7 +491,6 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
       });
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if constexpr (FULL) settle_sums();
   }
 
   // ---- outputs: the lane has row lr and columns 4 lg .. + 3 of each 16 x 16 block.  Each wave turns 16 rows at a time into whole
@@ -556,17 +545,16 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
   }
-  if constexpr (SUMS)
-    if (wn == 0) {
+  if constexpr (SUMS) {
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i) {
-        float x = sums[i];
-        x += __shfl_xor(x, 16);
-        x += __shfl_xor(x, 32);
-        const int m = m0 + wm * C::WTM + i * 16 + lr;
-        if (lg == 0 && m < g.Mout) g.dbias[(uint64_t)e * g.Mout + m] = (uint16_t)T::pack(x, 0.0f);
-      }
+    for (int n = 0; n < NSUM; ++n) {
+      float x = sums[n];
+      x += __shfl_xor(x, 16);
+      x += __shfl_xor(x, 32);
+      const int i = n * C::WN + wn, m = m0 + wm * C::WTM + i * 16 + lr;
+      if (i < C::FM && lg == 0 && m < g.Mout) g.dbias[(uint64_t)e * g.Mout + m] = (uint16_t)T::pack(x, 0.0f);
     }
+  }
 }
 
 // C: the tiles; H and Q: their halves and quarters.
@@ -639,8 +627,11 @@ hipError_t launch_grouped_tiles(GroupedGemm g, int cus, hipStream_t s) {
 
 template <class T, int KIND, bool GATHER>
 hipError_t launch_grouped_kind(const GroupedGemm& g, int cus, hipStream_t s) {
-  using Big = GroupedCfg<T, KIND, GATHER, 256, 256, 2, 2, 5>;
-  using Half = GroupedCfg<T, KIND, GATHER, 256, 128, 2, 2, 5>;
+  // 8 waves, two to a SIMD, so that one's products hide the other's loads and reads: 4 waves of 128 x 128 each, which read a
+  // third less from LDS, took 164 us and not 159 for 4096 rows of 8 experts, 4096 x 4096, and their dB with gathered rows 232 and not 206.
+  using Big = GroupedCfg<T, KIND, GATHER, 256, 256, 2, 4, 5>;
+  using Half = GroupedCfg<T, KIND, GATHER, 256, 128, 2, 4, 5>;
+  using Quarter = GroupedCfg<T, KIND, GATHER, 128, 128, 2, 4, 5>;
   using Small = GroupedCfg<T, KIND, GATHER, 128, 128, 2, 2, 5>;
   if constexpr (KIND == kGradB) {
     // (smaller tiles read dC and A more often: 8 experts of 2048 x 4096, 8002 rows 139 us against 205 of 128 x 128)
@@ -650,7 +641,7 @@ hipError_t launch_grouped_kind(const GroupedGemm& g, int cus, hipStream_t s) {
     // 4096, 8 experts, 1024 rows 76 us against 85 of 128 x 128 and 512 rows 72 / 66; dA 65 / 83 and 63 / 57; 64 experts of 512 x
     // 1024 with 125 rows each 32 / 21.
     const int64_t big = ((int64_t)g.R / 256 + g.E / 2) * cdiv(g.Nout, 256);
-    if ((int64_t)g.R >= 128 * (int64_t)g.E && big * 2 >= cus) return launch_grouped_tiles<Big, Half, Small>(g, cus, s);
+    if ((int64_t)g.R >= 128 * (int64_t)g.E && big * 2 >= cus) return launch_grouped_tiles<Big, Half, Quarter>(g, cus, s);
     if constexpr (KIND == kForward) {
       // Tiles of 32 x 128, in which most rows are there, for up to 24 rows of an expert: 8 experts of 4096 x 4096, 8 rows 38 us
       // against 64 with any larger tile, 128 rows 62 / 64, 512 rows 84 / 66; 64 experts of 2048 x 1024 with 28 rows each 68 / 58.
