@@ -634,22 +634,29 @@ hipError_t launch_grouped_kind(const GroupedGemm& g, int cus, hipStream_t s) {
   using Quarter = GroupedCfg<T, KIND, GATHER, 128, 128, 2, 4, 5>;
   using Small = GroupedCfg<T, KIND, GATHER, 128, 128, 2, 2, 5>;
   if constexpr (KIND == kGradB) {
-    // (smaller tiles read dC and A more often: 8 experts of 2048 x 4096, 8002 rows 139 us against 205 of 128 x 128)
-    return launch_grouped_tiles<Big, Big, Big>(g, cus, s);
+    // Smaller tiles read dC and A more often (8 experts of 2048 x 4096, 8002 rows 138 us against 171 of 128 x 128), but are more where the
+    // large ones leave half of the units idle: 4 experts of 1024 x 1024, 400 rows 8.9 / 6.0 and 1600 rows 16.5 / 10.2; of 2048 x
+    // 2048, 800 rows 17.0 / 18.1.
+    if (g.E * (int64_t)cdiv(g.Mout, 256) * cdiv(g.Nout, 256) * 2 > cus) return launch_grouped_tiles<Big, Big, Big>(g, cus, s);
   } else {
+    // about how many tiles there are with `rows` rows
+    auto tiles = [&](int rows, int cols) { return ((int64_t)g.R / rows + g.E / 2) * cdiv(g.Nout, cols); };
     // Tiles of 256 x 256 where experts have 128 rows or more on the average and there are tiles for half of the units: 4096 x
-    // 4096, 8 experts, 1024 rows 76 us against 85 of 128 x 128 and 512 rows 72 / 66; dA 65 / 83 and 63 / 57; 64 experts of 512 x
-    // 1024 with 125 rows each 32 / 21.
-    const int64_t big = ((int64_t)g.R / 256 + g.E / 2) * cdiv(g.Nout, 256);
-    if ((int64_t)g.R >= 128 * (int64_t)g.E && big * 2 >= cus) return launch_grouped_tiles<Big, Half, Quarter>(g, cus, s);
-    if constexpr (KIND == kForward) {
-      // Tiles of 32 x 128, in which most rows are there, for up to 24 rows of an expert: 8 experts of 4096 x 4096, 8 rows 38 us
-      // against 64 with any larger tile, 128 rows 62 / 64, 512 rows 84 / 66; 64 experts of 2048 x 1024 with 28 rows each 68 / 58.
-      using Few = GroupedCfg<T, KIND, GATHER, 32, 128, 1, 4, 8>;
-      if ((int64_t)g.R <= 24 * (int64_t)g.E) return launch_grouped_tiles<Few, Few, Few>(g, cus, s);
-    }
-    return launch_grouped_tiles<Small, Small, Small>(g, cus, s);
+    // 4096, 8 experts, 1024 rows 74 us against 84 of 128 x 128 and 512 rows 71 / 66; dA 65 / 83 and 61 / 58; 64 experts of 512 x
+    // 1024 with 125 rows each 29 / 21.
+    if ((int64_t)g.R >= 128 * (int64_t)g.E && tiles(256, 256) * 2 >= cus) return launch_grouped_tiles<Big, Half, Quarter>(g, cus, s);
+    // Tiles of 32 x 128, in which most rows are there, for up to 24 rows of an expert: 8 experts of 4096 x 4096, 8 rows 38 us
+    // against 56 with 128 x 128, 256 rows 69 / 66, 512 rows 84 / 66; 64 experts of 2048 x 1024 with 28 rows each 68 / 59.  And where
+    // all of them run at once, since a k-step of one takes half the time: 4 experts of 1024 x 1024, 800 rows 8.3 us against 13.1,
+    // 1600 rows 14.9 / 13.7.
+    using Few = GroupedCfg<T, KIND, GATHER, 32, 128, 1, 4, 8>;
+    if ((int64_t)g.R <= 24 * (int64_t)g.E || tiles(32, 128) <= cus) return launch_grouped_tiles<Few, Few, Few>(g, cus, s);
+    // Of 64 x 128 by the same rule: 4 experts of 1024 x 1024, 1600 rows 10.6 us against 13.8 with 128 x 128, of 2048 x 2048, 800 rows
+    // 16.3 / 21.6 and 1200 rows 28.0 / 22.3.
+    using Mid = GroupedCfg<T, KIND, GATHER, 64, 128, 2, 2, 8>;
+    if (tiles(64, 128) <= cus) return launch_grouped_tiles<Mid, Mid, Mid>(g, cus, s);
   }
+  return launch_grouped_tiles<Small, Small, Small>(g, cus, s);
 }
 
 template <class T>

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import experts_ref as ref
+import test_gpu_experts as plain
 import persistent_gemm_amd as pg
 
 pytestmark = pytest.mark.gpu
@@ -60,6 +61,30 @@ def test_row_gradient_cut_tiles(counts, K):
         x, b = d[lo:hi].double().cpu(), B[e].double().cpu()
         want[lo:hi], mag[lo:hi] = x @ b, x.abs() @ b.abs()
     ref.assert_near(got, want, ref.rounding(want, HF) * 1.001 + mag * (N + 1) * ref.STEP32)
+
+
+# Each size of tile (rows x columns of the output; 256 units) in each direction, its ends within a tile.
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("counts,N,K", [
+    ([33, 0, 200, 7], 400, 136),                 # 32 x 128
+    ([1000, 0, 1061], 520, 264),                 # 64 x 128
+    ([1000, 63, 1500], 777, 136),                # 128 x 128
+    ([2, 40, 0, 90, 500, 31] * 6, 1100, 72),     # 128 x 128, more experts than full tiles
+    ([700, 300, 600], 4099, 200),                # 256 x 256, whole and cut
+])
+def test_forward_tiles(counts, N, K, dtype):
+    plain._check_grouped(counts, N, K, dtype, bias=True, gather=77, tail=3)
+    plain._check_grouped(counts, N, K, dtype)
+
+
+@pytest.mark.parametrize("gather", [0, 77])
+@pytest.mark.parametrize("counts,N,K,dtype", [
+    ([33, 0, 200, 7], 136, 400, BF), ([1000, 0, 1061], 264, 520, HF), ([1000, 63, 1500], 136, 776, BF),
+    ([2, 40, 0, 90, 500, 31] * 6, 72, 1096, HF), ([700, 300, 600], 200, 4104, BF),
+    ([300, 0, 513], 2056, 1544, BF), ([65, 1, 130], 1800, 2312, HF),        # dB in tiles of 256 x 256
+])
+def test_backward_tiles(counts, N, K, dtype, gather):
+    plain._check_grouped_backward(counts, N, K, dtype, gather=gather, tail=4)
 
 
 def test_not_finite_values_stay_in_their_rows():
