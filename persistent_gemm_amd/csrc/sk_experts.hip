@@ -286,8 +286,9 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t first, int n,
   }
 }
 
-// Many tokens: their choices, and counts by expert of each workgroup's, part [workgroup][E].  (One pass over 16384 x 256 logits; what
-// bounds it is the k maxima of each token.)
+// Many tokens: their choices, and counts by expert of each workgroup's, part [workgroup][E].  (16384 x 256
+// fp32 logits, 8 chosen: 17.7 us.  What bounds it is the issue of some 410 vector instructions a token, half of them for the
+// eight maxima; the logits are 16.8 MB, 3.4 us.)
 constexpr int kChooseThreads = 1024, kPlaceThreads = 1024, kFewThreads = 512;
 template <class T, int L, int V>
 __global__ __launch_bounds__(kChooseThreads) void sk_route_choose(RouteArgs a) {
@@ -301,6 +302,8 @@ __global__ __launch_bounds__(kChooseThreads) void sk_route_choose(RouteArgs a) {
 }
 
 // The places of the pairs of kPlaceBlocks workgroups of the first kernel; rows behind the last expert's belong to no token.
+// (131072 pairs of 256 experts 10.4 us: the latency of the counts, of the scan and of the pairs' two readings one after the other.  Every
+// workgroup adds up all counts itself, which takes less than a kernel between the two would.)
 __global__ __launch_bounds__(kPlaceThreads) void sk_route_place(RouteArgs a) {
   __shared__ PlaceShared<kPlaceThreads> sh;
   for (int e = threadIdx.x; e < a.E; e += kPlaceThreads) sh.all[e] = sh.before[e] = 0;
@@ -342,7 +345,8 @@ __global__ __launch_bounds__(kFewThreads) void sk_route_few(RouteArgs a) {
 }
 
 // dlogits = w (d - sum w d) at the chosen experts, or p (d - sum w d) at all of them (d 0 where not chosen).
-// (Choice j is read by lane j.)
+// (Choice j is read by lane j.  16384 x 256 fp32, 8 chosen: 8.1 us, of which 18 MB of traffic are 3.7; with the choices handed round the
+// wave and compared with each lane's experts 10.5.)
 template <class T, int L, int V>
 __global__ __launch_bounds__(256) void sk_route_gradient(RouteGradArgs a) {
   constexpr int PER = 256 / L, KEPT = (kMaxChoices + L - 1) / L;
@@ -414,6 +418,7 @@ __global__ __launch_bounds__(256) void sk_route_gradient(RouteGradArgs a) {
 // ---------------------------------------------------------------- the weighted sum
 
 // out[t] = sum_j w[t][j] y[slots[t][j]], eight columns to a thread, fp32 sums in the order of j.
+// (8192 x 2 x 4096 bf16 36.5 us, 5.5 TB/s: bound by memory.)
 template <class T, bool SHORT>
 __global__ __launch_bounds__(256) void sk_combine(CombineArgs a) {
   const int per_row = (a.D + 7) / 8;
@@ -434,6 +439,7 @@ __global__ __launch_bounds__(256) void sk_combine(CombineArgs a) {
 }
 
 // A wave to a pair: dy[slot] = w dout[t] and dweights = <dout[t], y[slot]>.  Rows behind the last expert's are zeros.
+// (1037 x 4 x 2051 bf16 8.3 us, of which 38 MB of traffic are 7.5.)
 template <class T, bool SHORT>
 __global__ __launch_bounds__(256) void sk_combine_gradient(CombineGradArgs a) {
   const int lane = threadIdx.x & 63;
