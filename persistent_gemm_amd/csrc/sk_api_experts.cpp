@@ -53,7 +53,7 @@ bool route_sizes_ok(int64_t T, int64_t E, int64_t k) {
 extern "C" {
 
 int64_t sk_moe_route_work_bytes(int64_t T, int64_t E) {
-  return within(T, kMaxRows) && within(E, sk::kMaxExperts) ? sk::route_blocks(T) * E * 4 : 0;
+  return within(T, kMaxRows) && within(E, sk::kMaxExperts) ? sk::route_blocks(T, (int)E) * E * 4 : 0;
 }
 
 sk_status sk_moe_route(const void* logits, sk_elem elem, int normalize, int32_t* experts, float* weights,

@@ -333,13 +333,13 @@ struct RouteArgs {
   int* offsets;             // [E + 1]
   int* slots;               // [T][k], -1 likewise
   int* rows;                // [T k]: the token of each row, -1 behind the last expert's
-  int* part;                // [route_blocks(T)][E]
+  int* part;                // [route_blocks(T, E)][E]
   int64_t T;
   int E, k;
   int normalize;
   int per_block, blocks;    // tokens of a workgroup, and workgroups: set by the launcher
 };
-int64_t route_blocks(int64_t T);
+int64_t route_blocks(int64_t T, int E);
 hipError_t launch_route(RouteArgs a, int elem, hipStream_t s);
 
 struct RouteGradArgs {

@@ -207,7 +207,9 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t first, int n,
       for (int v = 0; v < V - 1 - round; ++v) {
         const bool swap = key[v + 1] > key[v];
         const uint32_t hi = max(key[v], key[v + 1]), lo = min(key[v], key[v + 1]);
-        const int e0 = swap ? expert[v + 1] : expert[v], e1 = swap ? expert[v] : expert[v + 1];
+        int above = expert[v + 1], own = expert[v];
+        asm volatile("" : "+v"(above), "+v"(own));       // (else the choice of two elements becomes one by an index, several of them for each)
+        const int e0 = swap ? above : own, e1 = swap ? own : above;
         key[v] = hi;
         key[v + 1] = lo;
         expert[v] = e0;
@@ -220,43 +222,33 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t first, int n,
       kept[q] = 0u;
       which[q] = -1;
     }
-    if constexpr (L == 64) {
-      // A token to a wave: what is chosen is the same in all lanes, and a scalar.  The lane's experts
-      // are four bits each of `order`.
-      std::conditional_t<(V > 8), uint64_t, uint32_t> order = 0;
+    // the lane's experts in the order of their keys, four bits each
+    std::conditional_t<(V > 8), uint64_t, uint32_t> order = 0;
+    static_assert(V <= 16);
 #pragma unroll
-      for (int v = 0; v < V; ++v) order |= (decltype(order))(expert[v] & 15) << (4 * v);
-      static_assert(V <= 16 && KEPT == 1);
-      for (int j = 0; j < a.k; ++j) {
-        const uint32_t most = max_of<L>(key[0]);
-        if (j == 0) top_key = most;
-        const int winner = __builtin_ctzll(__ballot(key[0] == most));
-        const int e = winner * V + (__builtin_amdgcn_readlane((int)order, winner) & 15) % V;
-        const bool mine = l == winner;
+    for (int v = 0; v < V; ++v) order |= (decltype(order))(expert[v] & 15) << (4 * v);
+    for (int j = 0; j < a.k; ++j) {
+      // (with a token to a wave all of this is the same in all lanes, and scalar)
+      const uint32_t most = max_of<L>(key[0]);
+      if (j == 0) top_key = most;
+      const int winner = __builtin_ctzll(__ballot(key[0] == most) >> group);            // the first lane of the token's
+      const int of = L == 64 ? __builtin_amdgcn_readlane((int)order, winner) : __shfl((int)order, group + winner);
+      const int e = winner * V + (of & 15) % V;
+      const bool mine = l == winner;
+      uint32_t above = 0u;
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = mine ? (v + 1 < V ? key[v + 1 < V ? v + 1 : 0] : 0u) : key[v];
-        order = mine ? order >> 4 : order;
-        kept[0] = l == j ? most : kept[0];
-        which[0] = l == j ? (most ? e : -1) : which[0];
+      for (int v = V - 1; v >= 0; --v) {
+        const uint32_t own = key[v];
+        asm volatile("" : "+v"(above));       // (as in the sort)
+        key[v] = mine ? above : own;
+        above = own;
       }
-    } else {
-      for (int j = 0; j < a.k; ++j) {
-        const uint32_t most = max_of<L>(key[0]);
-        if (j == 0) top_key = most;
-        const int winner = __builtin_ctzll(__ballot(key[0] == most) >> group);            // the first lane of the token's
-        const int e = __shfl(expert[0], group + winner);
-        const bool mine = l == winner;
+      order = mine ? order >> 4 : order;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          key[v] = mine ? (v + 1 < V ? key[v + 1 < V ? v + 1 : 0] : 0u) : key[v];
-          expert[v] = mine && v + 1 < V ? expert[v + 1 < V ? v + 1 : 0] : expert[v];
-        }
-#pragma unroll
-        for (int q = 0; q < KEPT; ++q) {
-          const bool here = j == q * L + l;
-          kept[q] = here ? most : kept[q];
-          which[q] = here && most ? e : which[q];
-        }
+      for (int q = 0; q < KEPT; ++q) {
+        const bool here = j == q * L + l;
+        kept[q] = here ? most : kept[q];
+        which[q] = here ? (most ? e : -1) : which[q];
       }
     }
     const float top = value_of(top_key);
@@ -287,7 +279,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t first, int n,
 }
 
 // Many tokens: their choices, and counts by expert of each workgroup's, part [workgroup][E].  (16384 x 256
-// fp32 logits, 8 chosen: 17.7 us.  What bounds it is the issue of some 410 vector instructions a token, half of them for the
+// fp32 logits, 8 chosen: 14.0 us.  What bounds it is the issue of some 350 vector instructions a token, half of them for the
 // eight maxima; the logits are 16.8 MB, 3.4 us.)
 constexpr int kChooseThreads = 1024, kPlaceThreads = 1024, kFewThreads = 512;
 template <class T, int L, int V>
@@ -507,21 +499,28 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Tokens of a workgroup: 64, and more where there would be over 256 workgroups, whose counts are all read by a quarter as many.
-int route_per_block(int64_t T) { return (int)(cdiv64(cdiv64(T, 256), 64) * 64); }
+// Tokens that one workgroup chooses for and places: two turns of its lanes.
+int64_t few_tokens(int E) { return E <= 64 ? kFewTokens : E <= 128 ? kFewTokens / 2 : kFewTokens / 4; }
+// Tokens of a workgroup of the first kernel: no more than its waves take at once, and more where there would be over 256 workgroups,
+// whose counts are all read by a quarter as many.  (1024 tokens of 256 experts, both kernels, 11.4 us with 16 and 21.4 with 64; of 8
+// 8.8 / 8.1.)
+int route_per_block(int64_t T, int E) {
+  const int least = E <= 32 ? 64 : 16;
+  return (int)(cdiv64(cdiv64(T, 256), least) * least);
+}
 // (none where one workgroup does it all)
-int64_t route_blocks(int64_t T) { return T <= kFewTokens ? 0 : cdiv64(T, route_per_block(T)); }
+int64_t route_blocks(int64_t T, int E) { return T <= few_tokens(E) ? 0 : cdiv64(T, route_per_block(T, E)); }
 
 hipError_t launch_route(RouteArgs a, int elem, hipStream_t s) {
   // one workgroup for few tokens: 1 token of 64 experts 4.2 us on the device against 7.0 as two kernels
-  if (a.T <= kFewTokens)
+  if (a.T <= few_tokens(a.E))
     return by_elem(elem, [&](auto t) {
       return by_experts(a.E, [&](auto l, auto v) {
         return launch(sk_route_few<decltype(t), decltype(l)::value, decltype(v)::value>, dim3(1), kFewThreads, s, a);
       });
     });
-  a.per_block = route_per_block(a.T);
-  a.blocks = (int)route_blocks(a.T);
+  a.per_block = route_per_block(a.T, a.E);
+  a.blocks = (int)route_blocks(a.T, a.E);
   const hipError_t e = by_elem(elem, [&](auto t) {
     return by_experts(a.E, [&](auto l, auto v) {
       return launch(sk_route_choose<decltype(t), decltype(l)::value, decltype(v)::value>, dim3((unsigned)a.blocks), kChooseThreads, s, a);

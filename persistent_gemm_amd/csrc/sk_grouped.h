@@ -233,9 +233,9 @@ __device__ __forceinline__ bool find_tile(const GroupedGemm& g, int t, GroupTile
   const int rows = max(1, min(BAND, tm_e - band * BAND));
   const int tn = at / rows, tm = band * BAND + (at - tn * rows);
   out->row0 = __builtin_amdgcn_readfirstlane(a + tm * BM);
-  out->rows = __builtin_amdgcn_readfirstlane(max(0, min(BM, b - a - tm * BM)));
+  out->rows = __builtin_amdgcn_readfirstlane(min(BM, b - a - tm * BM));
   out->tn = __builtin_amdgcn_readfirstlane(tn);
-  return out->rows > 0 && tn < tiles_n;
+  return in >= 0 && tm < tm_e && tn < tiles_n;      // (always, unless wrong offsets make the numbers of tiles pass 32 bits)
 }
 
 // Four outputs of a row from column n on, of which those below N are stored.
