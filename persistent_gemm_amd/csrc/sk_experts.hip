@@ -9,7 +9,7 @@ namespace {
 
 // ---------------------------------------------------------------- the choice
 
-constexpr int kFewTokens = 64, kPlaceBlocks = 4;
+constexpr int kFewTokens = 64, kPlaceBlocks = 2;
 
 // A logit as an integer that orders like it, 0 where it cannot be chosen (-inf, NaN).  (-0 is 0.)
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(kChooseThreads) void sk_route_choose(RouteArgs a) {
 }
 
 // The places of the pairs of kPlaceBlocks workgroups of the first kernel; rows behind the last expert's belong to no token.
-// (131072 pairs of 256 experts 10.4 us: the latency of the counts, of the scan and of the pairs' two readings one after the other.  Every
+// (131072 pairs of 256 experts 9.6 us: the latency of the counts, of the scan and of the pairs' two readings one after the other.  Every
 // workgroup adds up all counts itself, which takes less than a kernel between the two would.)
 __global__ __launch_bounds__(kPlaceThreads) void sk_route_place(RouteArgs a) {
   __shared__ PlaceShared<kPlaceThreads> sh;
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(kPlaceThreads) void sk_route_place(RouteArgs a) {
   const int own = (int)blockIdx.x * kPlaceBlocks;
   for (int e = threadIdx.x % lanes; e < a.E; e += lanes) {
     int all = 0, before = 0;
-#pragma unroll 16
+#pragma unroll 8
     for (int b = b0; b < a.blocks; b += share) {
       const int c = a.part[(int64_t)b * a.E + e];
       all += c;
@@ -499,10 +499,11 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Tokens that one workgroup chooses for and places: two turns of its lanes.
+// Tokens that one workgroup chooses for and places: two turns of its lanes.  (64 of 64 experts 6.0 us and 65 as two kernels 7.8, 32 and 33
+// of 128 6.6 / 7.9, 16 and 17 of 256 6.1 / 7.8.)
 int64_t few_tokens(int E) { return E <= 64 ? kFewTokens : E <= 128 ? kFewTokens / 2 : kFewTokens / 4; }
 // Tokens of a workgroup of the first kernel: no more than its waves take at once, and more where there would be over 256 workgroups,
-// whose counts are all read by a quarter as many.  (1024 tokens of 256 experts, both kernels, 11.4 us with 16 and 21.4 with 64; of 8
+// whose counts are all read by half as many.  (1024 tokens of 256 experts, both kernels, 11.4 us with 16 and 21.4 with 64; of 8
 // 8.8 / 8.1.)
 int route_per_block(int64_t T, int E) {
   const int least = E <= 32 ? 64 : 16;
