@@ -77,6 +77,14 @@ __global__ __launch_bounds__(256) void sk_quantize4(Quant4Args a) {
         mag = max(mag, (uint32_t)__shfl_xor((int)mag, d));
       }
       float s = ZERO ? (hi - lo) / 15.0f : bits_f(mag) / 7.0f;
+      if constexpr (ZERO && !std::is_same_v<T, _Float16>) {
+        // A difference beyond fp32, whose scale is not: of halves.  (A branch that the wave hardly ever takes; as a choice between the
+        // two 8192 x 8192 bf16 took 38.8 us and not 37.6.)
+        if (__builtin_expect(__ballot(s == __builtin_inff()) != 0, 0)) {
+          const float half = (0.5f * hi - 0.5f * lo) / 15.0f;
+          s = s == __builtin_inff() ? 2.0f * half : s;
+        }
+      }
       S stored;
       store_elem(&stored, s);
       s = fmaxf(load_elem(&stored), tiny);
