@@ -33,7 +33,7 @@ struct Bf16 {
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16(a, b); }
   static __device__ __forceinline__ float lo(uint32_t w) { return bf16_lo(w); }
   static __device__ __forceinline__ float hi(uint32_t w) { return bf16_hi(w); }
-  static constexpr uint32_t kOnes = 0x3f803f80u, kMinus16 = 0xc180c180u, kMinus24 = 0xc1c0c1c0u;
+  static constexpr uint32_t kOnes = 0x3f803f80u, kMinus16 = 0xbb80bb80u, kMinus24 = 0xbbc0bbc0u;      // (by 2^-12: sk_rows.hip)
   // c plus both halves of w
   static __device__ __forceinline__ float add2(uint32_t w, float c) {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));

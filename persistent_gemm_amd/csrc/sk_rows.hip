@@ -5,7 +5,10 @@
 //
 // 16 + q is what four code bits become with one mask in a 16-bit float of exponent 4, exactly, so a pair of codes costs
 // a shift and an and-or.  A group's inner sum is MFMAs' (16 rows of W by 16 of x, 32 of K), and so is the sum of x, with
-// -16 or -24 in place of W: what the inner sum starts from (other zero points are taken off it).  The offset of 16 costs little precision: the terms are about five times the exact ones, in fp32.
+// -16 or -24 in place of W: what the inner sum starts from (other zero points are taken off it).  The offset of 16 costs little
+// precision: the terms are about five times the exact ones, in fp32.  bf16 has fp32's range, so that 128 times 31 x would pass it for
+// x above 2^116: there the float has exponent -8, all sums are 2^-12 of the formula's (128 x 31 < 2^12), and the output's sum is
+// multiplied by 2^12.  (Powers of two: the same bits as without, but for sums below 2^-114, whose smallest step is 2^-137.)
 //
 // A workgroup takes 16 FN rows of W; its waves share out K in steps of 128 in turn, so that together they read whole
 // stretches of a row, straight to registers and D steps ahead.  x lies in LDS, its elements in the order that the codes come in
@@ -39,13 +42,13 @@ __device__ __forceinline__ void transpose4(v4u& a) {
   a = v4u{w[0], w[1], w[2], w[3]};
 }
 
-// Eight codes as 16 + q in 16-bit floats, pairs (i, i + 4).  (`base` in a vector register and the mask in a scalar one: with two
+// Eight codes as 16 + q, by 2^-12 in bf16, in 16-bit floats, pairs (i, i + 4).  (`base` in a vector register and the mask in a scalar one: with two
 // constants an and and an or would not be one instruction.)
 template <class T>
 struct Decode {
   static constexpr bool BF = std::is_same_v<T, Bf16>;
   static constexpr int at = BF ? 3 : 6;         // where the code's bits go
-  uint32_t mask = BF ? 0x00780078u : 0x03c003c0u, base = BF ? 0x41804180u : 0x4c004c00u;
+  uint32_t mask = BF ? 0x00780078u : 0x03c003c0u, base = BF ? 0x3b803b80u : 0x4c004c00u;
   __device__ __forceinline__ Decode() { asm volatile("" : "+s"(mask), "+v"(base)); }
   __device__ __forceinline__ v4u operator()(uint32_t d) const {
     return v4u{(d << at & mask) | base, ((at >= 4 ? d << (at - 4) : d >> (4 - at)) & mask) | base,
@@ -213,7 +216,8 @@ __global__ __launch_bounds__(64 * NWK, MT == 1 ? 4 : 2) void sk_rows(RowsGemm g)
                                     (uint32_t)((s - first) * 16 + ((4 * u + lg) ^ (m < rows ? m & 15 : 0))) * 16u;
                 x[i][u] = *(const __attribute__((address_space(3))) v4u*)(uintptr_t)(smem + at);
               }
-            // -16 times x's sum over a group (-24 times without zero points), the same in all four: what its products start from
+            // -16 times x's sum over a group (-24 times without zero points; by 2^-12 in bf16), the same in all four: what its
+            // products start from
             constexpr uint32_t by = ZERO ? T::kMinus16 : T::kMinus24;
             const v4u minus{by, by, by, by};
             v4f sum[NG][MT];
@@ -225,7 +229,7 @@ __global__ __launch_bounds__(64 * NWK, MT == 1 ? 4 : 2) void sk_rows(RowsGemm g)
 #pragma unroll
                 for (int u = 0; u < PER; ++u) sum[h][i] = T::mfma(minus, x[i][h * PER + u], sum[h][i]);
               }
-            float less[NG][MT];     // -x's sum
+            float less[NG][MT];     // -x's sum (by 2^-12 in bf16)
 #pragma unroll
             for (int h = 0; h < NG; ++h)
 #pragma unroll
@@ -272,6 +276,7 @@ __global__ __launch_bounds__(64 * NWK, MT == 1 ? 4 : 2) void sk_rows(RowsGemm g)
       v4f y = *red(0, b);
 #pragma unroll
       for (int w = 1; w < NWK; ++w) y += *red(w, b);
+      if constexpr (Decode<T>::BF) y *= 0x1p12f;
       const int n = n0 + (b / MT) * 16 + 4 * lg, m = m0 + (b % MT) * 16 + lr;
       if (g.bias) {
 #pragma unroll
