@@ -31,6 +31,13 @@ def _on(t, name, stream):
     return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
+def _integer(v, name):
+    n = int(v)
+    if n != v:
+        raise ValueError(f"{name} is {v!r}, expected a whole number")
+    return n
+
+
 def _types(t, name, full=True):
     """SK_ELEM_* of a tensor."""
     torch = _pg._torch()
@@ -82,12 +89,12 @@ def moe_route(logits, k, *, normalize=True, stream=None):
         if got is not None:
             raise _pg.SkError(got, "sk_moe_route")
     T, E = _dims(logits, "logits", 2)
+    k = _integer(k, "k")
     with _on(logits, "logits", stream):
         torch = _pg._torch()
         dev, e = logits.device, _types(logits, "logits")
         _pg._need(logits, "logits", (logits.dtype,), (T, E), dev)
         lib = _pg.load()
-        k = int(k)
         if not 1 <= k <= 32 or k > E:
             raise ValueError(f"k is {k}, expected 1 to {min(E, 32)}")
         new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)      # noqa: E731
@@ -274,6 +281,7 @@ def quantize_w4(w, group=128, *, zero=False, dtype=None, stream=None):
             if got is not None:
                 raise _pg.SkError(got, "sk_quantize_w4")
     shape = _dims(w, "w", (2, 3))
+    group = _integer(group, "group")
     with _on(w, "w", stream):
         torch = _pg._torch()
         dev, e = w.device, _types(w, "w")
@@ -283,7 +291,6 @@ def quantize_w4(w, group=128, *, zero=False, dtype=None, stream=None):
         if dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"dtype is {dtype}, expected bfloat16 or float16")
         lead, (N, K) = tuple(shape[:-2]), shape[-2:]
-        group = int(group)
         if group not in (32, 64, 128) or K % group:
             raise ValueError(f"group is {group}, expected 32, 64 or 128 and a divisor of {K}")
         q = torch.empty((*lead, N, K // 2), dtype=torch.uint8, device=dev)
