@@ -27,6 +27,8 @@ def _on(t, name, stream):
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(_pg._handle(stream), device=t.device)
+        elif stream.device != t.device:
+            raise ValueError(f"stream is of {stream.device}, {name} on {t.device}")
         return torch.cuda.stream(stream)
     return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 

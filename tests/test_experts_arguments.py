@@ -24,3 +24,26 @@ def test_sizes_are_whole_numbers(bad):
     for whole in (64, 64.0):
         with pytest.raises(ValueError, match="expected a GPU"):
             pg.quantize_w4(torch.zeros(4, 128), whole)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Its kernels would run there on tensors that are here."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    import persistent_gemm_amd.experts as experts
+
+    class Stream:
+        def __init__(self, index):
+            self.device, self.cuda_stream = torch.device("cuda", index), 0
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    with FakeTensorMode():
+        x = torch.empty(4, 8, device="cuda:0")
+        for stream in (Stream(1), Stream(7)):
+            with pytest.raises(ValueError, match="stream is of cuda"):
+                experts._on(x, "x", stream)
+            for call in (lambda: pg.moe_route(x, 2, stream=stream), lambda: pg.moe_combine(x, x, stream=stream),
+                         lambda: pg.quantize_w4(x, 32, stream=stream), lambda: pg.gemm_grouped(x, x[None], x, stream=stream)):
+                with pytest.raises(ValueError, match="stream is of cuda"):
+                    call()
+        experts._on(x, "x", Stream(0))
