@@ -109,13 +109,10 @@ struct Operand {
   static constexpr int PERIOD = 16;                                // rows
   static constexpr int ALIKE = NW * RPU % PERIOD == 0 ? 1 : PERIOD / (NW * RPU);
   static_assert(PERIOD % (NW * RPU) == 0 || NW * RPU % PERIOD == 0, "whole periods");
-  static_assert(!TURN || (BX >= 64 && BX <= 256), "the permutation below");
+  static_assert(!TURN || BX == 128 || BX == 256, "the permutation below");
 
   // The permutation of a turned operand's row, in 16-byte chunks.
-  static __device__ __forceinline__ int swizzle(int row) {
-    if constexpr (BX == 64) return 2 * (((row >> 1) & 1) | ((row >> 3) & 1) << 1);
-    else return 2 * ((row & 3) | ((row >> 3) & 1) << 2);
-  }
+  static __device__ __forceinline__ int swizzle(int row) { return 2 * ((row & 3) | ((row >> 3) & 1) << 2); }
   // Load i of wave w: the lane's row, and its chunk of that row.
   static __device__ __forceinline__ int row_of(int w, int i, int lane) { return (w + i * NW) * RPU + lane / (64 / RPU); }
   static __device__ __forceinline__ int chunk_of(int w, int i, int lane) {
@@ -505,7 +502,8 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
     int ln = lane;      // (a copy whose uses cannot move ahead of the k-steps, where there are no registers for them)
     asm volatile("" : "+v"(ln));
     const int lr = ln & 15, lg = ln >> 4;
-    auto turn = [](int row) { return CH == 16 ? row : CH == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };   // of a row's chunks, for the banks
+    static_assert(CH == 8 || CH == 4, "the permutation below");
+    auto turn = [](int row) { return CH == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };   // of a row's chunks, for the banks
     const uint32_t area = ring + (uint32_t)wave * 16 * C::WTN * 2;
     const int nw = n0 + wn * C::WTN;
     float b[C::FN][4];
