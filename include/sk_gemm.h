@@ -366,7 +366,11 @@ sk_status sk_norm_backward(const sk_norm_grad_args* args);
  *
  * None of these calls uses scratch of the library, so all of them may be captured into a HIP graph, and calls of
  * several host threads or streams do not meet.  Offsets, slots and row indexes are device data that the host does not
- * see: kernels hold each to its range, so that wrong ones give wrong rows and no access out of bounds. */
+ * see: kernels hold each to its range, so that wrong ones give wrong rows and no access out of bounds.
+ *
+ * Sizes are at least 1 (there are no calls without rows), E at most 1024, k 32, rows and tokens below 2^31 - 2^20, N and D 2^22,
+ * the dimension summed over 2^21: K, and in the gradients N as well, though the forward takes 2^22.  No output may overlap an input or
+ * another output (SK_ERR_ARG).  Pointers are aligned to their elements, and to 16 bytes (SK_ERR_ALIGN) where the call's text says so. */
 
 /* The k largest of each token's E logits (elem: bf16, fp16 or fp32; [T][E]), and the order of the pairs (token, choice)
  * by expert:
@@ -400,7 +404,7 @@ sk_status sk_moe_combine(const void* y, sk_elem elem, const int32_t* slots, cons
 
 /* Its gradients: dy[slots[t][j]] = weights[t][j] dout[t] [R][D], and dweights[t][j] = <dout[t], y[slots[t][j]]> (float
  * [T][k], or NULL; y is needed with it).  No two pairs may share a slot (sk_moe_route's do not).  Rows of dy without a
- * pair are zeros: with offsets (int32 [E+1]) they have to be those behind offsets[E]; with NULL any. */
+ * pair are zeros: with offsets (int32 [E+1]) they have to be those behind offsets[E]; with NULL any.  dy is 16-byte aligned. */
 sk_status sk_moe_combine_backward(const void* dout, const void* y, sk_elem elem, const int32_t* slots,
                                   const float* weights, const int32_t* offsets, void* dy, float* dweights, int64_t T,
                                   int64_t k, int64_t R, int64_t D, int64_t E, void* stream);
@@ -420,7 +424,7 @@ sk_status sk_gemm_grouped(const void* A, const void* B, sk_elem elem, const int3
  *                  rows behind offsets[E] become zeros
  *   dB [E][N][K]:  sum over the expert's rows of dC[r][n] A[rows[r]][k]  (zeros for an expert without rows)
  *   dbias [E][N]:  sum of its rows of dC
- * B is needed for dA, A for dB and for dbias.  N too is a multiple of 8, dC is 16-byte aligned. */
+ * B is needed for dA, A for dB and for dbias.  N too is a multiple of 8 and at most 2^21, dC is 16-byte aligned as A and B are. */
 sk_status sk_gemm_grouped_backward(const void* dC, const void* A, const void* B, sk_elem elem, const int32_t* offsets,
                                    const int32_t* rows, void* dA, void* dB, void* dbias, int64_t R, int64_t T, int64_t E,
                                    int64_t N, int64_t K, void* stream);
@@ -433,10 +437,12 @@ sk_status sk_gemm_grouped_backward(const void* dC, const void* A, const void* B,
  *     without zero points  scale = max|w| / 7,  code = 8 + w / scale
  *     with them            scale = (max(w, 0) - min(w, 0)) / 15,  zero = -min(w, 0) / scale,  code = zero + w / scale
  * quotients to nearest, ties to even, codes and zero points held to 0 .. 15.  A group that holds an infinity or a NaN, or
- * whose scale is beyond its type, has a NaN scale, and codes and a zero point of 0.  q is 16-byte aligned, the others to their elements. */
+ * whose scale is beyond its type, has a NaN scale, and codes and a zero point of 0.  The difference and the quotient of a scale are
+ * rounded to fp32 first (next to the border between two of its type's numbers it may so be the other one), the quotients with it
+ * are not.  q is 16-byte aligned. */
 sk_status sk_quantize_w4(const void* w, sk_elem elem, void* q, void* scale, sk_elem scale_elem, uint8_t* zero, int64_t E,
                          int64_t N, int64_t K, int64_t group, void* stream);
-/* out [E][N][K] of the scale's type = scale (code - zero). */
+/* out [E][N][K] of the scale's type = scale (code - zero).  q and out are 16-byte aligned. */
 sk_status sk_dequantize_w4(const void* q, const void* scale, sk_elem scale_elem, const uint8_t* zero, void* out,
                            int64_t E, int64_t N, int64_t K, int64_t group, void* stream);
 

@@ -1,7 +1,8 @@
 """A layer of experts: routing, products grouped by expert, and products with 4-bit weights.
 
 Every call runs in the library's HIP kernels (``include/sk_gemm.h`` has layouts and limits) and uses no scratch of the
-library, so all of them may be captured into a HIP graph.  Outputs are allocated on the stream that the call uses.
+library, so all of them may be captured into a HIP graph.  Outputs are allocated on the stream that the call uses.  Tensors
+are contiguous, and every size is at least 1: a call without rows or tokens raises.
 """
 
 from __future__ import annotations
@@ -235,7 +236,7 @@ def gemm_grouped(A, B, offsets, bias=None, *, rows=None, out=None, stream=None):
 
 def gemm_grouped_backward(dC, A, B, offsets, *, rows=None, need_dA=True, need_dB=True, need_dbias=True, stream=None):
     """Gradients of gemm_grouped: (dA, dB, dbias), None where not asked for.  dC is [R, N] of A's type (N, too, a
-    multiple of 8).  dA [R, K] has a row for each row of the product (zeros behind the last expert's): with rows,
+    multiple of 8, and at most 2^21).  dA [R, K] has a row for each row of the product (zeros behind the last expert's): with rows,
     moe_combine(dA, slots) adds a token's up.  dB [E, N, K] and dbias [E, N] are zeros for an expert without rows."""
     if stream is None:
         got = (_pg._NATIVE or _pg._native()).gemm_grouped_backward(dC, A, B, offsets, rows, need_dA, need_dB, need_dbias)
