@@ -279,8 +279,8 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t first, int n,
 }
 
 // Many tokens: their choices, and counts by expert of each workgroup's, part [workgroup][E].  (16384 x 256
-// fp32 logits, 8 chosen: 14.0 us.  What bounds it is the issue of some 350 vector instructions a token, half of them for the
-// eight maxima; the logits are 16.8 MB, 3.4 us.)
+// fp32 logits, 8 chosen: 16.5 us traced by itself; with the places 22.5 us as a call among others.  What bounds it is the issue of
+// some 350 vector instructions a token, half of them for the eight maxima; the logits are 16.8 MB, 2.8 us at 6.1 TB/s.)
 constexpr int kChooseThreads = 1024, kPlaceThreads = 1024, kFewThreads = 512;
 template <class T, int L, int V>
 __global__ __launch_bounds__(kChooseThreads) void sk_route_choose(RouteArgs a) {
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(kChooseThreads) void sk_route_choose(RouteArgs a) {
 }
 
 // The places of the pairs of kPlaceBlocks workgroups of the first kernel; rows behind the last expert's belong to no token.
-// (131072 pairs of 256 experts 9.6 us: the latency of the counts, of the scan and of the pairs' two readings one after the other.  Every
+// (131072 pairs of 256 experts 9.7 us traced: the latency of the counts, of the scan and of the pairs' two readings one after the other.  Every
 // workgroup adds up all counts itself, which takes less than a kernel between the two would.)
 __global__ __launch_bounds__(kPlaceThreads) void sk_route_place(RouteArgs a) {
   __shared__ PlaceShared<kPlaceThreads> sh;
@@ -337,8 +337,8 @@ __global__ __launch_bounds__(kFewThreads) void sk_route_few(RouteArgs a) {
 }
 
 // dlogits = w (d - sum w d) at the chosen experts, or p (d - sum w d) at all of them (d 0 where not chosen).
-// (Choice j is read by lane j.  16384 x 256 fp32, 8 chosen: 8.1 us, of which 18 MB of traffic are 3.7; with the choices handed round the
-// wave and compared with each lane's experts 10.5.)
+// (Choice j is read by lane j.  16384 x 256 fp32, 8 chosen, over the chosen 5.2 us and over all 7.6, of which 18 and 35 MB of traffic
+// are 3.0 and 5.8; with the choices handed round the wave and compared with each lane's experts a third more.)
 template <class T, int L, int V>
 __global__ __launch_bounds__(256) void sk_route_gradient(RouteGradArgs a) {
   constexpr int PER = 256 / L, KEPT = (kMaxChoices + L - 1) / L;
@@ -410,7 +410,7 @@ __global__ __launch_bounds__(256) void sk_route_gradient(RouteGradArgs a) {
 // ---------------------------------------------------------------- the weighted sum
 
 // out[t] = sum_j w[t][j] y[slots[t][j]], eight columns to a thread, fp32 sums in the order of j.
-// (8192 x 2 x 4096 bf16 36.5 us, 5.5 TB/s: bound by memory.)
+// (8192 x 2 x 4096 bf16 39.5 us from memory, 5.1 TB/s, which bounds it; 30 us where y is in the last-level cache.)
 template <class T, bool SHORT>
 __global__ __launch_bounds__(256) void sk_combine(CombineArgs a) {
   const int per_row = (a.D + 7) / 8;
@@ -431,7 +431,7 @@ __global__ __launch_bounds__(256) void sk_combine(CombineArgs a) {
 }
 
 // A wave to a pair: dy[slot] = w dout[t] and dweights = <dout[t], y[slot]>.  Rows behind the last expert's are zeros.
-// (1037 x 4 x 2051 bf16 8.3 us, of which 38 MB of traffic are 7.5.)
+// (1037 x 4 x 2051 bf16 9.4 us, of which 38 MB of traffic are 6.2.)
 template <class T, bool SHORT>
 __global__ __launch_bounds__(256) void sk_combine_gradient(CombineGradArgs a) {
   const int lane = threadIdx.x & 63;
@@ -499,12 +499,12 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Tokens that one workgroup chooses for and places: two turns of its lanes.  (64 of 64 experts 6.0 us and 65 as two kernels 7.8, 32 and 33
-// of 128 6.6 / 7.9, 16 and 17 of 256 6.1 / 7.8.)
+// Tokens that one workgroup chooses for and places: two turns of its lanes.  (64 of 64 experts 6.0 us and as two kernels 8.0, 32 of 128
+// 6.6 / 7.9, 16 of 256 6.3 / 8.0.)
 int64_t few_tokens(int E) { return E <= 64 ? kFewTokens : E <= 128 ? kFewTokens / 2 : kFewTokens / 4; }
 // Tokens of a workgroup of the first kernel: no more than its waves take at once, and more where there would be over 256 workgroups,
-// whose counts are all read by half as many.  (1024 tokens of 256 experts, both kernels, 11.4 us with 16 and 21.4 with 64; of 8
-// 8.8 / 8.1.)
+// whose counts are all read by half as many.  (1024 tokens of 256 experts, both kernels, 10.1 us with 16 and 17.9 with 64; of 8
+// 8.2 / 8.1.)
 int route_per_block(int64_t T, int E) {
   const int least = E <= 32 ? 64 : 16;
   return (int)(cdiv64(cdiv64(T, 256), least) * least);
@@ -513,7 +513,7 @@ int route_per_block(int64_t T, int E) {
 int64_t route_blocks(int64_t T, int E) { return T <= few_tokens(E) ? 0 : cdiv64(T, route_per_block(T, E)); }
 
 hipError_t launch_route(RouteArgs a, int elem, hipStream_t s) {
-  // one workgroup for few tokens: 1 token of 64 experts 4.2 us on the device against 7.0 as two kernels
+  // one workgroup for few tokens: 1 token of 64 experts 5.2 us against 8.0 as two kernels
   if (a.T <= few_tokens(a.E))
     return by_elem(elem, [&](auto t) {
       return by_experts(a.E, [&](auto l, auto v) {

@@ -299,7 +299,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
   }
   // (gather, dB) where the wave's TOK rows of each of AHEAD k-steps begin, one in each lane, out of range where there is no row.  The
   // rows' indexes are asked for AHEAD k-steps before, since the wait for them is also one for all direct loads before it.  (Asked for in
-  // every k-step, as scalars, they made all waits for LDS reads wait for them: 8002 rows of 8 experts, 2048 x 4096, 170 us and not 145.)
+  // every k-step, as scalars, they made all waits for LDS reads wait for them: 8002 rows of 8 experts, 2048 x 4096, 17 % longer.)
   constexpr int TOK = C::KIND == kGradB && C::GATHER ? C::Q_PT * OpQ::RPU : 1, AHEAD = 64 / TOK;
   uint32_t held = 0;
   int asked = 0;
@@ -417,7 +417,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedGemm& g, const Grouped
   };
   // The reads beside a half's products are begun in its first three quarters, so that they are there at its end.  The direct
   // loads go behind the products of its first half with 8 waves (spread over all of it, 4148 rows of 16 experts, 2051 x
-  // 1288, took 48.5 us and not 46, in the second half 51), and are spread over all of it with 4.
+  // 1288, took 5 % longer, in the second half 11 %), and are spread over all of it with 4.
   constexpr int NS = C::FM * C::FN, NR = C::FM + C::FN, NB = NS >= 8 ? NS * 3 / 4 : NS;
   constexpr auto place_of = [](int l, int n) { return C::NW == 8 ? 1 + l * NS / n / 2 : l * NS / n; };      // behind which product load l of n goes
   using std::integral_constant;
@@ -564,7 +564,7 @@ __global__ __launch_bounds__(C::NT, C::NW / 4 * (C::LDS > 80 * 1024 ? 1 : 2)) vo
   if constexpr (C::KIND == kGradB) {
     // The experts in turn, and of each one's tiles (columns of them in turn) a run to each XCD.  (With a run of all experts' tiles
     // to each XCD, which leaves it with the experts that have the most rows, 8 experts of 500 to 1600 rows, 4096 x 2048, took
-    // 178 us and not 139.  The experts with the most rows first: no change.)
+    // 28 % longer.  The experts with the most rows first: no change.)
     const int per_e = g.tiles_m * g.tiles_n, t = (int)blockIdx.x % per_e;
     p.e = (int)blockIdx.x / per_e;
     const int x = t & 7, i = x * (per_e >> 3) + min(x, per_e & 7) + (t >> 3), tn = i / g.tiles_m;
@@ -626,31 +626,31 @@ hipError_t launch_grouped_tiles(GroupedGemm g, int cus, hipStream_t s) {
 template <class T, int KIND, bool GATHER>
 hipError_t launch_grouped_kind(const GroupedGemm& g, int cus, hipStream_t s) {
   // 8 waves, two to a SIMD, so that one's products hide the other's loads and reads: 4 waves of 128 x 128 each, which read a
-  // third less from LDS, took 164 us and not 159 for 4096 rows of 8 experts, 4096 x 4096, and their dB with gathered rows 232 and not 206.
+  // third less from LDS, took 3 % longer for 4096 rows of 8 experts, 4096 x 4096, and 13 % for their dB with gathered rows.
   using Big = GroupedCfg<T, KIND, GATHER, 256, 256, 2, 4, 5>;
   using Half = GroupedCfg<T, KIND, GATHER, 256, 128, 2, 4, 5>;
   using Quarter = GroupedCfg<T, KIND, GATHER, 128, 128, 2, 4, 5>;
   using Small = GroupedCfg<T, KIND, GATHER, 128, 128, 2, 2, 5>;
   if constexpr (KIND == kGradB) {
-    // Smaller tiles read dC and A more often (8 experts of 2048 x 4096, 8002 rows 138 us against 171 of 128 x 128), but are more where the
-    // large ones leave half of the units idle: 4 experts of 1024 x 1024, 400 rows 8.9 / 6.0 and 1600 rows 16.5 / 10.2; of 2048 x
-    // 2048, 800 rows 17.0 / 18.1.
+    // (Here and below calls among others, with operands from memory.)  Smaller tiles read dC and A more often (8 experts of 2048 x 4096,
+    // 8002 rows 128 us against 162 of 128 x 128), but are more where the large ones leave half of the units idle: 4 experts of
+    // 1024 x 1024, 400 rows 8.7 / 6.3 and 1600 rows 14.8 / 10.2; of 2048 x 2048, 800 rows 15.7 / 17.4.
     if (g.E * (int64_t)cdiv(g.Mout, 256) * cdiv(g.Nout, 256) * 2 > cus) return launch_grouped_tiles<Big, Big, Big>(g, cus, s);
   } else {
     // about how many tiles there are with `rows` rows
     auto tiles = [&](int rows, int cols) { return ((int64_t)g.R / rows + g.E / 2) * cdiv(g.Nout, cols); };
     // Tiles of 256 x 256 where experts have 128 rows or more on the average and there are tiles for half of the units: 4096 x
-    // 4096, 8 experts, 1024 rows 74 us against 84 of 128 x 128 and 512 rows 71 / 66; dA 65 / 83 and 61 / 58; 64 experts of 512 x
-    // 1024 with 125 rows each 29 / 21.
+    // 4096, 8 experts, 4096 rows 113 us against 157 of 128 x 128, 2048 rows 84 / 91, 1024 rows 72 / 68, 512 rows 67 / 65; dA of
+    // 2048 rows 75 / 89, 1024 rows 65 / 58; 64 experts of 512 x 1024 with 125 rows each 23.4 / 21.2.
     if ((int64_t)g.R >= 128 * (int64_t)g.E && tiles(256, 256) * 2 >= cus) return launch_grouped_tiles<Big, Half, Quarter>(g, cus, s);
-    // Tiles of 32 x 128, in which most rows are there, for up to 24 rows of an expert: 8 experts of 4096 x 4096, 8 rows 38 us
-    // against 56 with 128 x 128, 256 rows 69 / 66, 512 rows 84 / 66; 64 experts of 2048 x 1024 with 28 rows each 68 / 59.  And where
-    // all of them run at once, since a k-step of one takes half the time: 4 experts of 1024 x 1024, 800 rows 8.3 us against 13.1,
-    // 1600 rows 14.9 / 13.7.
+    // Tiles of 32 x 128, in which most rows are there, for up to 24 rows of an expert: 8 experts of 4096 x 4096, 8 rows 59.9 us
+    // against 62.6 with 128 x 128 (the weights alone take 44 to 55), 512 rows 65.3 / 64.8, 1024 rows 115 / 68; 64 experts of 2048 x 1024 with
+    // 28 rows each 61.9 / 56.0.  And where all of them run at once, since a k-step of one takes half the time: 4 experts of 1024 x
+    // 1024, 800 rows 9.3 us against 16.1, 1600 rows 17.1 / 16.2.
     using Few = GroupedCfg<T, KIND, GATHER, 32, 128, 1, 4, 8>;
     if ((int64_t)g.R <= 24 * (int64_t)g.E || tiles(32, 128) <= cus) return launch_grouped_tiles<Few, Few, Few>(g, cus, s);
-    // Of 64 x 128 by the same rule: 4 experts of 1024 x 1024, 1600 rows 10.6 us against 13.8 with 128 x 128, of 2048 x 2048, 800 rows
-    // 16.3 / 21.6 and 1200 rows 28.0 / 22.3.
+    // Of 64 x 128 by the same rule: 4 experts of 1024 x 1024, 1600 rows 10.7 us against 16.2 with 128 x 128, of 2048 x 2048, 800 rows
+    // 18.0 / 28.5 and 1200 rows 33.4 / 28.6.
     using Mid = GroupedCfg<T, KIND, GATHER, 64, 128, 2, 2, 8>;
     if (tiles(64, 128) <= cus) return launch_grouped_tiles<Mid, Mid, Mid>(g, cus, s);
   }

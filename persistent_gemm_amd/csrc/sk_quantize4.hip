@@ -5,8 +5,10 @@
 //   with them             s = (hi - lo) / 15,          z = -lo / s,  q = z + w / s,   hi = max(w, 0), lo = min(w, 0)
 //
 // each quotient to nearest, ties to even, codes and zero points held to 0 .. 15.  s is rounded to its type (and at least its
-// smallest normal number) before it divides.  A group with an infinity or a NaN, or whose scale is beyond its type, has a NaN
-// scale, and codes and a zero point of 0.
+// smallest normal number) before it divides; the difference hi - lo and the quotient are fp32's before that, so that next to the border
+// between two of its type's numbers s may be the other one (about one group in 10^5 of an fp32 weight; the codes fit the s that is
+// stored all the same).  A group with an infinity or a NaN, or whose scale is beyond its type, has a NaN scale, and codes and a zero point
+// of 0.
 
 #include "sk_experts.h"
 
@@ -30,8 +32,8 @@ __device__ __forceinline__ float nearest(float w, float s, float r) {
 }
 
 // 8 elements to a thread, G / 8 threads to a group, a wave to 512 consecutive elements of a row; a workgroup takes those of ROWS rows, a
-// quarter to each wave, and stores their scales, which lie row by row, in stretches.  Bound by memory: 8192 x 8192 bf16 35 us (4.8 TB/s; 65
-// with a division for each element and 256 bytes of a row at a time).
+// quarter to each wave, and stores their scales, which lie row by row, in stretches.  Bound by memory: 8192 x 8192 bf16 37.5 us from
+// memory (4.5 TB/s; with a division for each element and 256 bytes of a row at a time nearly twice that).
 template <class T, class S, int G, bool ZERO, int ROWS>
 __global__ __launch_bounds__(256) void sk_quantize4(Quant4Args a) {
   constexpr int L = G / 8, PER = 512 / G;        // lanes of a group; groups of a wave's stretch

@@ -313,20 +313,22 @@ hipError_t launch_rows_of(const RowsGemm& g, int cus, hipStream_t s) {
   constexpr int MORE = GROUP == 32 ? 1 : 2;     // (the scales of 32 rows of groups of 32 do not fit the registers)
   if (g.offsets && per <= 8) {
     // Four waves to a workgroup: an expert's few rows are soon done, and several workgroups to a unit share what begins and ends
-    // them (16 tokens x 2 of 8, 4096 x 4096, groups of 64 with zero points: 28.6 us against 30.7 with 8 waves and 40.7 with 16).
+    // them (16 tokens x 2 of 8, 4096 x 4096, groups of 64 with zero points: 25.5 us against 28.1 with 8 waves and 40.1 with 16; here
+    // and below calls among others, with weights from memory).
     if (!wide) return launch_rows_as<T, GROUP, ZERO, false, 1, 1, 4>(g, s);
     return launch_rows_as<T, GROUP, ZERO, true, MORE, 1, 4>(g, s);
   }
   if (!g.offsets && per <= 4) {
-    // 1x8192x8192 10.3 us against 13.0 with 4 waves and 15.2 with 16
+    // 1x8192x8192 11.0 us against 12.4 with 4 waves and 12.2 with 16
     if (!wide) return launch_rows_as<T, GROUP, ZERO, false, 1, 1, 8>(g, s);
-    // 32 rows of W to a workgroup where half as many still fill the device (8192: 10.3 us against 11.8; 4096: 6.2 / 4.8)
+    // 32 rows of W to a workgroup where half as many still fill the device (16384x8192 19.2 us against 22.7 with 16, 8192x8192 11.0 / 11.2,
+    // 4096x4096 6.1 / 5.1)
     if (MORE > 1 && cdiv(g.N, 32) >= cus) return launch_rows_as<T, GROUP, ZERO, true, MORE, 1, 8>(g, s);
     return launch_rows_as<T, GROUP, ZERO, true, 1, 1, 8>(g, s);
   }
   if (!g.offsets && per <= 32) {
-    // Every workgroup reads all of x: more waves to it (16x8192x8192 16.2 us against 25.6 with 8).  Up to 32 rows as two workgroups of
-    // 16 (32x8192x8192 30.5 us against 39.6 with 32 at a time; 64 rows 62 / 42).
+    // Every workgroup reads all of x: more waves to it (16x8192x8192 18.3 us against 22.1 with 8; 5 rows 13.1 / 13.4, but 32 rows 31.9 /
+    // 28.7).  Up to 32 rows as two workgroups of 16 (32x8192x8192 31.9 us against 42.0 with 32 at a time; 64 rows 59.6 / 42.0).
     if (!wide) return launch_rows_as<T, GROUP, ZERO, false, 1, 1, 16>(g, s);
     return launch_rows_as<T, GROUP, ZERO, true, MORE, 1, 16>(g, s);
   }
